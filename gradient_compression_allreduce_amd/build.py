@@ -6,7 +6,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 SO = os.path.join(LIBDIR, "libgq.so")
-SOURCES = ["gq_abi.cpp", "gq_chunker.cpp", "gq_kernels.hip", "gq_check.hip", "gq_noalloc.hip"]
+SOURCES = ["gq_abi.cpp", "gq_chunker.cpp", "gq_kernels.hip", "gq_check.hip", "gq_noalloc.hip",
+           "gq_mx4.cpp", "gq_mx4.hip", "gq_mx4_product.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -31,7 +32,7 @@ def build(verbose=False):
     os.makedirs(LIBDIR, exist_ok=True)
     objs, procs = [], []
     for src in SOURCES:   # the sources compile in parallel
-        obj = os.path.join(LIBDIR, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(LIBDIR, src + ".o")
         cmd = [hipcc(), *HIPCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cpp"):
             cmd[1:1] = ["-x", "hip"]

@@ -1,0 +1,193 @@
+// gq_mx4_product.hip -- C = A B^T, or C += A B^T, of two MX4 matrices on the
+// scaled 4-bit matrix instructions of gfx950 (gq_mm.h: the tile loop; the
+// product of two blocks takes their two scale bytes as operands, so nothing
+// is decoded).  Sums are binary32.
+//   k_mx4_product  a tile of C; or, where C has too few tiles to fill the
+//                  device, the tile's share of K into a partial C of its own;
+//   k_mx4_join     adds the partial sums in the order of K.
+#include <hip/hip_fp16.h>
+
+#include "gq_mm.h"
+#include "gq_mx4.h"
+#include "gq_mx4_product.h"
+
+namespace gq {
+namespace {
+
+using Big = MmShape<256, 256, 2, 4>;
+using Mid = MmShape<128, 128, 2, 2>;
+using Small = MmShape<64, 64, 2, 2>;
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+    const uint32_t u = __float_as_uint(v);
+    if ((u & 0x7fffffffu) > kInfBits) return static_cast<uint16_t>((u >> 16) | 0x40u);
+    return static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+}
+
+__device__ __forceinline__ uint16_t f16_bits(float v) {
+    return __half_as_ushort(__float2half_rn(v));
+}
+
+// Four consecutive columns of a row of C, `n` of them inside.
+template <gq_dtype DT>
+__device__ __forceinline__ void store4(void *c, int64_t at, mm_f32x4 v, int n, bool vec,
+                                       bool add) {
+    if constexpr (DT == GQ_F32) {
+        float *p = static_cast<float *>(c) + at;
+        if (n >= 4 && vec) {
+            mm_f32x4 *q = reinterpret_cast<mm_f32x4 *>(p);
+            if (add) {
+                const mm_f32x4 o = *q;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = __fadd_rn(o[k], v[k]);
+            }
+            *q = v;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < n) p[k] = add ? __fadd_rn(p[k], v[k]) : v[k];
+        }
+    } else {
+        uint16_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = DT == GQ_F16 ? f16_bits(v[k]) : bf16_bits(v[k]);
+        uint16_t *p = static_cast<uint16_t *>(c) + at;
+        if (n >= 4 && vec) {
+            *reinterpret_cast<uint2 *>(p) =
+                make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16),
+                           h[2] | (static_cast<uint32_t>(h[3]) << 16));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < n) p[k] = h[k];
+        }
+    }
+}
+
+template <typename S, gq_dtype DT>
+__global__ __launch_bounds__(S::THREADS) void k_mx4_product(const MxPArgs a) {
+    __shared__ __align__(128) char s0[S::STAGE_MX];
+    __shared__ __align__(128) char s1[S::STAGE_MX];
+    const int tm = static_cast<int>((a.m + S::BM - 1) / S::BM);
+    const int tn = static_cast<int>((a.n + S::BN - 1) / S::BN);
+    int t = mm_xcd(blockIdx.x, gridDim.x);
+    const int split = t / (tm * tn);
+    int ti, tj;
+    mm_tile(t - split * tm * tn, tm, tn, ti, tj);
+    const int64_t i0 = static_cast<int64_t>(ti) * S::BM, j0 = static_cast<int64_t>(tj) * S::BN;
+    const uint32_t bytes = static_cast<uint32_t>(a.nb) * MX_BYTES;
+    const MmRows p = mm_rows(a.a, bytes, i0, a.m, S::BM);
+    const MmRows q = mm_rows(a.b, bytes, j0, a.n, S::BN);
+    MmScale sc = {nullptr, a.nb};
+    {
+        const int r = threadIdx.x;
+        if (r < S::BM) {
+            if (i0 + r < a.m) sc.p = a.sa + (i0 + r) * a.nb;
+        } else if (r < S::BM + S::BN && j0 + r - S::BM < a.n) {
+            sc.p = a.sb + (j0 + r - S::BM) * a.nb;
+        }
+    }
+    mm_f32x4 acc[S::FM][S::FN] = {};
+    const int pairs_all = static_cast<int>((a.nb + 15) / 16);
+    const int k0 = split * a.pairs;
+    const int pairs = pairs_all - k0 < a.pairs ? pairs_all - k0 : a.pairs;
+    mm_loop<S, true>(p, q, sc, 2 * k0, pairs, s0, s1, acc);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t r0 = i0 + wave / S::WN * (S::BM / S::WM) + (lane & 15);
+    const int64_t c0 = j0 + wave % S::WN * (S::BN / S::WN) + (lane >> 4) * 4;
+    void *c = a.c;
+    int64_t ldc = a.ldc;
+    bool vec = a.vec != 0, add = a.add != 0;
+    if (a.splits > 1) {
+        c = a.part + split * a.m * a.n;
+        ldc = a.n;
+        vec = a.n % 4 == 0;
+        add = false;
+    }
+#pragma unroll
+    for (int i = 0; i < S::FM; ++i) {
+        const int64_t r = r0 + 16 * i;
+        if (r >= a.m) continue;
+#pragma unroll
+        for (int j = 0; j < S::FN; ++j) {
+            const int64_t col = c0 + 16 * j;
+            const int left = a.n - col < 4 ? static_cast<int>(a.n - col) : 4;
+            if (left <= 0) continue;
+            if (DT != GQ_F32 && a.splits > 1)
+                store4<GQ_F32>(c, r * ldc + col, acc[i][j], left, vec, false);
+            else
+                store4<DT>(c, r * ldc + col, acc[i][j], left, vec, add);
+        }
+    }
+}
+
+template <gq_dtype DT>
+__global__ __launch_bounds__(256) void k_mx4_join(const MxPArgs a) {
+    const int64_t total = a.m * a.n;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < total;
+         e += static_cast<int64_t>(gridDim.x) * 256) {
+        float v = a.part[e];
+        for (int s = 1; s < a.splits; ++s) v = __fadd_rn(v, a.part[s * total + e]);
+        const int64_t row = e / a.n, at = row * a.ldc + (e - row * a.n);
+        if constexpr (DT == GQ_F32) {
+            float *c = static_cast<float *>(a.c) + at;
+            *c = a.add ? __fadd_rn(*c, v) : v;
+        } else {
+            static_cast<uint16_t *>(a.c)[at] = DT == GQ_F16 ? f16_bits(v) : bf16_bits(v);
+        }
+    }
+}
+
+int64_t tiles(const MxPArgs &a, int t) { return (a.m + t - 1) / t * ((a.n + t - 1) / t); }
+
+template <typename S>
+hipError_t product_shape(const MxPArgs &a, gq_dtype dt, hipStream_t st) {
+    const dim3 grid(static_cast<unsigned>(tiles(a, S::BM) * a.splits));
+    const dim3 blk(S::THREADS);
+    if (dt == GQ_F32) hipLaunchKernelGGL((k_mx4_product<S, GQ_F32>), grid, blk, 0, st, a);
+    else if (dt == GQ_F16) hipLaunchKernelGGL((k_mx4_product<S, GQ_F16>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((k_mx4_product<S, GQ_BF16>), grid, blk, 0, st, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t want = (a.m * a.n + 255) / 256;
+    const dim3 jg(static_cast<unsigned>(want < 4096 ? want : 4096));
+    if (dt == GQ_F32) hipLaunchKernelGGL(k_mx4_join<GQ_F32>, jg, dim3(256), 0, st, a);
+    else if (dt == GQ_F16) hipLaunchKernelGGL(k_mx4_join<GQ_F16>, jg, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(k_mx4_join<GQ_BF16>, jg, dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// The tile and the number of parts of K for an m x n x k product: the
+// largest tile that gives every compute unit one, and where even the
+// smallest gives too few, K in as many parts (of at least four K steps
+// each) as fill them.
+MxPlan mx4_product_plan(int64_t m, int64_t n, int64_t k) {
+    MxPArgs a{};
+    a.m = m;
+    a.n = n;
+    const int64_t pairs = ((k + MX_BLOCK - 1) / MX_BLOCK + 15) / 16;
+    MxPlan p{};
+    p.tile = tiles(a, 256) >= MX_CUS ? 256 : tiles(a, 128) >= MX_CUS ? 128 : 64;
+    const int64_t t = tiles(a, p.tile);
+    int64_t splits = t >= MX_CUS ? 1 : MX_CUS / t;
+    if (splits > pairs / 2) splits = pairs / 2;
+    if (splits < 1) splits = 1;
+    const int64_t per = (pairs + splits - 1) / splits;
+    p.pairs = static_cast<int32_t>(per);
+    p.splits = static_cast<int32_t>((pairs + per - 1) / per);
+    return p;
+}
+
+hipError_t launch_mx4_product(const MxPArgs &in, int64_t k, gq_dtype dt, hipStream_t st) {
+    MxPArgs a = in;
+    const MxPlan p = mx4_product_plan(a.m, a.n, k);
+    a.splits = a.part ? p.splits : 1;
+    a.pairs = a.splits > 1 ? p.pairs : static_cast<int32_t>((a.nb + 15) / 16);
+    if (p.tile == 256) return product_shape<Big>(a, dt, st);
+    if (p.tile == 128) return product_shape<Mid>(a, dt, st);
+    return product_shape<Small>(a, dt, st);
+}
+
+}  // namespace gq

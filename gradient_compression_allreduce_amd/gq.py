@@ -18,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SO = os.path.join(HERE, "_lib", "libgq.so")
 
 GQ_OK, GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_CAPACITY, GQ_ERR_HIP, GQ_ERR_DEVICE = range(6)
-GQ_F32, GQ_F16 = 0, 1
+GQ_F32, GQ_F16, GQ_BF16 = 0, 1, 2
 GQ_SCHED_LAYER, GQ_SCHED_CHUNK = 0, 1
 GQ_PIPE_OVERLAP, GQ_PIPE_SERIAL = 0, 1
 GQ_FORM_PERSISTENT, GQ_FORM_TWO_PASS, GQ_FORM_SHORT_UNITS = 0, 1, 2
@@ -35,7 +35,9 @@ EXPORTS = ("gq_last_error", "gq_version", "gq_plan_chunks", "gq_units_create",
            "gq_reduce_dequant", "gq_requantize", "gq_reduce_requantize",
            "gq_sum_f32", "gq_error_report", "gq_pipe_create", "gq_pipe_destroy",
            "gq_pipe_slots", "gq_pipe_schedule", "gq_pipe_faults", "gq_pipe_clear_faults", "gq_pipe_step", "gq_chunker_create",
-           "gq_chunker_destroy", "gq_chunker_update", "gq_chunker_predict", "gq_chunker_plan")
+           "gq_chunker_destroy", "gq_chunker_update", "gq_chunker_predict", "gq_chunker_plan",
+           "gq_mx4_sizes", "gq_mx4_quantize", "gq_mx4_reduce_dequant", "gq_mx4_reduce_requantize",
+           "gq_mx4_product_workspace", "gq_mx4_product")
 GQ_STATS = 10
 STATS = ("max_abs_err", "max_abs_ref", "max_rel_err", "sum_abs_err", "sum_abs_ref",
          "mean_rel_err", "sum_dd", "sum_rr", "sum_dr", "cos")
@@ -123,6 +125,18 @@ def _load():
     L.gq_sum_f32.argtypes = [vp, i32, i32, f32, i64, i32, vp, vp]
     L.gq_error_report.restype = st
     L.gq_error_report.argtypes = [vp, vp, vp, vp, vp, vp]
+    L.gq_mx4_sizes.restype = st
+    L.gq_mx4_sizes.argtypes = [i64, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)]
+    L.gq_mx4_quantize.restype = st
+    L.gq_mx4_quantize.argtypes = [vp, i32, i32, f32, i64, i64, i64, i32, vp, vp, vp]
+    L.gq_mx4_reduce_dequant.restype = st
+    L.gq_mx4_reduce_dequant.argtypes = [vp, vp, i32, i64, i64, vp, vp]
+    L.gq_mx4_reduce_requantize.restype = st
+    L.gq_mx4_reduce_requantize.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp, vp]
+    L.gq_mx4_product_workspace.restype = st
+    L.gq_mx4_product_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    L.gq_mx4_product.restype = st
+    L.gq_mx4_product.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, i64, vp, i64, vp]
     return L
 
 
@@ -260,6 +274,8 @@ def _dt():
         _TORCH["bits"] = (torch.int32, torch.uint32)
         _TORCH["i64"] = (torch.int64,)
         _TORCH["f64"] = (torch.float64,)
+        _TORCH["u8"] = (torch.uint8,)
+        _TORCH["code"] = {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16}
     return _TORCH
 
 
@@ -686,3 +702,138 @@ def gq_chunker_plan(chunker, numel, elem_bytes):
     _check(lib.gq_chunker_plan(chunker.handle, numel, elem_bytes, off.ctypes.data, off.size,
                                ctypes.byref(cnt)))
     return off
+
+
+def _matrix(name, t, dtypes, dev):
+    """(rows, cols, row stride) of a tensor on device `dev` that is a vector
+    (one row) or a matrix whose rows are contiguous."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError("%s must be a tensor on the HIP device" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be of dtype %s, got %s"
+                        % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s is on device %d, the current device is %d"
+                         % (name, t.get_device(), dev))
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 1:
+        rows, cols, ld, step = 1, shape[0], shape[0], stride[0]
+    elif len(shape) == 2:
+        rows, cols = shape
+        ld, step = (stride[0] if rows > 1 else cols), stride[1]
+    else:
+        raise ValueError("%s must be a vector or a matrix, has %d dimensions" % (name, len(shape)))
+    if rows < 1 or cols < 1:
+        raise ValueError("%s is empty" % name)
+    if cols > 1 and step != 1:
+        raise ValueError("%s: the elements of a row must be contiguous" % name)
+    if rows > 1 and ld < cols:
+        raise ValueError("%s: rows overlap (row stride %d, %d columns)" % (name, ld, cols))
+    return rows, cols, ld
+
+
+MX4_BLOCK = 32
+
+
+def gq_mx4_sizes(rows, cols):
+    """(scale bytes, code bytes) of a rows x cols matrix in 4 bits."""
+    n, b = ctypes.c_int64(0), ctypes.c_int64(0)
+    _check(lib.gq_mx4_sizes(rows, cols, ctypes.byref(n), ctypes.byref(b)))
+    return n.value, b.value
+
+
+def gq_mx4_quantize(xs, scales, codes, in_mul=1.0, transpose=False, stream=None):
+    """Scales and codes (uint8, sizes from gq_mx4_sizes) of W gradients or
+    matrices xs (float32, float16 or bfloat16, all of one shape and row
+    stride): blocks of 32 along the rows, or with transpose down the columns
+    (the codes of the transposed matrix)."""
+    dev = _current_device()
+    T = _dt()
+    W = _ranks("xs", xs)
+    dt = getattr(xs[0], "dtype", None)
+    if dt not in T["code"]:
+        raise TypeError("elements must be float32, float16 or bfloat16, got %s" % dt)
+    rows, cols, ld = geo = _matrix("xs[0]", xs[0], (dt,), dev)
+    for i in range(1, W):
+        if _matrix("xs[%d]" % i, xs[i], (dt,), dev) != geo:
+            raise ValueError("xs[%d] differs from xs[0] in shape or row stride" % i)
+    r, c = (cols, rows) if transpose else (rows, cols)
+    nb = r * (-(-c // MX4_BLOCK))
+    _need_list("scales", scales, W, nb, T["u8"], dev)
+    _need_list("codes", codes, W, 16 * nb, T["u8"], dev)
+    px, k1 = _ptrs(xs)
+    ps, k2 = _ptrs(scales)
+    pq, k3 = _ptrs(codes)
+    _check(lib.gq_mx4_quantize(px, W, T["code"][dt], in_mul, rows, cols, ld,
+                               1 if transpose else 0, ps, pq, _stream(stream)))
+
+
+def _mx4_inputs(codes, scales, rows, cols, dev):
+    rows, cols = int(rows), int(cols)
+    if rows < 1 or cols < 1:
+        raise ValueError("rows and cols must be >= 1, got %d and %d" % (rows, cols))
+    T = _dt()
+    W = _ranks("codes", codes)
+    nb = rows * (-(-cols // MX4_BLOCK))
+    _need_list("codes", codes, W, 16 * nb, T["u8"], dev)
+    _need_list("scales", scales, W, nb, T["u8"], dev)
+    return W, nb
+
+
+def gq_mx4_reduce_dequant(codes, scales, rows, cols, r_out, stream=None):
+    """Rank-order fp32 sum of W ranks' codes of a rows x cols matrix (one
+    rank: its values)."""
+    dev = _current_device()
+    W, _ = _mx4_inputs(codes, scales, rows, cols, dev)
+    _need("r_out", r_out, rows * cols, _dt()["f32"], dev)
+    pq, k1 = _ptrs(codes)
+    ps, k2 = _ptrs(scales)
+    _check(lib.gq_mx4_reduce_dequant(pq, ps, W, rows, cols, r_out.data_ptr(), _stream(stream)))
+
+
+def gq_mx4_reduce_requantize(codes, scales, rows, cols, scale_out, q_out, r_out=None, stream=None):
+    """The same sum, quantized again into scale_out and q_out; r_out: also
+    the sum."""
+    dev = _current_device()
+    T = _dt()
+    W, nb = _mx4_inputs(codes, scales, rows, cols, dev)
+    _need("scale_out", scale_out, nb, T["u8"], dev)
+    _need("q_out", q_out, 16 * nb, T["u8"], dev)
+    if r_out is not None:
+        _need("r_out", r_out, rows * cols, T["f32"], dev)
+    pq, k1 = _ptrs(codes)
+    ps, k2 = _ptrs(scales)
+    rp = r_out.data_ptr() if r_out is not None else None
+    _check(lib.gq_mx4_reduce_requantize(pq, ps, W, rows, cols, rp, scale_out.data_ptr(),
+                                        q_out.data_ptr(), _stream(stream)))
+
+
+def gq_mx4_product_workspace(m, n, k):
+    """Bytes of workspace with which gq_mx4_product splits k (0: it does not)."""
+    v = ctypes.c_int64(0)
+    _check(lib.gq_mx4_product_workspace(m, n, k, ctypes.byref(v)))
+    return v.value
+
+
+def gq_mx4_product(a, a_scale, b, b_scale, k, out, accumulate=False, workspace=None, stream=None):
+    """out (m x n; float32, float16 or bfloat16) = A B^T from the codes and
+    scales of an m x k and an n x k matrix; accumulate (float32): out += it.
+    workspace: None, or a uint8 tensor of gq_mx4_product_workspace bytes."""
+    dev = _current_device()
+    T = _dt()
+    m, n, ldc = _matrix("out", out, T["code"], dev)
+    k = int(k)
+    if k < 1:
+        raise ValueError("k must be >= 1, got %d" % k)
+    nb = -(-k // MX4_BLOCK)
+    _need("a", a, 16 * m * nb, T["u8"], dev)
+    _need("a_scale", a_scale, m * nb, T["u8"], dev)
+    _need("b", b, 16 * n * nb, T["u8"], dev)
+    _need("b_scale", b_scale, n * nb, T["u8"], dev)
+    wp, wn = None, 0
+    if workspace is not None:
+        _need("workspace", workspace, 0, T["u8"], dev)
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    _check(lib.gq_mx4_product(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+                              m, n, k, T["code"][out.dtype], 1 if accumulate else 0,
+                              out.data_ptr(), ldc, wp, wn, _stream(stream)))

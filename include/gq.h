@@ -79,7 +79,8 @@ typedef enum {
 
 typedef enum {
     GQ_F32 = 0, /* IEEE binary32 gradient elements */
-    GQ_F16 = 1  /* IEEE binary16 gradient elements (loss-scaled, see in_mul) */
+    GQ_F16 = 1, /* IEEE binary16 gradient elements (loss-scaled, see in_mul) */
+    GQ_BF16 = 2 /* bfloat16 elements: gq_mx4_* and gq_ortho_* only */
 } gq_dtype;
 
 /* Largest number of simulated ranks a call accepts. */
@@ -563,6 +564,93 @@ gq_status gq_sum_f32(const void *const *x, int32_t W, gq_dtype dt, float in_mul,
 #define GQ_STATS 10
 gq_status gq_error_report(const int8_t *q, const float *scale, const float *ref,
                           const gq_units *u, double *stats_out, gq_stream stream);
+
+/* ---- Microscaled 4-bit gradients -----------------------------------------
+ * A second wire format beside int8 codes: 4.25 bits per element.  A matrix of
+ * rows x cols elements (a flat gradient is one row) is cut along its rows
+ * into blocks of 32 elements, a row's last block holding what is left.  A
+ * block is a scale byte s, standing for 2^(s - 127) (255: NaN), and 16 code
+ * bytes, element 2i in the low half of byte i; a code is a sign bit over an
+ * index into {0, 0.5, 1, 1.5, 2, 3, 4, 6}.  These are the E8M0 scales and E2M1
+ * elements of the OCP microscaling formats (MXFP4).  Row r's blocks follow
+ * row r-1's: scales [rows][nb], codes [rows][nb][16], nb = ceil(cols / 32);
+ * codes past a row's end are 0.
+ * Quantizing g = float(x) * in_mul, with M = max|g| over the block:
+ *   s = 0 if M = 0, else max(0, floor(log2 M) - 2 + 127);
+ *   code = g * 2^(127 - s) rounded half to even to the magnitudes above,
+ *   magnitudes above 6 to 6, the sign of g kept (of zeros too);
+ *   a block holding inf or NaN gets s = 255 and codes 0.
+ * Nothing here needs a unit table, waits, or allocates. */
+
+/* gq_mx4_sizes -- number of scale bytes and of code bytes of a rows x cols
+ * matrix (host only; either pointer may be NULL).  Errors: GQ_ERR_INVALID
+ * (rows or cols < 1, or more than 2^40 codes). */
+gq_status gq_mx4_sizes(int64_t rows, int64_t cols, int64_t *n_scales, int64_t *code_bytes);
+
+/*
+ * gq_mx4_quantize -- scales and codes of W ranks' matrices.
+ * x          host array of W device pointers, 16-byte aligned; dt GQ_F32,
+ *            GQ_F16 or GQ_BF16; row r starts at element r * ld.
+ * in_mul     as for gq_quantize.
+ * ld         >= cols (ignored for one row).
+ * transpose  0: blocks along the rows of x.  Otherwise the scales and codes
+ *            of x transposed (cols rows of ceil(rows / 32) blocks): blocks
+ *            down the columns of x, as a product over x's rows needs them.
+ * scale_out, q_out  host arrays of W device pointers, of the sizes
+ *            gq_mx4_sizes gives; codes 16-byte aligned.
+ * Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_HIP.
+ */
+gq_status gq_mx4_quantize(const void *const *x, int32_t W, gq_dtype dt, float in_mul, int64_t rows,
+                          int64_t cols, int64_t ld, int32_t transpose, uint8_t *const *scale_out,
+                          uint8_t *const *q_out, gq_stream stream);
+
+/*
+ * gq_mx4_reduce_dequant -- r = ((+0 + d_0) + d_1) + ... + d_{W-1} in binary32,
+ * ranks in order, each d the exact value of its code and scale and each sum
+ * rounded once.  W = 1 decodes.  r_out: rows x cols fp32, contiguous, 16-byte
+ * aligned.  Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_HIP.
+ */
+gq_status gq_mx4_reduce_dequant(const uint8_t *const *q, const uint8_t *const *scale, int32_t W,
+                                int64_t rows, int64_t cols, float *r_out, gq_stream stream);
+
+/*
+ * gq_mx4_reduce_requantize -- the same sum, quantized again: what
+ * gq_mx4_quantize gives for it, fused.  r_out: NULL, or also receives the
+ * sum.  The outputs may not overlap the inputs.
+ */
+gq_status gq_mx4_reduce_requantize(const uint8_t *const *q, const uint8_t *const *scale, int32_t W,
+                                   int64_t rows, int64_t cols, float *r_out, uint8_t *scale_out,
+                                   uint8_t *q_out, gq_stream stream);
+
+/* gq_mx4_product_workspace -- bytes of workspace with which gq_mx4_product
+ * splits k over more work groups where m x n alone gives too few (0 where it
+ * never does).  Host only.  Errors: GQ_ERR_INVALID. */
+gq_status gq_mx4_product_workspace(int64_t m, int64_t n, int64_t k, int64_t *bytes);
+
+/*
+ * gq_mx4_product -- c[i][j] = sum over k of a[i][k] * b[j][k], binary32 sums.
+ * a, a_scale  codes and scales of an m x k matrix; b, b_scale of an n x k
+ *             matrix.  A weight gradient dY^T X over tokens takes the codes
+ *             that gq_mx4_quantize writes with `transpose` for dY and X.
+ * m, n        1 .. 2^28, m * n <= 2^36.  k: 1 .. 2^24.
+ * dt          type of c: GQ_F32, GQ_F16 or GQ_BF16 (rounded once at the end).
+ * accumulate  nonzero (GQ_F32 only): c += the product, with one rounded sum
+ *             per element, as for a gradient summed over micro-batches.
+ * c           row i starts at element i * ldc (ldc >= n); aligned to its
+ *             element, so it may lie anywhere in a flat gradient buffer.
+ * workspace   NULL (k is then not split), or device memory of at least the
+ *             bytes gq_mx4_product_workspace gives, 16-byte aligned; calls
+ *             that share it must be ordered.
+ * The order of the sum over k depends on m, n, k and on whether a workspace
+ * is given, and on nothing else: equal calls give equal bits.  A NaN scale
+ * gives NaN in its row (of a) or column (of b).
+ * Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_CAPACITY (workspace too
+ * small), GQ_ERR_HIP.
+ */
+gq_status gq_mx4_product(const uint8_t *a, const uint8_t *a_scale, const uint8_t *b,
+                         const uint8_t *b_scale, int64_t m, int64_t n, int64_t k, gq_dtype dt,
+                         int32_t accumulate, void *c, int64_t ldc, void *workspace,
+                         int64_t workspace_bytes, gq_stream stream);
 
 #ifdef __cplusplus
 }
