@@ -7,7 +7,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 SO = os.path.join(LIBDIR, "libgq.so")
 SOURCES = ["gq_abi.cpp", "gq_chunker.cpp", "gq_kernels.hip", "gq_check.hip", "gq_noalloc.hip",
-           "gq_mx4.cpp", "gq_mx4.hip", "gq_mx4_product.hip"]
+           "gq_mx4.cpp", "gq_mx4.hip", "gq_mx4_product.hip", "gq_ortho.cpp", "gq_ortho.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

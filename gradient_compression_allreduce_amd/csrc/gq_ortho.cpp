@@ -1,0 +1,324 @@
+// gq_ortho.cpp -- the C-ABI entry points of the orthogonalised update: plans
+// (the matrices of a model, their workspace and the launches' tile tables)
+// and the step.  Contracts: include/gq.h.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "gq_args.h"
+#include "gq_ortho.h"
+
+using namespace gq;
+
+struct gq_ortho {
+    int device = -1;
+    int64_t n = 0;                 // elements of the flat buffers
+    int64_t n_mats = 0;
+    int32_t steps = 0;
+    int32_t tile = 0;
+    float eps = 0.0f;
+    std::vector<float> coef;       // [steps][3]
+    int64_t ws_bytes = 0;
+    char *d_mem = nullptr;         // one allocation: workspace, partials, tables
+    _Float16 *d_ws = nullptr;
+    double *d_part = nullptr;
+    OrMat *d_mats = nullptr;
+    OrTile *d_tiles[OR_TABLES] = {};
+    int64_t n_tiles[OR_TABLES] = {};
+};
+
+namespace {
+
+constexpr int64_t kMaxSide = 1 << 22;       // longer side (buffer bounds are 32 bits)
+constexpr int64_t kMaxShort = 1 << 15;      // shorter side
+constexpr int64_t kMaxMats = 1 << 20;
+constexpr int64_t kMaxTiles = int64_t{1} << 22;
+constexpr int64_t kCus = 256;
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// A run of one matrix's tiles that should share an XCD's L2 cache.
+struct Run {
+    int64_t first, count;
+    int64_t cost;
+};
+
+// Work group i runs on XCD i % 8.  The tiles' runs are dealt out to the eight
+// XCDs, the costliest first, each to the XCD with the least work so far;
+// an XCD that runs out earlier gets empty entries.
+std::vector<OrTile> deal(const std::vector<OrTile> &tiles, std::vector<Run> runs) {
+    std::stable_sort(runs.begin(), runs.end(),
+                     [](const Run &p, const Run &q) { return p.cost > q.cost; });
+    std::vector<OrTile> queue[8];
+    int64_t load[8] = {};
+    for (const Run &r : runs) {
+        const int x = static_cast<int>(std::min_element(load, load + 8) - load);
+        queue[x].insert(queue[x].end(), tiles.begin() + r.first,
+                        tiles.begin() + r.first + r.count);
+        load[x] += r.cost * r.count;
+    }
+    size_t longest = 0;
+    for (const auto &v : queue) longest = std::max(longest, v.size());
+    std::vector<OrTile> out(8 * longest, OrTile{-1, 0, 0});
+    for (int x = 0; x < 8; ++x)
+        for (size_t i = 0; i < queue[x].size(); ++i) out[8 * i + x] = queue[x][i];
+    while (!out.empty() && out.back().mat < 0) out.pop_back();
+    return out;
+}
+
+// Tiles of all matrices' s x s (upper half) or s x l outputs.
+std::vector<OrTile> product_tiles(const std::vector<OrMat> &mats, int tile, bool gram) {
+    std::vector<OrTile> tiles;
+    std::vector<Run> runs;
+    for (size_t m = 0; m < mats.size(); ++m) {
+        const int ts = mats[m].sp / tile, tl = mats[m].lp / tile;
+        const int64_t first = static_cast<int64_t>(tiles.size());
+        if (gram) {
+            for (int i = 0; i < ts; ++i)
+                for (int j = i; j < ts; ++j) tiles.push_back({static_cast<int32_t>(m), i, j});
+        } else {
+            for (int i0 = 0; i0 < ts; i0 += 8)
+                for (int j = 0; j < tl; ++j)
+                    for (int i = i0; i < std::min(ts, i0 + 8); ++i)
+                        tiles.push_back({static_cast<int32_t>(m), i, j});
+        }
+        const int64_t cost = gram ? mats[m].lp : mats[m].sp;
+        for (int64_t f = first; f < static_cast<int64_t>(tiles.size()); f += 32)
+            runs.push_back({f, std::min<int64_t>(32, static_cast<int64_t>(tiles.size()) - f), cost});
+    }
+    return deal(tiles, runs);
+}
+
+// The plan's tile: the largest whose s x l products still give every compute
+// unit a tile.
+int choose_tile(const int64_t *rows, const int64_t *cols, int64_t n) {
+    for (const int t : {256, 128}) {
+        int64_t tiles = 0;
+        for (int64_t i = 0; i < n; ++i)
+            tiles += ((rows[i] + t - 1) / t) * ((cols[i] + t - 1) / t);
+        if (tiles >= kCus) return t;
+    }
+    return 64;
+}
+
+gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_rows,
+                       const int64_t *h_cols, int64_t n_mats, int32_t steps, const float *coef,
+                       float eps, const float *out_mul, gq_ortho **out) {
+    std::vector<OrMat> mats(static_cast<size_t>(n_mats));
+    const int tile = choose_tile(h_rows, h_cols, n_mats);
+    std::vector<OrTile> tab[OR_TABLES];
+    int64_t at = 0, parts = 0;
+    for (int64_t i = 0; i < n_mats; ++i) {
+        OrMat &m = mats[static_cast<size_t>(i)];
+        std::memset(&m, 0, sizeof m);
+        m.off = h_off[i];
+        m.rows = static_cast<int32_t>(h_rows[i]);
+        m.cols = static_cast<int32_t>(h_cols[i]);
+        m.tr = m.rows > m.cols;
+        m.s = std::min(m.rows, m.cols);
+        m.l = std::max(m.rows, m.cols);
+        m.sp = static_cast<int32_t>(round_up(m.s, tile));
+        m.lp = static_cast<int32_t>(round_up(m.l, tile));
+        m.scale = std::exp2(std::round(0.5f * std::log2(static_cast<float>(m.l))));
+        m.out_mul = out_mul ? out_mul[i] : 1.0f;
+        m.vec = m.off % 4 == 0 && m.cols % 4 == 0;
+        const int64_t xl = static_cast<int64_t>(m.sp) * m.lp, al = static_cast<int64_t>(m.sp) * m.sp;
+        for (int k = 0; k < 2; ++k) {
+            m.x[k] = at;
+            at += xl;
+            m.xt[k] = at;
+            at += xl;
+        }
+        m.a = at;
+        at += al;
+        m.b = at;
+        at += al;
+        // at most 1024 partial sums a matrix, of at least 8192 elements
+        const int64_t elems = (m.off & 3) + static_cast<int64_t>(m.rows) * m.cols;
+        m.chunk = std::max<int64_t>(8192, round_up((elems + 1023) / 1024, 4));
+        m.part = static_cast<int32_t>(parts);
+        m.parts = static_cast<int32_t>((elems + m.chunk - 1) / m.chunk);
+        parts += m.parts;
+        for (int32_t p = 0; p < m.parts; ++p) tab[OR_NORM].push_back({static_cast<int32_t>(i), p, 0});
+        const int rp = m.tr ? m.lp : m.sp, cp = m.tr ? m.sp : m.lp;
+        for (int r = 0; r < rp / OR_CAST_TILE; ++r)
+            for (int c = 0; c < cp / OR_CAST_TILE; ++c)
+                tab[OR_CAST].push_back({static_cast<int32_t>(i), r, c});
+        if (static_cast<int64_t>(tab[OR_CAST].size()) >= kMaxTiles)
+            return arg_fail(GQ_ERR_INVALID, op, "more than %lld tiles: too many elements",
+                            static_cast<long long>(kMaxTiles));
+    }
+    tab[OR_GRAM] = product_tiles(mats, tile, true);
+    tab[OR_X] = product_tiles(mats, tile, false);
+    gq_ortho *P = new gq_ortho;
+    P->steps = steps;
+    P->tile = tile;
+    P->eps = eps;
+    static const float quintic[3] = {3.4445f, -4.7750f, 2.0315f};
+    for (int32_t k = 0; k < 3 * steps; ++k) P->coef.push_back(coef ? coef[k] : quintic[k % 3]);
+    P->n_mats = n_mats;
+    P->n = h_off[n_mats - 1] + h_rows[n_mats - 1] * h_cols[n_mats - 1];
+    hipError_t e = hipGetDevice(&P->device);
+    // one allocation, every part at a multiple of 256 bytes
+    int64_t size = round_up(at * 2, 256);
+    const int64_t part_at = size;
+    size += round_up(parts * 8, 256);
+    const int64_t mats_at = size;
+    size += round_up(static_cast<int64_t>(mats.size() * sizeof(OrMat)), 256);
+    int64_t tab_at[OR_TABLES];
+    for (int k = 0; k < OR_TABLES; ++k) {
+        tab_at[k] = size;
+        size += round_up(static_cast<int64_t>(tab[k].size() * sizeof(OrTile)), 256);
+    }
+    P->ws_bytes = size;
+    if (e == hipSuccess)
+        e = hipMalloc(reinterpret_cast<void **>(&P->d_mem), static_cast<size_t>(size));
+    if (e == hipSuccess) {
+        P->d_ws = reinterpret_cast<_Float16 *>(P->d_mem);
+        P->d_part = reinterpret_cast<double *>(P->d_mem + part_at);
+        P->d_mats = reinterpret_cast<OrMat *>(P->d_mem + mats_at);
+        e = hipMemcpy(P->d_mats, mats.data(), mats.size() * sizeof(OrMat), hipMemcpyHostToDevice);
+    }
+    for (int k = 0; k < OR_TABLES && e == hipSuccess; ++k) {
+        P->d_tiles[k] = reinterpret_cast<OrTile *>(P->d_mem + tab_at[k]);
+        P->n_tiles[k] = static_cast<int64_t>(tab[k].size());
+        e = hipMemcpy(P->d_tiles[k], tab[k].data(), tab[k].size() * sizeof(OrTile),
+                      hipMemcpyHostToDevice);
+    }
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    if (e != hipSuccess) {
+        (void)hipGetLastError();
+        if (P->d_mem) (void)hipFree(P->d_mem);
+        delete P;
+        return arg_fail(GQ_ERR_HIP, op, "allocating %lld bytes failed: %s",
+                        static_cast<long long>(size), hipGetErrorString(e));
+    }
+    *out = P;
+    return arg_ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+gq_status gq_ortho_create(const int64_t *h_off, const int64_t *h_rows, const int64_t *h_cols,
+                          int64_t n_mats, int32_t steps, const float *coef, float eps,
+                          const float *out_mul, gq_ortho **out) {
+    const char *op = "gq_ortho_create";
+    if (!out) return arg_fail(GQ_ERR_INVALID, op, "out is NULL");
+    *out = nullptr;
+    if (!h_off || !h_rows || !h_cols)
+        return arg_fail(GQ_ERR_INVALID, op, "h_off, h_rows or h_cols is NULL");
+    if (n_mats < 1 || n_mats > kMaxMats)
+        return arg_fail(GQ_ERR_INVALID, op, "n_mats = %lld outside [1, %lld]",
+                        static_cast<long long>(n_mats), static_cast<long long>(kMaxMats));
+    if (steps < 1 || steps > GQ_ORTHO_MAX_STEPS)
+        return arg_fail(GQ_ERR_INVALID, op, "steps = %d outside [1, %d]", steps,
+                        GQ_ORTHO_MAX_STEPS);
+    if (!std::isfinite(eps) || !(eps >= 0.0f))
+        return arg_fail(GQ_ERR_INVALID, op, "eps = %g must be finite and >= 0",
+                        static_cast<double>(eps));
+    for (int32_t k = 0; coef && k < 3 * steps; ++k)
+        if (!std::isfinite(coef[k]))
+            return arg_fail(GQ_ERR_INVALID, op, "coef[%d] is not finite", k);
+    int64_t end = 0;
+    for (int64_t i = 0; i < n_mats; ++i) {
+        const int64_t r = h_rows[i], c = h_cols[i];
+        if (r < 1 || c < 1 || std::max(r, c) > kMaxSide || std::min(r, c) > kMaxShort)
+            return arg_fail(GQ_ERR_INVALID, op,
+                            "matrix %lld of %lld x %lld: sides must be 1 .. %lld, the shorter one "
+                            "at most %lld", static_cast<long long>(i), static_cast<long long>(r),
+                            static_cast<long long>(c), static_cast<long long>(kMaxSide),
+                            static_cast<long long>(kMaxShort));
+        if (h_off[i] < end || h_off[i] > kMaxElems - r * c)
+            return arg_fail(GQ_ERR_INVALID, op,
+                            "matrix %lld at %lld overlaps the one before, or ends above 2^40",
+                            static_cast<long long>(i), static_cast<long long>(h_off[i]));
+        end = h_off[i] + r * c;
+        if (out_mul && !std::isfinite(out_mul[i]))
+            return arg_fail(GQ_ERR_INVALID, op, "out_mul[%lld] is not finite",
+                            static_cast<long long>(i));
+    }
+    try {
+        return ortho_create(op, h_off, h_rows, h_cols, n_mats, steps, coef, eps, out_mul, out);
+    } catch (const std::bad_alloc &) {
+        return arg_fail(GQ_ERR_INVALID, op, "out of host memory");
+    }
+}
+
+gq_status gq_ortho_destroy(gq_ortho *p) {
+    if (!p) return arg_ok();
+    if (p->d_mem) (void)hipFree(p->d_mem);
+    delete p;
+    return arg_ok();
+}
+
+gq_status gq_ortho_info(const gq_ortho *p, int64_t *n, int64_t *n_mats, int64_t *bytes,
+                        int32_t *tile) {
+    if (!p) return arg_fail(GQ_ERR_INVALID, "gq_ortho_info", "plan is NULL");
+    if (n) *n = p->n;
+    if (n_mats) *n_mats = p->n_mats;
+    if (bytes) *bytes = p->ws_bytes;
+    if (tile) *tile = p->tile;
+    return arg_ok();
+}
+
+gq_status gq_ortho_step(gq_ortho *p, const void *g, gq_dtype dt, float in_mul, float *momentum,
+                        float mu, int32_t nesterov, gq_dtype out_dt, void *out, gq_stream stream) {
+    const char *op = "gq_ortho_step";
+    GQ_ARG(arg_dtype(op, "dtype", dt));
+    GQ_ARG(arg_mul(op, in_mul));
+    if (out_dt != GQ_F16 && out_dt != GQ_BF16)
+        return arg_fail(GQ_ERR_INVALID, op, "out must be GQ_F16 or GQ_BF16, got %d",
+                        static_cast<int>(out_dt));
+    GQ_ARG(arg_ptr(op, "g", g, 16));
+    GQ_ARG(arg_ptr(op, "out", out, 16));
+    if (momentum) {
+        GQ_ARG(arg_ptr(op, "momentum", momentum, 16));
+        if (!std::isfinite(mu) || !(mu >= 0.0f))
+            return arg_fail(GQ_ERR_INVALID, op, "mu = %g must be finite and >= 0",
+                            static_cast<double>(mu));
+    }
+    if (!p) return arg_fail(GQ_ERR_INVALID, op, "plan is NULL");
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return arg_fail(GQ_ERR_HIP, op, "hipGetDevice failed");
+    if (dev != p->device)
+        return arg_fail(GQ_ERR_DEVICE, op, "current device %d, plan lives on device %d", dev,
+                        p->device);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    OrArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.mats = p->d_mats;
+    a.ws = p->d_ws;
+    a.part = p->d_part;
+    a.g = g;
+    a.m = momentum;
+    a.out = out;
+    a.in_mul = in_mul;
+    a.mu = mu;
+    a.eps = p->eps;
+    a.nesterov = nesterov != 0;
+    a.tiles = p->d_tiles[OR_NORM];
+    hipError_t e = launch_ortho_norm(a, p->n_tiles[OR_NORM], dt, st);
+    a.tiles = p->d_tiles[OR_CAST];
+    if (e == hipSuccess) e = launch_ortho_cast(a, p->n_tiles[OR_CAST], dt, st);
+    for (int32_t k = 0; k < p->steps && e == hipSuccess; ++k) {
+        a.a = p->coef[3 * k];
+        a.b = p->coef[3 * k + 1];
+        a.c = p->coef[3 * k + 2];
+        a.cur = k & 1;
+        a.tiles = p->d_tiles[OR_GRAM];
+        e = launch_ortho_mm(a, p->n_tiles[OR_GRAM], p->tile, OR_MM_GRAM, out_dt, st);
+        if (e == hipSuccess)
+            e = launch_ortho_mm(a, p->n_tiles[OR_GRAM], p->tile, OR_MM_POLY, out_dt, st);
+        a.tiles = p->d_tiles[OR_X];
+        if (e == hipSuccess)
+            e = launch_ortho_mm(a, p->n_tiles[OR_X], p->tile,
+                                k + 1 < p->steps ? OR_MM_STEP : OR_MM_LAST, out_dt, st);
+    }
+    return arg_launch(op, e);
+}
+
+}  // extern "C"

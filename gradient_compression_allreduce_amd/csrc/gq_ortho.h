@@ -1,0 +1,62 @@
+// gq_ortho.h -- types shared by the host side (gq_ortho.cpp) and the kernels
+// (gq_ortho.hip) of the orthogonalised update.  Not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gq.h"
+
+namespace gq {
+
+// One matrix of a plan.  X is the matrix itself or, where it has more rows
+// than columns, its transpose: s x l with s <= l, padded with zeros to
+// sp x lp (multiples of the plan's tile).  Offsets are fp16 elements of the
+// plan's workspace; x and xt hold X and X^T twice, read and written in turn.
+struct OrMat {
+    int64_t off;        // first element in the flat gradient, momentum and output
+    int64_t x[2];       // [sp][lp]
+    int64_t xt[2];      // [lp][sp]
+    int64_t a;          // [sp][sp]
+    int64_t b;          // [sp][sp]
+    int64_t chunk;      // elements (a multiple of 4) per partial sum of squares
+    int32_t rows, cols;
+    int32_t s, l, sp, lp;
+    int32_t tr;         // X is the transpose
+    int32_t part;       // first partial sum of squares, and how many
+    int32_t parts;
+    float scale;        // X is stored times this power of two
+    float out_mul;
+    int32_t vec;        // rows start at multiples of four elements
+};
+
+// A tile of a launch (mat < 0: none, it only keeps the order of the XCDs).
+struct OrTile {
+    int32_t mat, i, j;
+};
+
+struct OrArgs {
+    const OrMat *mats;
+    const OrTile *tiles;
+    _Float16 *ws;
+    double *part;
+    const void *g;
+    float *m;           // NULL: no momentum
+    void *out;
+    float in_mul, mu, eps;
+    float a, b, c;      // the step's coefficients
+    int32_t nesterov;
+    int32_t cur;        // which of x[] is read
+};
+
+enum OrTable { OR_NORM = 0, OR_CAST = 1, OR_GRAM = 2, OR_X = 3, OR_TABLES = 4 };
+enum OrMode { OR_MM_GRAM = 0, OR_MM_POLY = 1, OR_MM_STEP = 2, OR_MM_LAST = 3 };
+
+constexpr int OR_CAST_TILE = 64;
+
+hipError_t launch_ortho_norm(const OrArgs &a, int64_t n, gq_dtype dt, hipStream_t s);
+hipError_t launch_ortho_cast(const OrArgs &a, int64_t n, gq_dtype dt, hipStream_t s);
+hipError_t launch_ortho_mm(const OrArgs &a, int64_t n, int tile, OrMode mode, gq_dtype out,
+                           hipStream_t s);
+
+}  // namespace gq

@@ -37,7 +37,8 @@ EXPORTS = ("gq_last_error", "gq_version", "gq_plan_chunks", "gq_units_create",
            "gq_pipe_slots", "gq_pipe_schedule", "gq_pipe_faults", "gq_pipe_clear_faults", "gq_pipe_step", "gq_chunker_create",
            "gq_chunker_destroy", "gq_chunker_update", "gq_chunker_predict", "gq_chunker_plan",
            "gq_mx4_sizes", "gq_mx4_quantize", "gq_mx4_reduce_dequant", "gq_mx4_reduce_requantize",
-           "gq_mx4_product_workspace", "gq_mx4_product")
+           "gq_mx4_product_workspace", "gq_mx4_product", "gq_ortho_create", "gq_ortho_destroy",
+           "gq_ortho_info", "gq_ortho_step")
 GQ_STATS = 10
 STATS = ("max_abs_err", "max_abs_ref", "max_rel_err", "sum_abs_err", "sum_abs_ref",
          "mean_rel_err", "sum_dd", "sum_rr", "sum_dr", "cos")
@@ -137,6 +138,15 @@ def _load():
     L.gq_mx4_product_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
     L.gq_mx4_product.restype = st
     L.gq_mx4_product.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, i64, vp, i64, vp]
+    L.gq_ortho_create.restype = st
+    L.gq_ortho_create.argtypes = [vp, vp, vp, i64, i32, vp, f32, vp, ctypes.POINTER(vp)]
+    L.gq_ortho_destroy.restype = st
+    L.gq_ortho_destroy.argtypes = [vp]
+    L.gq_ortho_info.restype = st
+    L.gq_ortho_info.argtypes = [vp, ctypes.POINTER(i64), ctypes.POINTER(i64), ctypes.POINTER(i64),
+                                ctypes.POINTER(i32)]
+    L.gq_ortho_step.restype = st
+    L.gq_ortho_step.argtypes = [vp, vp, i32, f32, vp, f32, i32, i32, vp, vp]
     return L
 
 
@@ -275,6 +285,7 @@ def _dt():
         _TORCH["i64"] = (torch.int64,)
         _TORCH["f64"] = (torch.float64,)
         _TORCH["u8"] = (torch.uint8,)
+        _TORCH["half"] = (torch.float16, torch.bfloat16)
         _TORCH["code"] = {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16}
     return _TORCH
 
@@ -837,3 +848,92 @@ def gq_mx4_product(a, a_scale, b, b_scale, k, out, accumulate=False, workspace=N
     _check(lib.gq_mx4_product(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
                               m, n, k, T["code"][out.dtype], 1 if accumulate else 0,
                               out.data_ptr(), ldc, wp, wn, _stream(stream)))
+
+
+ORTHO_COEF = (3.4445, -4.7750, 2.0315)
+
+
+class Ortho:
+    """Owner of a gq_ortho plan (destroyed with the object)."""
+
+    def __init__(self, shapes, offsets=None, steps=5, coef=None, eps=1e-7, out_mul=None):
+        shapes = np.asarray(shapes, dtype=np.int64)
+        if shapes.ndim != 2 or shapes.shape[1] != 2 or shapes.shape[0] < 1:
+            raise ValueError("shapes must be a list of (rows, cols)")
+        rows, cols = (np.ascontiguousarray(shapes[:, k]) for k in range(2))
+        count = rows.size
+        if offsets is None:
+            offsets = np.concatenate([[0], np.cumsum(rows * cols)[:-1]])
+        off = np.ascontiguousarray(offsets, dtype=np.int64)
+        if off.shape != (count,):
+            raise ValueError("offsets must hold one offset per matrix")
+        cp = mp = None
+        if coef is not None:
+            coef = np.ascontiguousarray(coef, dtype=np.float32)
+            if coef.shape != (steps, 3):
+                raise ValueError("coef must hold (a, b, c) for each of the %d steps" % steps)
+            cp = coef.ctypes.data
+        if out_mul is not None:
+            out_mul = np.ascontiguousarray(out_mul, dtype=np.float32)
+            if out_mul.shape != (count,):
+                raise ValueError("out_mul must hold one number per matrix")
+            mp = out_mul.ctypes.data
+        h = ctypes.c_void_p()
+        _check(lib.gq_ortho_create(off.ctypes.data, rows.ctypes.data, cols.ctypes.data, count,
+                                   steps, cp, eps, mp, ctypes.byref(h)))
+        self.handle = h
+        self.n = int(off[-1] + rows[-1] * cols[-1])
+        self.n_mats = count
+        _live.add(self)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            _check(lib.gq_ortho_destroy(self.handle))
+            self.handle = ctypes.c_void_p()
+
+    def __del__(self):
+        # (at interpreter shutdown this module's globals may already be
+        # None; the exit hook has freed the handle by then)
+        try:
+            if not _finalizing():
+                self.close()
+        except Exception:
+            pass
+
+
+def gq_ortho_create(shapes, offsets=None, steps=5, coef=None, eps=1e-7, out_mul=None):
+    """Plan for matrices of the given (rows, cols), which lie at `offsets` in
+    the flat buffers (None: one after another).  coef: (a, b, c) per step."""
+    return Ortho(shapes, offsets, steps, coef, eps, out_mul)
+
+
+def gq_ortho_destroy(plan):
+    plan.close()
+
+
+def gq_ortho_info(plan):
+    """{"n", "n_mats", "bytes", "tile"} of a plan."""
+    n, c, b = ctypes.c_int64(0), ctypes.c_int64(0), ctypes.c_int64(0)
+    t = ctypes.c_int32(0)
+    _check(lib.gq_ortho_info(plan.handle, ctypes.byref(n), ctypes.byref(c), ctypes.byref(b),
+                             ctypes.byref(t)))
+    return {"n": n.value, "n_mats": c.value, "bytes": b.value, "tile": t.value}
+
+
+def gq_ortho_step(plan, g, out, in_mul=1.0, momentum=None, mu=0.95, nesterov=True, stream=None):
+    """out (float16 or bfloat16) = the orthogonalised update of every matrix
+    of the plan from the flat gradient g (float32, float16 or bfloat16) and,
+    if given, the flat fp32 momentum, which is updated."""
+    if not isinstance(plan, Ortho) or not getattr(plan, "handle", None):
+        raise ValueError("plan must be a live plan (gq_ortho_create)")
+    dev = _current_device()
+    T = _dt()
+    _need("g", g, plan.n, T["code"], dev)
+    _need("out", out, plan.n, T["half"], dev)
+    mp = None
+    if momentum is not None:
+        _need("momentum", momentum, plan.n, T["f32"], dev)
+        mp = momentum.data_ptr()
+    _check(lib.gq_ortho_step(plan.handle, g.data_ptr(), T["code"][g.dtype], in_mul, mp, mu,
+                             1 if nesterov else 0, T["code"][out.dtype], out.data_ptr(),
+                             _stream(stream)))

@@ -652,6 +652,74 @@ gq_status gq_mx4_product(const uint8_t *a, const uint8_t *a_scale, const uint8_t
                          int32_t accumulate, void *c, int64_t ldc, void *workspace,
                          int64_t workspace_bytes, gq_stream stream);
 
+/* ---- Orthogonalised update -------------------------------------------------
+ * The optimizer step that takes the reduced gradient of a weight matrix to an
+ * update whose singular values all lie near 1 (as the Muon optimizer does).
+ * Per matrix, with g = float(x) * in_mul:
+ *   m <- mu * m + g          (two rounded binary32 operations)
+ *   u = m, or with nesterov g + mu * m;  without momentum u = g
+ *   X = u / (|u|_F + eps)    (|u|_F from a binary64 sum of squares)
+ *   per step, with its coefficients (a, b, c):
+ *     G = X X^T;  X <- a X + (b G + c G G) X
+ *     (on the transpose where a matrix has more rows than columns)
+ *   out = out_mul * X
+ * X, G and b G + c G G are rounded to binary16 each time they are stored;
+ * products are summed in binary32.  A rounding of X (2^-12 of its norm) grows
+ * by at most the step's largest slope, a = 3.4445 for singular values near 0
+ * in the default coefficients: for gradients whose small singular values are
+ * below about 1/500 of the largest, those directions of the result carry
+ * that noise.  A zero matrix gives 0; inf or NaN makes its own matrix NaN and
+ * no other. */
+
+typedef struct gq_ortho gq_ortho;
+
+/*
+ * gq_ortho_create -- plan the step for the matrices of a model on the current
+ * device.
+ * h_off, h_rows, h_cols  host arrays of n_mats (1 .. 2^20): matrix i is rows
+ *             x cols, row-major and contiguous, from element h_off[i] of the
+ *             flat buffers on; offsets increase and matrices do not overlap.
+ *             Elements between them are neither read nor written.  The
+ *             shorter side is at most 2^15, the longer at most 2^22.
+ * steps       1 .. GQ_ORTHO_MAX_STEPS.
+ * coef        NULL: (3.4445, -4.7750, 2.0315) in every step; otherwise a host
+ *             array of 3 * steps finite floats.
+ * eps         finite, >= 0 (a common choice is 1e-7).
+ * out_mul     NULL (1), or a host array of n_mats finite floats.
+ * Allocates device memory (about 8 bytes per element, and 4 per element of
+ * the square of each shorter side, sides rounded up to the tile) and
+ * synchronizes.  Errors: GQ_ERR_INVALID, GQ_ERR_HIP.
+ */
+#define GQ_ORTHO_MAX_STEPS 16
+gq_status gq_ortho_create(const int64_t *h_off, const int64_t *h_rows, const int64_t *h_cols,
+                          int64_t n_mats, int32_t steps, const float *coef, float eps,
+                          const float *out_mul, gq_ortho **out);
+
+/* Free a plan (its work must have completed; NULL is accepted). */
+gq_status gq_ortho_destroy(gq_ortho *p);
+
+/* Elements of the flat buffers (the end of the last matrix), matrices, bytes
+ * of device memory, and rows and columns of an output tile (informational);
+ * any pointer may be NULL. */
+gq_status gq_ortho_info(const gq_ortho *p, int64_t *n, int64_t *n_mats, int64_t *bytes,
+                        int32_t *tile);
+
+/*
+ * gq_ortho_step -- one update of all of the plan's matrices.
+ * g         device array of n elements of dt (GQ_F32, GQ_F16 or GQ_BF16),
+ *           16-byte aligned, e.g. the sum a reduce call wrote.
+ * in_mul    as for gq_quantize.
+ * momentum  NULL, or a device array of n fp32, 16-byte aligned, updated.
+ * mu        finite, >= 0; nesterov: 0 or not.  Ignored without momentum.
+ * out       device array of n elements of out_dt (GQ_F16 or GQ_BF16),
+ *           16-byte aligned, not overlapping g or momentum.
+ * The plan holds the call's workspace: calls that use one plan must be
+ * ordered, captured ones included.  Equal calls give equal bits.
+ * Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_DEVICE, GQ_ERR_HIP.
+ */
+gq_status gq_ortho_step(gq_ortho *p, const void *g, gq_dtype dt, float in_mul, float *momentum,
+                        float mu, int32_t nesterov, gq_dtype out_dt, void *out, gq_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
