@@ -2,24 +2,39 @@
 // shared by the MX4 product and the fp16 products of the orthogonalisation.
 // Not part of the ABI.
 //
-// Both operands are rows of contiguous K.  A K step is 128 bytes of every
-// row (64 fp16 elements, 256 4-bit codes); a lane's operand of one 16 x 16
-// matrix instruction is 16 bytes of a row in either type, so the loop, its
-// LDS layout and its loads do not depend on the type.
+// P is stored by rows of contiguous K; so is Q, or (fp16) Q^T is: K rows of
+// contiguous columns of C.  A K step is 128 bytes of every row (64 fp16
+// elements, 256 4-bit codes), a whole line of the L2 cache: with half lines
+// the requests to the L2 cache bound the loop (fp16 at 8192^3: 1.02 PFLOP/s
+// with steps of 64 bytes, 1.21 with 128).  A lane's operand of one 16 x 16
+// matrix instruction is 16 bytes of a row in either type, so the loops,
+// their LDS layout and their loads do not depend on the type.
 //   * Loads go from global memory to LDS with no register in between
-//     (16 bytes per lane), one step ahead of the arithmetic, into the other of
-//     two buffers; rows and chunks outside the matrix read as zeros by the
-//     buffer descriptor's bound.
-//   * In LDS a row's eight 16-byte chunks are stored at (chunk ^ (row & 7)),
-//     so the 16 rows that a matrix instruction reads at one chunk index fall
-//     into different banks.  A wave's load writes consecutive LDS addresses, so
-//     the exchange is made on the global side, in which chunk a lane asks for.
+//     (16 bytes per lane).  Rows, columns and chunks outside the matrix read as
+//     zeros by the buffer descriptor's bound; the number of steps is rounded
+//     up to an even one.
+//   * In LDS the eight 16-byte chunks of row r are stored at chunk ^ (r & 7).
+//     A 16-byte LDS read serves the lanes 0-3, 12-15 and 20-27 together (and
+//     so on): with this order those sixteen fall into different banks.  A
+//     wave's load writes consecutive LDS addresses, so the exchange is made
+//     on the global side, in which chunk a lane asks for.
 //   * The instruction's first operand is Q and its second P: a lane then
 //     holds four consecutive columns of one row of C.
+//   * mm_loop (tiles of 128 and 64): two buffers of a step each; two or more
+//     work groups per compute unit cover each other's waits.
+//   * mm_quad (tiles of 256, one work group of eight waves per compute unit):
+//     each of P and Q is two halves of 128 rows with buffers of their own, and
+//     the waves go through the four quadrants of C together, so a half's
+//     buffer is free again after the first quadrant that reads it and its
+//     next load starts then, one and a half steps ahead.  (fp16 at 8192^3:
+//     1.24-1.28 PFLOP/s, 1.21 with the two whole buffers, and 1.24 for the
+//     library's product; 4 bits: 3.9 PFLOP/s, 3.75.)
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 namespace gq {
 namespace {
@@ -27,167 +42,559 @@ namespace {
 typedef float mm_f32x4 __attribute__((ext_vector_type(4)));
 typedef int mm_i32x4 __attribute__((ext_vector_type(4)));
 typedef int mm_i32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned int mm_u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int mm_u32x2 __attribute__((ext_vector_type(2)));
+typedef short mm_i16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 mm_f16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void mm_lds_void;
+typedef __attribute__((address_space(3))) mm_i16x4 mm_lds_i16x4;
 
 constexpr int MM_STEP = 128;     // bytes of K per step and row
 
-// A matrix operand's rows [row0, ...) as a buffer: `bytes` per row, `rows`
-// valid rows from row0 on (at most 256 of them are read).
+// The thread's number, as if it were read anew: addresses that follow from it
+// are then worked out where they are used.  (The compiler would keep all of
+// them in registers through the loop, which has none to spare, and reload
+// some from memory in every step.)
+__device__ __forceinline__ int mm_tid() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
+// Tile shapes: T x T of C by WM x WN waves.  A wave's part of C is PARTS
+// blocks of FM x FN matrix instructions; block b, instruction row i and the
+// lane's row r (0 .. 15) are at part_row / part_col of the tile.
+template <int T_, int WM_, int WN_>
+struct MmShape {
+    static constexpr int T = T_, WM = WM_, WN = WN_;
+    static constexpr bool QUAD = T == 256;
+    static constexpr int THREADS = 64 * WM * WN;
+    static constexpr int PARTS = QUAD ? 2 : 1;
+    static constexpr int FM = T / WM / 16, FN = T / WN / 16 / PARTS;
+    static constexpr int UNIT = QUAD ? 128 * MM_STEP : 2 * T * MM_STEP;  // bytes of one buffer
+    static constexpr int SB = T > 128 ? T / 16 : 8;              // bytes of a scale row
+    static constexpr int SCALES = 2 * SB * 256;                  // scale bytes of two steps
+    // first row of instruction row i, and first column of block b
+    static __device__ __forceinline__ int part_row(int wave, int i) {
+        if (QUAD) return (i >> 2) * 128 + wave / WN * 64 + (i & 3) * 16;
+        return wave / WN * (T / WM) + 16 * i;
+    }
+    static __device__ __forceinline__ int part_col(int wave, int b) {
+        if (QUAD) return b * 128 + wave % WN * 32;
+        return wave % WN * (T / WN);
+    }
+};
+using MmBig = MmShape<256, 2, 4>;
+using MmMid = MmShape<128, 2, 2>;
+using MmSmall = MmShape<64, 2, 2>;
+
+// Rows [row0, row0 + tile) of an operand, `bytes` per row, as a buffer.
 struct MmRows {
     __amdgpu_buffer_rsrc_t rsrc;
     uint32_t bytes;
 };
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mm_buffer(const char *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0, static_cast<int>(bytes),
+                                             0x00027000);
+}
+
 __device__ __forceinline__ MmRows mm_rows(const void *base, uint32_t bytes, int64_t row0,
                                           int64_t rows, int tile) {
     const int64_t left = rows - row0;
     const uint32_t valid = static_cast<uint32_t>(left < tile ? left : tile);
-    const char *p = static_cast<const char *>(base) + row0 * bytes;
-    return {__builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(p), 0,
-                                              static_cast<int>(valid * bytes), 0x00027000),
-            bytes};
+    return {mm_buffer(static_cast<const char *>(base) + row0 * bytes, valid * bytes), bytes};
 }
 
-// Starts the loads of R rows' K step kt into `lds` (R * 128 bytes).
+__device__ __forceinline__ void mm_dma(const __amdgpu_buffer_rsrc_t &r, char *lds, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void *)lds, 16, static_cast<int>(off), 0, 0,
+                                             0);
+}
+
+// Starts the loads of the R rows from row0 of the tile on of a step into
+// `lds` (R * 128 bytes).
 template <int R, int THREADS>
-__device__ __forceinline__ void mm_load(const MmRows &m, char *lds, int kt) {
-    const int tid = threadIdx.x;
+__device__ __forceinline__ void mm_load(const MmRows &m, char *lds, int step, int row0) {
+    const int tid = mm_tid();
     const uint32_t row = tid >> 3;
-    const uint32_t at = static_cast<uint32_t>(kt) * MM_STEP + (((tid & 7) ^ (row & 7)) << 4);
+    const uint32_t at = static_cast<uint32_t>(step) * MM_STEP + (((tid & 7) ^ (row & 7)) << 4);
     // a chunk past the row's end must not read the next row
-    const uint32_t off = at < m.bytes ? row * m.bytes + at : 0xfffffff0u;
-    char *dst = lds + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
+    const bool in = at < m.bytes;
+    const uint32_t off = in ? (row + row0) * m.bytes + at : 0xfffffff0u;
+    char *dst = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
 #pragma unroll
-    for (int i = 0; i < R * 8 / THREADS; ++i) {
-        const uint32_t o = off + (at < m.bytes ? i * (THREADS / 8) * m.bytes : 0u);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            m.rsrc, (__attribute__((address_space(3))) void *)(dst + i * THREADS * 16), 16,
-            static_cast<int>(o), 0, 0, 0);
-    }
+    for (int i = 0; i < R * 8 / THREADS; ++i)
+        mm_dma(m.rsrc, dst + i * THREADS * 16, off + (in ? i * (THREADS / 8) * m.bytes : 0u));
 }
 
 // The 16 bytes of row r16 (a multiple of 16) + lane % 16 that the lane
-// contributes to the matrix instruction of half kk of the step.
-__device__ __forceinline__ mm_i32x4 mm_frag(const char *lds, int r16, int kk) {
-    const int lane = threadIdx.x & 63;
+// contributes to a matrix instruction of half kk of the step.
+__device__ __forceinline__ mm_i32x4 mm_frag(const char *lds, int r16, int kk, int lane) {
     const int chunk = (kk * 4 + (lane >> 4)) ^ (lane & 7);
     return *reinterpret_cast<const mm_i32x4 *>(lds + (r16 + (lane & 15)) * MM_STEP + chunk * 16);
 }
 
+// Q by rows of columns (fp16): `pitch` bytes between the K rows, `base` at the
+// tile's first column, `skip` bytes before it in the row.
+struct MmCols {
+    const char *base;
+    uint32_t pitch, skip;
+    int rows;
+};
+
+// Where K row r of a step keeps its 32-byte pieces (16 columns): piece ^ this.
+// A transposing read takes 16 columns of four rows for each 16 lanes; the
+// rows that are read together fall into different banks.
+template <int BN>
+__device__ __forceinline__ uint32_t mm_turn(uint32_t r) {
+    const uint32_t g = ((r >> 3) ^ (r >> 4)) & 1u;
+    return BN >= 128 ? (r & 3u) | (g << 2) : ((r >> 1) & 1u) | (g << 1);
+}
+
+// Starts the loads of a step: 64 K rows of the BN columns from col0 of the
+// tile on (BN * 128 bytes).
+template <int BN, int THREADS>
+__device__ __forceinline__ void mm_load(const MmCols &m, char *lds, int step, int col0) {
+    const int left = m.rows - step * 64;
+    const uint32_t valid = left < 0 ? 0u : left < 64 ? left : 64u;
+    const __amdgpu_buffer_rsrc_t r =
+        mm_buffer(m.base + static_cast<int64_t>(step) * 64 * m.pitch + col0 * 2,
+                  valid ? valid * m.pitch - m.skip - col0 * 2 : 0u);
+    constexpr int CH = BN / 8;           // 16-byte chunks per row
+    const int tid = mm_tid();
+    char *dst = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+#pragma unroll
+    for (int i = 0; i < BN * 8 / THREADS; ++i) {
+        const uint32_t row = (i * THREADS + tid) / CH;
+        const uint32_t chunk = (tid % CH) ^ (mm_turn<BN>(row) << 1);
+        mm_dma(r, dst + i * THREADS * 16, row * m.pitch + chunk * 16);
+    }
+}
+
+// Where element (row, col) of a step's K rows lies.
+template <int BN>
+__device__ __forceinline__ int mm_cols_at(uint32_t row, uint32_t col) {
+    return row * (BN * 2) + (((col >> 4) ^ mm_turn<BN>(row)) << 5) + (col & 15) * 2;
+}
+
+// The lane's 8 elements of K (32 * kk + 8 * (lane / 16) on) of columns c16 +
+// 16 j + lane % 16.  The reads and the wait for them are one asm block: the
+// compiler takes the builtin for a read that may touch any load to LDS under
+// way, and would wait for all of them before each.
+template <int BN, int FN>
+__device__ __forceinline__ void mm_frag_cols(const char *lds, int c16, int kk, int lane,
+                                             mm_i32x4 (&f)[FN]) {
+    const int q = lane & 15;
+    uint32_t at[2 * FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint32_t row = kk * 32 + (lane >> 4) * 8 + t * 4 + (q >> 2);
+            const char *p = lds + mm_cols_at<BN>(row, c16 + 16 * j + (q & 3) * 4);
+            at[2 * j + t] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)p));
+        }
+    }
+    mm_u32x2 h[2 * FN];
+    static_assert(FN == 2 || FN == 4, "columns per wave");
+    if constexpr (FN == 4) {
+        asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %9\n\t"
+                     "ds_read_b64_tr_b16 %2, %10\n\tds_read_b64_tr_b16 %3, %11\n\t"
+                     "ds_read_b64_tr_b16 %4, %12\n\tds_read_b64_tr_b16 %5, %13\n\t"
+                     "ds_read_b64_tr_b16 %6, %14\n\tds_read_b64_tr_b16 %7, %15\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(h[0]), "=&v"(h[1]), "=&v"(h[2]), "=&v"(h[3]), "=&v"(h[4]),
+                       "=&v"(h[5]), "=&v"(h[6]), "=&v"(h[7])
+                     : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]),
+                       "v"(at[6]), "v"(at[7])
+                     : "memory");
+    } else {
+        asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %5\n\t"
+                     "ds_read_b64_tr_b16 %2, %6\n\tds_read_b64_tr_b16 %3, %7\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(h[0]), "=&v"(h[1]), "=&v"(h[2]), "=&v"(h[3])
+                     : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+                     : "memory");
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+        f[j] = __builtin_bit_cast(mm_i32x4, __builtin_shufflevector(h[2 * j], h[2 * j + 1], 0, 1, 2, 3));
+}
+
 // Scale bytes of the MX4 rows of a tile: thread t looks after row t of the
-// P rows followed by the Q rows, eight bytes per K step.
+// P rows followed by the Q rows, sixteen bytes for each two steps.  In LDS
+// the byte of block b and row 16 i + r lies at (16 b + r) * SB + i (SB bytes
+// for the at most SB values of i), so a lane's scales of all its P (and Q)
+// operands of a step are neighbours, and the matrix instructions pick them by
+// number.  Rows and blocks outside take the nearest one inside: their codes
+// read as zeros.
 struct MmScale {
-    const uint8_t *p;    // the row's scales; NULL for a row outside
+    const uint8_t *p;      // the row's scales
+    const uint8_t *ahead;  // the same, or with nb < 16 any sixteen readable bytes
     int64_t nb;
 };
 
-__device__ __forceinline__ uint64_t mm_scale8(const MmScale &s, int kt) {
-    const int64_t b = static_cast<int64_t>(kt) * 8;
-    uint64_t v = 0;
-    if (s.p && b + 8 <= s.nb) {
-        __builtin_memcpy(&v, s.p + b, 8);
-    } else if (s.p) {
-        for (int i = 0; i < 8; ++i)
-            if (b + i < s.nb) v |= static_cast<uint64_t>(s.p[b + i]) << (8 * i);
+// The sixteen bytes of a group, any number of blocks.
+__device__ __forceinline__ mm_u32x4 mm_scale_any(const MmScale &s, int group) {
+    const int64_t b = static_cast<int64_t>(group) * 16;
+    mm_u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t at = b + i < s.nb ? b + i : s.nb - 1;
+        v[i >> 2] |= static_cast<uint32_t>(s.p[at]) << (8 * (i & 3));
     }
     return v;
 }
 
-// Tile shapes: BM x BN of C by WM x WN waves, FM x FN matrix instructions
-// per wave and half step.
-template <int BM_, int BN_, int WM_, int WN_>
-struct MmShape {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
-    static constexpr int THREADS = 64 * WM * WN;
-    static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-    static constexpr int STAGE = (BM + BN) * MM_STEP;            // bytes of one buffer
-    static constexpr int STAGE_MX = STAGE + (BM + BN) * 8;       // with scales behind
+// The same for a later group (so nb > 16): one load of the sixteen bytes that
+// end no later than the row, and, apart so that the load stays in flight,
+// their shift down to the group's first (0 but in the row's last group).  A
+// group past the row's end reads what nobody uses.
+__device__ __forceinline__ mm_u32x4 mm_scale_load(const MmScale &s, int group) {
+    const int64_t b = static_cast<int64_t>(group) * 16, last = s.nb > 16 ? s.nb - 16 : 0;
+    mm_u32x4 v;
+    __builtin_memcpy(&v, s.ahead + (b < last ? b : last), 16);
+    return v;
+}
+
+__device__ __forceinline__ mm_u32x4 mm_scale_shift(mm_u32x4 v, const MmScale &s, int group) {
+    const int64_t late = static_cast<int64_t>(group) * 16 - (s.nb - 16);
+    const int by = late <= 0 ? 0 : late > 15 ? 15 : static_cast<int>(late);
+    return __builtin_bit_cast(mm_u32x4, __builtin_bit_cast(unsigned __int128, v) >> (8 * by));
+}
+
+// The bytes of rows 16 i + r for i in [first, first + F) (first a multiple of
+// F): F <= 4 in w[0], otherwise in both.  (Always one read of eight bytes:
+// of that one the compiler keeps what it may alias.)
+template <int F>
+struct MmBytes {
+    uint32_t w[2];
+    __device__ __forceinline__ void read(const char *row, int first) {
+        const mm_u32x2 v = *reinterpret_cast<const mm_u32x2 *>(row + (first & ~7));
+        w[0] = v.x;
+        w[1] = v.y;
+        if (F <= 4) w[0] = (first & 4) ? v.y : v.x;
+        if (F <= 2) w[0] >>= 8 * (first & 2);
+    }
 };
 
-// acc += the K steps [kt0, kt0 + 2 * pairs) of the tile's product.  s0 and
-// s1 are two LDS arrays of a stage each (two arrays, so that the compiler
-// sees that the loads under way do not touch what is being read).  Steps
-// past the rows' ends add zeros.  Every load has landed on return, and all
-// waves have passed their last read.
-template <typename S, bool MX>
-__device__ __forceinline__ void mm_loop(const MmRows &p, const MmRows &q, const MmScale &sc,
-                                        int kt0, int pairs, char *s0, char *s1,
-                                        mm_f32x4 (&acc)[S::FM][S::FN]) {
+// c += the product of two MX4 operands, scale byte I of sq and J of sp.
+template <int I, int J>
+__device__ __forceinline__ mm_f32x4 mm_mx(mm_i32x4 q, mm_i32x4 p, mm_f32x4 c, uint32_t sq,
+                                          uint32_t sp) {
+    const mm_i32x8 a = {q.x, q.y, q.z, q.w, 0, 0, 0, 0}, b = {p.x, p.y, p.z, p.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, I, static_cast<int>(sq),
+                                                            J, static_cast<int>(sp));
+}
+
+// f(0), f(1), ... f(N - 1), each number a constant.
+template <int N, typename F>
+__device__ __forceinline__ void mm_each(F &f) {
+    if constexpr (N > 0) {
+        mm_each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
+}
+
+template <int AT>
+__device__ __forceinline__ void mm_put_byte(uint32_t lds, uint32_t byte) {
+    asm volatile("ds_write_b8 %0, %1 offset:%2" ::"v"(lds), "v"(byte), "n"(AT) : "memory");
+}
+
+// Waits until at most N of the wave's loads are under way.
+template <int N>
+__device__ __forceinline__ void mm_wait() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// (a barrier alone: what the waves hand each other is in LDS, put there by
+// loads that have been waited for and writes that have been, and buffers are
+// reused after reads whose results have been used)
+__device__ __forceinline__ void mm_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Writes the thread's scale bytes of a group to half `half` of the scales.
+// (in asm: of most of these writes the compiler does not see which array they
+// go to, and would wait for every load to LDS first)
+template <typename S>
+__device__ __forceinline__ void mm_put_scale(const char *scale, int half, mm_u32x4 v) {
+    const int t = mm_tid();
+    if (2 * S::T < S::THREADS && t >= 2 * S::T) return;
+    const bool isp = t < S::T;
+    const int row = isp ? t : t - S::T;
+    const char *d = scale + half * S::SCALES + (isp ? 0 : S::SB * 256) + (row & 15) * S::SB +
+                    (row >> 4);
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)d));
+    auto put = [&](auto bc) {
+        constexpr int b = decltype(bc)::value;
+        mm_put_byte<b * 16 * S::SB>(at, v[b >> 2] >> (8 * (b & 3)));
+    };
+    mm_each<16>(put);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
+// c[i][j] += p[i] q[j] over one half step.
+template <bool MX, int FM, int FN>
+__device__ __forceinline__ void mm_block(const mm_i32x4 (&p)[FM], const mm_i32x4 (&q)[FN],
+                                         const uint32_t (&sp)[2], uint32_t sq,
+                                         mm_f32x4 (&c)[FM][FN]) {
+    if constexpr (MX) {
+        auto row = [&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            c[i][0] = mm_mx<0, (i & 3)>(q[0], p[i], c[i][0], sq, sp[i >> 2]);
+            c[i][1] = mm_mx<1, (i & 3)>(q[1], p[i], c[i][1], sq, sp[i >> 2]);
+            if constexpr (FN == 4) {
+                c[i][2] = mm_mx<2, (i & 3)>(q[2], p[i], c[i][2], sq, sp[i >> 2]);
+                c[i][3] = mm_mx<3, (i & 3)>(q[3], p[i], c[i][3], sq, sp[i >> 2]);
+            }
+        };
+        mm_each<FM>(row);
+    } else {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    __builtin_bit_cast(mm_f16x8, q[j]), __builtin_bit_cast(mm_f16x8, p[i]), c[i][j],
+                    0, 0, 0);
+    }
+}
+
+// The LDS of a work group.  The buffers are arrays of their own, so that the
+// compiler sees that the loads under way do not touch what is being read.
+// (Tiles of 128 and 64 use the first two.)
+#define MM_LDS(S)                                                                     \
+    __shared__ __align__(128) char mm_u0[S::UNIT];                                    \
+    __shared__ __align__(128) char mm_u1[S::UNIT];                                    \
+    __shared__ __align__(128) char mm_u2[S::QUAD ? S::UNIT : 16];                     \
+    __shared__ __align__(128) char mm_u3[S::QUAD ? S::UNIT : 16];                     \
+    __shared__ __align__(128) char mm_u4[S::QUAD ? S::UNIT : 16];                     \
+    __shared__ __align__(128) char mm_u5[S::QUAD ? S::UNIT : 16];                     \
+    __shared__ __align__(128) char mm_u6[S::QUAD ? S::UNIT : 16];                     \
+    __shared__ __align__(128) char mm_u7[S::QUAD ? S::UNIT : 16];                     \
+    const MmLds mm_lds = {mm_u0, mm_u1, mm_u2, mm_u3, mm_u4, mm_u5, mm_u6, mm_u7}
+
+struct MmLds {
+    char *u0, *u1, *u2, *u3, *u4, *u5, *u6, *u7;
+    // the wave's own 1 / (waves) of the buffers, after the loop (in asm, lest
+    // the choice becomes a table of LDS addresses, which cannot be linked)
+    template <typename S>
+    __device__ __forceinline__ char *own(int wave) const {
+        uint32_t at = 0;
+        char *const u[8] = {u0, u1, u2, u3, u4, u5, u6, u7};
+#pragma unroll
+        for (int k = 0; k < (S::QUAD ? 8 : 2); ++k) {
+            uint32_t a = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)u[k]));
+            asm("" : "+s"(a));
+            if (k == (S::QUAD ? wave : wave >> 1)) at = a;
+        }
+        if (!S::QUAD) at += (wave & 1) * (S::UNIT / 2);
+        return (char *)reinterpret_cast<mm_lds_void *>(at);
+    }
+};
+
+// A wave's sums: block b, instruction row i, instruction column j.
+template <typename S>
+struct MmAcc {
+    mm_f32x4 c[S::PARTS][S::FM][S::FN];
+};
+
+// What the caller adds to the sums from a step's Q rows while they lie in LDS
+// (nothing).
+struct MmNoExtra {
+    template <typename A>
+    __device__ __forceinline__ void operator()(A &, const char *, int, int) const {}
+};
+
+// acc += the steps [2 * group0, 2 * (group0 + groups)) of the tile's product.
+// MX: the operands are MX4 and `scale` is an LDS array of 2 * S::SCALES bytes.
+// extra(acc, q, step, b) is called where the step's Q rows of block b lie at
+// q.  Every load has landed on return, and all waves have passed their last
+// read.
+template <typename S, bool MX, typename Q, typename X>
+__device__ __forceinline__ void mm_two(const MmRows &p, const Q &q, const MmScale &sc, int group0,
+                                       int groups, const MmLds &u, char *scale, const X &extra,
+                                       MmAcc<S> &acc) {
+    constexpr bool ROWS = std::is_same<Q, MmRows>::value;
+    constexpr int T = S::T;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    const int rm = wave / S::WN * (S::BM / S::WM), rn = wave % S::WN * (S::BN / S::WN);
-    auto load = [&](char *s, int kt) {
-        mm_load<S::BM, S::THREADS>(p, s, kt);
-        mm_load<S::BN, S::THREADS>(q, s + S::BM * MM_STEP, kt);
+    const int rm = S::part_row(wave, 0), rn = S::part_col(wave, 0);
+    auto load = [&](char *s, int step) {
+        mm_load<T, S::THREADS>(p, s, step, 0);
+        mm_load<T, S::THREADS>(q, s + T * MM_STEP, step, 0);
     };
-    auto put_scale = [&](char *s, uint64_t v) {
-        if (S::BM + S::BN == S::THREADS || static_cast<int>(threadIdx.x) < S::BM + S::BN)
-            *reinterpret_cast<uint64_t *>(s + S::STAGE + threadIdx.x * 8) = v;
-    };
-    auto landed = [&]() {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-    };
-    auto compute = [&](const char *s) {
-        uint2 sp[S::FM], sq[S::FN];
-        if constexpr (MX) {
-#pragma unroll
-            for (int i = 0; i < S::FM; ++i)
-                sp[i] = *reinterpret_cast<const uint2 *>(s + S::STAGE +
-                                                         (rm + 16 * i + (lane & 15)) * 8);
-#pragma unroll
-            for (int j = 0; j < S::FN; ++j)
-                sq[j] = *reinterpret_cast<const uint2 *>(
-                    s + S::STAGE + (S::BM + rn + 16 * j + (lane & 15)) * 8);
-        }
-        const int sh = (lane >> 4) * 8;
+    auto compute = [&](const char *s, int half, int t, int step) {
+        extra(acc, s + T * MM_STEP, step, 0);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             mm_i32x4 fp[S::FM], fq[S::FN];
-#pragma unroll
-            for (int i = 0; i < S::FM; ++i) fp[i] = mm_frag(s, rm + 16 * i, kk);
-#pragma unroll
-            for (int j = 0; j < S::FN; ++j) fq[j] = mm_frag(s + S::BM * MM_STEP, rn + 16 * j, kk);
-#pragma unroll
-            for (int i = 0; i < S::FM; ++i) {
-#pragma unroll
-                for (int j = 0; j < S::FN; ++j) {
-                    if constexpr (MX) {
-                        const mm_i32x8 a = {fq[j].x, fq[j].y, fq[j].z, fq[j].w, 0, 0, 0, 0};
-                        const mm_i32x8 b = {fp[i].x, fp[i].y, fp[i].z, fp[i].w, 0, 0, 0, 0};
-                        const int sa = static_cast<int>((kk ? sq[j].y : sq[j].x) >> sh);
-                        const int sb = static_cast<int>((kk ? sp[i].y : sp[i].x) >> sh);
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            a, b, acc[i][j], 4, 4, 0, sa, 0, sb);
-                    } else {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            __builtin_bit_cast(mm_f16x8, fq[j]), __builtin_bit_cast(mm_f16x8, fp[i]),
-                            acc[i][j], 0, 0, 0);
-                    }
-                }
+            MmBytes<S::FM> sp = {};
+            MmBytes<S::FN> sq = {};
+            if constexpr (MX) {
+                const int br = (8 * t + 4 * kk + (lane >> 4)) * 16 + (lane & 15);
+                sp.read(scale + (half * S::SCALES + br * S::SB), rm / 16);
+                sq.read(scale + (half * S::SCALES + S::SB * 256 + br * S::SB), rn / 16);
             }
+            if constexpr (ROWS) {
+#pragma unroll
+                for (int j = 0; j < S::FN; ++j) fq[j] = mm_frag(s + T * MM_STEP, rn + 16 * j, kk, lane);
+            }
+#pragma unroll
+            for (int i = 0; i < S::FM; ++i) fp[i] = mm_frag(s, rm + 16 * i, kk, lane);
+            if constexpr (!ROWS) mm_frag_cols<T, S::FN>(s + T * MM_STEP, rn, kk, lane, fq);
+            __builtin_amdgcn_s_setprio(1);
+            mm_block<MX>(fp, fq, sp.w, sq.w[0], acc.c[0]);
+            __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    uint64_t v = 0;
-    load(s0, kt0);
-    if constexpr (MX) put_scale(s0, mm_scale8(sc, kt0));
-    for (int k = 0; k < pairs; ++k) {
-        const int kt = kt0 + 2 * k;
-        landed();
-        load(s1, kt + 1);
-        if constexpr (MX) v = mm_scale8(sc, kt + 1);
+    if constexpr (MX) mm_put_scale<S>(scale, 0, mm_scale_any(sc, group0));
+    load(u.u0, 2 * group0);
+    for (int g = 0; g < groups; ++g) {
+        const int step = 2 * (group0 + g), half = g & 1;
+        mm_u32x4 v;
+        mm_wait<0>();
+        mm_barrier();
+        if constexpr (MX) v = mm_scale_load(sc, group0 + g + 1);
+        load(u.u1, step + 1);
         __builtin_amdgcn_sched_barrier(0);
-        compute(s0);
-        if constexpr (MX) put_scale(s1, v);
-        landed();
-        load(s0, kt + 2);
-        if constexpr (MX) v = mm_scale8(sc, kt + 2);
+        compute(u.u0, half, 0, step);
+        mm_wait<0>();
+        mm_barrier();
+        load(u.u0, step + 2);
         __builtin_amdgcn_sched_barrier(0);
-        compute(s1);
-        if constexpr (MX) put_scale(s0, v);
+        compute(u.u1, half, 1, step + 1);
+        // into the other half, whose last readers passed this group's first
+        // barrier; written before the next barrier
+        if constexpr (MX)
+            mm_put_scale<S>(scale, (g + 1) & 1, mm_scale_shift(v, sc, group0 + g + 1));
     }
-    landed();
+    mm_wait<0>();
+    __syncthreads();
+}
+
+// The same for tiles of 256: u0 - u3 and u4 - u7 hold P0, Q0, Q1, P1 of an
+// even and an odd step.
+template <typename S, bool MX, typename Q, typename X>
+__device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmScale &sc, int group0,
+                                        int groups, const MmLds &u, char *scale, const X &extra,
+                                        MmAcc<S> &acc) {
+    constexpr bool ROWS = std::is_same<Q, MmRows>::value;
+    constexpr int L = 128 * 8 / S::THREADS;     // a wave's loads per half
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rm = S::part_row(wave, 0), rn = S::part_col(wave, 0);
+    auto load_p = [&](char *s, int step, int h) { mm_load<128, S::THREADS>(p, s, step, 128 * h); };
+    auto load_q = [&](char *s, int step, int h) { mm_load<128, S::THREADS>(q, s, step, 128 * h); };
+    // one half of P (four instruction rows) and both of Q, of both half steps
+    mm_i32x4 fp[2][4], fq[2][2][2];
+    uint32_t sp[2][2] = {}, sq[2][2] = {};
+    auto read_p = [&](const char *s, int half, int t, int h) {
+        const int lane = mm_tid() & 63;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            if constexpr (MX) {
+                MmBytes<4> b;
+                const int br = (8 * t + 4 * kk + (lane >> 4)) * 16 + (lane & 15);
+                b.read(scale + (half * S::SCALES + br * S::SB), 8 * h + rm / 16);
+                sp[kk][0] = b.w[0];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fp[kk][i] = mm_frag(s, rm + 16 * i, kk, lane);
+        }
+    };
+    auto read_q = [&](const char *s, int half, int t, int h) {
+        const int lane = mm_tid() & 63;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            if constexpr (MX) {
+                MmBytes<2> b;
+                const int br = (8 * t + 4 * kk + (lane >> 4)) * 16 + (lane & 15);
+                b.read(scale + (half * S::SCALES + S::SB * 256 + br * S::SB), 8 * h + rn / 16);
+                sq[h][kk] = b.w[0];
+            }
+            if constexpr (ROWS) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) fq[h][kk][j] = mm_frag(s, rn + 16 * j, kk, lane);
+            } else {
+                mm_frag_cols<128, 2>(s, rn, kk, lane, fq[h][kk]);
+            }
+        }
+    };
+    // quadrant (h, b): the instruction rows 4 h .. 4 h + 3 of block b
+    auto quadrant = [&](int h, int b) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            mm_f32x4(&c)[4][2] = *reinterpret_cast<mm_f32x4(*)[4][2]>(&acc.c[b][4 * h]);
+            mm_block<MX>(fp[kk], fq[b][kk], sp[kk], sq[b][kk], c);
+        }
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // A step: each half is loaded again, for the step after next, once all
+    // waves have read it into registers.  Loads are in the order P0 Q0 Q1 P1
+    // of each step, and the waits leave those in flight that are not needed.
+    auto step_of = [&](char *p0, char *q0, char *q1, char *p1, char *other_p1, int step, int half,
+                       int t) {
+        mm_wait<5 * L>();       // P0, Q0 here; Q1, P1 and three of the next step may not be
+        mm_barrier();
+        load_p(other_p1, step + 1, 1);
+        read_p(p0, half, t, 0);
+        read_q(q0, half, t, 0);
+        extra(acc, q0, step, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        quadrant(0, 0);
+        mm_wait<5 * L>();       // Q1
+        mm_barrier();
+        load_p(p0, step + 2, 0);
+        load_q(q0, step + 2, 0);
+        read_q(q1, half, t, 1);
+        extra(acc, q1, step, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        quadrant(0, 1);
+        mm_wait<6 * L>();       // P1
+        mm_barrier();
+        load_q(q1, step + 2, 1);
+        read_p(p1, half, t, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        quadrant(1, 1);
+        quadrant(1, 0);
+    };
+    if constexpr (MX) mm_put_scale<S>(scale, 0, mm_scale_any(sc, group0));
+    const int first = 2 * group0;
+    load_p(u.u0, first, 0);
+    load_q(u.u1, first, 0);
+    load_q(u.u2, first, 1);
+    load_p(u.u3, first, 1);
+    load_p(u.u4, first + 1, 0);
+    load_q(u.u5, first + 1, 0);
+    load_q(u.u6, first + 1, 1);
+    for (int g = 0; g < groups; ++g) {
+        const int step = first + 2 * g, half = g & 1;
+        mm_u32x4 v;
+        step_of(u.u0, u.u1, u.u2, u.u3, u.u7, step, half, 0);
+        if constexpr (MX) v = mm_scale_load(sc, group0 + g + 1);
+        step_of(u.u4, u.u5, u.u6, u.u7, u.u3, step + 1, half, 1);
+        // into the other half, whose last readers passed this group's first
+        // barrier; written before the next barrier
+        if constexpr (MX)
+            mm_put_scale<S>(scale, (g + 1) & 1, mm_scale_shift(v, sc, group0 + g + 1));
+    }
+    mm_wait<0>();
+    __syncthreads();
+}
+
+template <typename S, bool MX, typename Q, typename X>
+__device__ __forceinline__ void mm_loop(const MmRows &p, const Q &q, const MmScale &sc, int group0,
+                                        int groups, const MmLds &u, char *scale, const X &extra,
+                                        MmAcc<S> &acc) {
+    if constexpr (S::QUAD) mm_quad<S, MX>(p, q, sc, group0, groups, u, scale, extra, acc);
+    else mm_two<S, MX>(p, q, sc, group0, groups, u, scale, extra, acc);
 }
 
 // Work group -> tile.  Consecutive work groups go to the eight XCDs in turn;

@@ -14,7 +14,7 @@ constexpr int64_t MX_CUS = 256;   // compute units of an MI355X
 struct MxPlan {
     int32_t tile;     // rows and columns of C per work group
     int32_t splits;   // parts of K
-    int32_t pairs;    // K steps per part, in pairs
+    int32_t groups;   // 512 elements of K each, per part
 };
 
 struct MxPArgs {
@@ -22,7 +22,7 @@ struct MxPArgs {
     void *c;
     float *part;      // NULL, or [splits][m][n] partial sums
     int64_t m, n, nb, ldc;
-    int32_t pairs;
+    int32_t groups;
     int32_t splits;
     int32_t vec;      // four columns of C from a multiple of 4 on are aligned
     int32_t add;

@@ -14,10 +14,6 @@
 namespace gq {
 namespace {
 
-using Big = MmShape<256, 256, 2, 4>;
-using Mid = MmShape<128, 128, 2, 2>;
-using Small = MmShape<64, 64, 2, 2>;
-
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
     const uint32_t u = __float_as_uint(v);
     if ((u & 0x7fffffffu) > kInfBits) return static_cast<uint16_t>((u >> 16) | 0x40u);
@@ -66,35 +62,32 @@ __device__ __forceinline__ void store4(void *c, int64_t at, mm_f32x4 v, int n, b
 
 template <typename S, gq_dtype DT>
 __global__ __launch_bounds__(S::THREADS) void k_mx4_product(const MxPArgs a) {
-    __shared__ __align__(128) char s0[S::STAGE_MX];
-    __shared__ __align__(128) char s1[S::STAGE_MX];
-    const int tm = static_cast<int>((a.m + S::BM - 1) / S::BM);
-    const int tn = static_cast<int>((a.n + S::BN - 1) / S::BN);
+    MM_LDS(S);
+    __shared__ __align__(128) char mm_scale[2 * S::SCALES];
+    const int tm = static_cast<int>((a.m + S::T - 1) / S::T);
+    const int tn = static_cast<int>((a.n + S::T - 1) / S::T);
     int t = mm_xcd(blockIdx.x, gridDim.x);
     const int split = t / (tm * tn);
     int ti, tj;
     mm_tile(t - split * tm * tn, tm, tn, ti, tj);
-    const int64_t i0 = static_cast<int64_t>(ti) * S::BM, j0 = static_cast<int64_t>(tj) * S::BN;
+    const int64_t i0 = static_cast<int64_t>(ti) * S::T, j0 = static_cast<int64_t>(tj) * S::T;
     const uint32_t bytes = static_cast<uint32_t>(a.nb) * MX_BYTES;
-    const MmRows p = mm_rows(a.a, bytes, i0, a.m, S::BM);
-    const MmRows q = mm_rows(a.b, bytes, j0, a.n, S::BN);
-    MmScale sc = {nullptr, a.nb};
+    const MmRows p = mm_rows(a.a, bytes, i0, a.m, S::T);
+    const MmRows q = mm_rows(a.b, bytes, j0, a.n, S::T);
+    MmScale sc = {nullptr, nullptr, a.nb};
     {
         const int r = threadIdx.x;
-        if (r < S::BM) {
-            if (i0 + r < a.m) sc.p = a.sa + (i0 + r) * a.nb;
-        } else if (r < S::BM + S::BN && j0 + r - S::BM < a.n) {
-            sc.p = a.sb + (j0 + r - S::BM) * a.nb;
-        }
+        const int64_t pr = i0 + r < a.m ? i0 + r : a.m - 1;
+        const int64_t qr = j0 + r - S::T < a.n ? j0 + r - S::T : a.n - 1;
+        sc.p = r < S::T ? a.sa + pr * a.nb : a.sb + qr * a.nb;
+        sc.ahead = a.nb > 16 ? sc.p : a.a;
     }
-    mm_f32x4 acc[S::FM][S::FN] = {};
-    const int pairs_all = static_cast<int>((a.nb + 15) / 16);
-    const int k0 = split * a.pairs;
-    const int pairs = pairs_all - k0 < a.pairs ? pairs_all - k0 : a.pairs;
-    mm_loop<S, true>(p, q, sc, 2 * k0, pairs, s0, s1, acc);
+    MmAcc<S> acc = {};
+    const int all = static_cast<int>((a.nb + 15) / 16);
+    const int k0 = split * a.groups;
+    mm_loop<S, true>(p, q, sc, k0, all - k0 < a.groups ? all - k0 : a.groups, mm_lds, mm_scale,
+                     MmNoExtra{}, acc);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t r0 = i0 + wave / S::WN * (S::BM / S::WM) + (lane & 15);
-    const int64_t c0 = j0 + wave % S::WN * (S::BN / S::WN) + (lane >> 4) * 4;
     void *c = a.c;
     int64_t ldc = a.ldc;
     bool vec = a.vec != 0, add = a.add != 0;
@@ -106,17 +99,20 @@ __global__ __launch_bounds__(S::THREADS) void k_mx4_product(const MxPArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < S::FM; ++i) {
-        const int64_t r = r0 + 16 * i;
+        const int64_t r = i0 + S::part_row(wave, i) + (lane & 15);
         if (r >= a.m) continue;
 #pragma unroll
-        for (int j = 0; j < S::FN; ++j) {
-            const int64_t col = c0 + 16 * j;
-            const int left = a.n - col < 4 ? static_cast<int>(a.n - col) : 4;
-            if (left <= 0) continue;
-            if (DT != GQ_F32 && a.splits > 1)
-                store4<GQ_F32>(c, r * ldc + col, acc[i][j], left, vec, false);
-            else
-                store4<DT>(c, r * ldc + col, acc[i][j], left, vec, add);
+        for (int b = 0; b < S::PARTS; ++b) {
+#pragma unroll
+            for (int j = 0; j < S::FN; ++j) {
+                const int64_t col = j0 + S::part_col(wave, b) + 16 * j + (lane >> 4) * 4;
+                const int left = a.n - col < 4 ? static_cast<int>(a.n - col) : 4;
+                if (left <= 0) continue;
+                if (DT != GQ_F32 && a.splits > 1)
+                    store4<GQ_F32>(c, r * ldc + col, acc.c[b][i][j], left, vec, false);
+                else
+                    store4<DT>(c, r * ldc + col, acc.c[b][i][j], left, vec, add);
+            }
         }
     }
 }
@@ -142,7 +138,7 @@ int64_t tiles(const MxPArgs &a, int t) { return (a.m + t - 1) / t * ((a.n + t - 
 
 template <typename S>
 hipError_t product_shape(const MxPArgs &a, gq_dtype dt, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>(tiles(a, S::BM) * a.splits));
+    const dim3 grid(static_cast<unsigned>(tiles(a, S::T) * a.splits));
     const dim3 blk(S::THREADS);
     if (dt == GQ_F32) hipLaunchKernelGGL((k_mx4_product<S, GQ_F32>), grid, blk, 0, st, a);
     else if (dt == GQ_F16) hipLaunchKernelGGL((k_mx4_product<S, GQ_F16>), grid, blk, 0, st, a);
@@ -161,22 +157,22 @@ hipError_t product_shape(const MxPArgs &a, gq_dtype dt, hipStream_t st) {
 
 // The tile and the number of parts of K for an m x n x k product: the
 // largest tile that gives every compute unit one, and where even the
-// smallest gives too few, K in as many parts (of at least four K steps
+// smallest gives too few, K in as many parts (of at least 1024 elements
 // each) as fill them.
 MxPlan mx4_product_plan(int64_t m, int64_t n, int64_t k) {
     MxPArgs a{};
     a.m = m;
     a.n = n;
-    const int64_t pairs = ((k + MX_BLOCK - 1) / MX_BLOCK + 15) / 16;
+    const int64_t groups = ((k + MX_BLOCK - 1) / MX_BLOCK + 15) / 16;
     MxPlan p{};
     p.tile = tiles(a, 256) >= MX_CUS ? 256 : tiles(a, 128) >= MX_CUS ? 128 : 64;
     const int64_t t = tiles(a, p.tile);
     int64_t splits = t >= MX_CUS ? 1 : MX_CUS / t;
-    if (splits > pairs / 2) splits = pairs / 2;
+    if (splits > groups / 2) splits = groups / 2;
     if (splits < 1) splits = 1;
-    const int64_t per = (pairs + splits - 1) / splits;
-    p.pairs = static_cast<int32_t>(per);
-    p.splits = static_cast<int32_t>((pairs + per - 1) / per);
+    const int64_t per = (groups + splits - 1) / splits;
+    p.groups = static_cast<int32_t>(per);
+    p.splits = static_cast<int32_t>((groups + per - 1) / per);
     return p;
 }
 
@@ -184,10 +180,10 @@ hipError_t launch_mx4_product(const MxPArgs &in, int64_t k, gq_dtype dt, hipStre
     MxPArgs a = in;
     const MxPlan p = mx4_product_plan(a.m, a.n, k);
     a.splits = a.part ? p.splits : 1;
-    a.pairs = a.splits > 1 ? p.pairs : static_cast<int32_t>((a.nb + 15) / 16);
-    if (p.tile == 256) return product_shape<Big>(a, dt, st);
-    if (p.tile == 128) return product_shape<Mid>(a, dt, st);
-    return product_shape<Small>(a, dt, st);
+    a.groups = a.splits > 1 ? p.groups : static_cast<int32_t>((a.nb + 15) / 16);
+    if (p.tile == 256) return product_shape<MmBig>(a, dt, st);
+    if (p.tile == 128) return product_shape<MmMid>(a, dt, st);
+    return product_shape<MmSmall>(a, dt, st);
 }
 
 }  // namespace gq

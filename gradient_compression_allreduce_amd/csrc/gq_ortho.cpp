@@ -123,12 +123,10 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
         m.lp = static_cast<int32_t>(round_up(m.l, tile));
         m.scale = std::exp2(std::round(0.5f * std::log2(static_cast<float>(m.l))));
         m.out_mul = out_mul ? out_mul[i] : 1.0f;
-        m.vec = m.off % 4 == 0 && m.cols % 4 == 0;
+        m.align = (m.off | m.cols) % 8 == 0 ? 8 : (m.off | m.cols) % 4 == 0 ? 4 : 1;
         const int64_t xl = static_cast<int64_t>(m.sp) * m.lp, al = static_cast<int64_t>(m.sp) * m.sp;
         for (int k = 0; k < 2; ++k) {
             m.x[k] = at;
-            at += xl;
-            m.xt[k] = at;
             at += xl;
         }
         m.a = at;

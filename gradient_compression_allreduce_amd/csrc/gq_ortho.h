@@ -12,11 +12,10 @@ namespace gq {
 // One matrix of a plan.  X is the matrix itself or, where it has more rows
 // than columns, its transpose: s x l with s <= l, padded with zeros to
 // sp x lp (multiples of the plan's tile).  Offsets are fp16 elements of the
-// plan's workspace; x and xt hold X and X^T twice, read and written in turn.
+// plan's workspace; X is held twice, read and written in turn.
 struct OrMat {
     int64_t off;        // first element in the flat gradient, momentum and output
     int64_t x[2];       // [sp][lp]
-    int64_t xt[2];      // [lp][sp]
     int64_t a;          // [sp][sp]
     int64_t b;          // [sp][sp]
     int64_t chunk;      // elements (a multiple of 4) per partial sum of squares
@@ -27,7 +26,7 @@ struct OrMat {
     int32_t parts;
     float scale;        // X is stored times this power of two
     float out_mul;
-    int32_t vec;        // rows start at multiples of four elements
+    int32_t align;      // elements that the rows start at multiples of: 8, 4 or 1
 };
 
 // A tile of a launch (mat < 0: none, it only keeps the order of the XCDs).

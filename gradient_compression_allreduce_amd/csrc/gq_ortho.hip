@@ -2,7 +2,7 @@
 // T steps of the quintic Newton-Schulz iteration on every matrix of a plan,
 //   X <- u / (|u|_F + eps);  G = X X^T;  Q = b G + c G G;  X <- a X + Q X.
 //   k_ortho_norm  momentum, and each matrix's sum of squares in binary64;
-//   k_ortho_cast  X and X^T in fp16 from u and the sum of squares;
+//   k_ortho_cast  X in fp16 from u and the sum of squares;
 //   k_ortho_mm    the three products of a step over the tiles of all
 //                 matrices together (gq_mm.h: the tile loop), the polynomial
 //                 and the update in its epilogue.
@@ -114,11 +114,11 @@ __global__ __launch_bounds__(OR_BLOCK) void k_ortho_norm(const OrArgs a) {
     if (threadIdx.x == 0) a.part[mt.part + t.i] = sum;
 }
 
-// ---- X and X^T ------------------------------------------------------------------
+// ---- X --------------------------------------------------------------------------
 // A work group takes a 64 x 64 tile of the padded matrix as it lies in the
-// gradient, and writes it to X and, turned in LDS, to X^T (or the other way
-// round where X is the transpose).  Each work group adds up its matrix's
-// partial sums itself, always in the same order.
+// gradient, and writes it to X, turned in LDS where X is the transpose.  Each
+// work group adds up its matrix's partial sums itself, always in the same
+// order.
 template <typename T, bool MOM>
 __global__ __launch_bounds__(OR_BLOCK) void k_ortho_cast(const OrArgs a) {
     __shared__ double sh[OR_BLOCK / 64];
@@ -133,9 +133,7 @@ __global__ __launch_bounds__(OR_BLOCK) void k_ortho_cast(const OrArgs a) {
                        (__dsqrt_rn(sum) + static_cast<double>(a.eps));
     const T *g = static_cast<const T *>(a.g);
     const int c = (threadIdx.x & 15) * 4;
-    const int rp = mt.tr ? mt.lp : mt.sp, cp = mt.tr ? mt.sp : mt.lp;
-    _Float16 *direct = a.ws + (mt.tr ? mt.xt[0] : mt.x[0]);
-    _Float16 *turned = a.ws + (mt.tr ? mt.x[0] : mt.xt[0]);
+    _Float16 *x = a.ws + mt.x[0];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (threadIdx.x >> 4) + 16 * i;
@@ -146,7 +144,7 @@ __global__ __launch_bounds__(OR_BLOCK) void k_ortho_cast(const OrArgs a) {
             const int n = mt.cols - col;    // elements of the row from col on
             f32x4 gv = u, mv = u;
             const bool need_g = !MOM || a.nesterov;
-            if (mt.vec && n >= 4) {
+            if (mt.align > 1 && n >= 4) {
                 if (need_g) gv = load4(g, e, e, e + 4);
                 if (MOM) mv = *reinterpret_cast<const f32x4 *>(a.m + e);
             } else {
@@ -167,19 +165,22 @@ __global__ __launch_bounds__(OR_BLOCK) void k_ortho_cast(const OrArgs a) {
         }
         f16x4 h;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            h[k] = static_cast<_Float16>(u[k]);
-            turn[c + k][r] = h[k];
+        for (int k = 0; k < 4; ++k) h[k] = static_cast<_Float16>(u[k]);
+        if (mt.tr) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) turn[c + k][r] = h[k];
+        } else {
+            *reinterpret_cast<f16x4 *>(x + static_cast<int64_t>(row) * mt.lp + col) = h;
         }
-        *reinterpret_cast<f16x4 *>(direct + static_cast<int64_t>(row) * cp + col) = h;
     }
+    if (!mt.tr) return;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (threadIdx.x >> 4) + 16 * i;
-        const f16x4 h = *reinterpret_cast<const f16x4 *>(&turn[r][c]);
-        *reinterpret_cast<f16x4 *>(turned + static_cast<int64_t>(t.j * OR_CAST_TILE + r) * rp +
-                                   t.i * OR_CAST_TILE + c) = h;
+        *reinterpret_cast<f16x4 *>(x + static_cast<int64_t>(t.j * OR_CAST_TILE + r) * mt.lp +
+                                   t.i * OR_CAST_TILE + c) =
+            *reinterpret_cast<const f16x4 *>(&turn[r][c]);
     }
 }
 
@@ -192,86 +193,198 @@ __device__ __forceinline__ uint16_t out_bits(float v, bool bf16) {
     return static_cast<uint16_t>((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
 }
 
+typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+
+// A wave's part of the tile, TM x TN 16-bit values, on its way out through
+// LDS, so that its stores fill whole lines: 16-byte chunk c of row r lies at
+// chunk c ^ (r & 7) (TN = 64) or c ^ (r >> 1 & 3) (TN = 32).
+template <int TN>
+__device__ __forceinline__ int out_at(int r, int chunk) {
+    const int turn = TN == 64 ? r & 7 : (r >> 1) & 3;
+    return r * TN * 2 + ((chunk ^ turn) << 4);
+}
+
+// Eight values from row r, column 8 * chunk on.
+template <int TN>
+__device__ __forceinline__ u16x8 out_row(const char *lds, int r, int chunk) {
+    return *reinterpret_cast<const u16x8 *>(lds + out_at<TN>(r, chunk));
+}
+
+// Eight values down column c16 + lane % 16, from row r32 + 8 * (lane / 16) on.
+template <int TN>
+__device__ __forceinline__ u16x8 out_col(const char *lds, int r32, int c16) {
+    const int lane = threadIdx.x & 63, q = lane & 15;
+    u16x8 v;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int r = r32 + 8 * (lane >> 4) + 4 * t + (q >> 2);
+        const char *p = lds + out_at<TN>(r, (c16 >> 3) + ((q >> 1) & 1)) + (q & 1) * 8;
+        const mm_i16x4 h = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_i16x4 *)p);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[4 * t + k] = static_cast<unsigned short>(h[k]);
+    }
+    return v;
+}
+
+// The first n of eight values; al: how many elements o is a multiple of.
+__device__ __forceinline__ void store8(uint16_t *o, u16x8 v, int n, int al) {
+    if (n >= 8 && al == 8) {
+        *reinterpret_cast<u16x8 *>(o) = v;
+    } else if (n >= 8 && al == 4) {
+        *reinterpret_cast<u16x4 *>(o) = u16x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<u16x4 *>(o + 4) = u16x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < n) o[k] = v[k];
+    }
+}
+
+// a X of the wave's part of the tile, added while those rows of X pass through
+// LDS as rows of K: X is then read once.
+struct AddX {
+    float a;
+    int i0;     // the tile's first row
+    template <typename S>
+    __device__ __forceinline__ void operator()(MmAcc<S> &acc, const char *q, int step, int b) const {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int lane = mm_tid() & 63;
+        constexpr int BN = S::QUAD ? 128 : S::T;      // columns of q
+        constexpr int RUN = S::QUAD ? 4 : S::FM;      // instruction rows that lie together
+#pragma unroll
+        for (int i0r = 0; i0r < S::FM; i0r += RUN) {
+            const int row = i0 + S::part_row(wave, i0r) - 64 * step;
+            if (row < 0 || row >= 64) continue;
+#pragma unroll
+            for (int i = i0r; i < i0r + RUN; ++i) {
+#pragma unroll
+                for (int j = 0; j < S::FN; ++j) {
+                    const int col = (S::part_col(wave, 0) + 16 * j + (lane >> 4) * 4);
+                    const f16x4 x = *reinterpret_cast<const f16x4 *>(
+                        q + mm_cols_at<BN>(row + 16 * (i - i0r) + (lane & 15), col));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc.c[b][i][j][k] =
+                            __fmaf_rn(a, static_cast<float>(x[k]), acc.c[b][i][j][k]);
+                }
+                __builtin_amdgcn_sched_barrier(0);   // few registers at a time
+            }
+        }
+    }
+};
+
 // MODE OR_MM_GRAM: G = X X^T          (K: columns of X)
 //      OR_MM_POLY: Q = b G + c G G    (G = G^T)
-//      OR_MM_STEP: X <- a X + Q X     (both X and X^T written)
+//      OR_MM_STEP: X <- a X + Q X     (K: rows of X)
 //      OR_MM_LAST: the same into the caller's output
 template <typename S, int MODE>
 __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a, int bf16) {
-    __shared__ __align__(128) char s0[S::STAGE];
-    __shared__ __align__(128) char s1[S::STAGE];
+    MM_LDS(S);
     const OrTile t = a.tiles[blockIdx.x];
     if (t.mat < 0) return;
     const OrMat &mt = a.mats[t.mat];
     const int sp = mt.sp, lp = mt.lp;
-    const int i0 = t.i * S::BM, j0 = t.j * S::BN;
-    const _Float16 *x = a.ws + mt.x[a.cur], *xt = a.ws + mt.xt[a.cur];
+    const int i0 = t.i * S::T, j0 = t.j * S::T;
+    const _Float16 *x = a.ws + mt.x[a.cur];
     const _Float16 *pm = MODE == OR_MM_GRAM ? x : a.ws + (MODE == OR_MM_POLY ? mt.a : mt.b);
-    const _Float16 *qm = MODE == OR_MM_GRAM ? x : MODE == OR_MM_POLY ? pm : xt;
     const int kdim = MODE == OR_MM_GRAM ? lp : sp;
-    const int qrows = MODE >= OR_MM_STEP ? lp : sp;
-    const MmRows p = mm_rows(pm, kdim * 2, i0, sp, S::BM);
-    const MmRows q = mm_rows(qm, kdim * 2, j0, qrows, S::BN);
-    mm_f32x4 acc[S::FM][S::FN] = {};
-    mm_loop<S, false>(p, q, MmScale{}, 0, (kdim / 64 + 1) / 2, s0, s1, acc);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int r0 = i0 + wave / S::WN * (S::BM / S::WM) + (lane & 15);
-    const int c0 = j0 + wave % S::WN * (S::BN / S::WN) + (lane >> 4) * 4;
+    const MmRows p = mm_rows(pm, kdim * 2, i0, sp, S::T);
+    MmAcc<S> acc = {};
+    const int groups = (kdim + 127) / 128;
+    if constexpr (MODE == OR_MM_GRAM || MODE == OR_MM_POLY) {
+        const MmRows q = mm_rows(pm, kdim * 2, j0, sp, S::T);
+        mm_loop<S, false>(p, q, MmScale{}, 0, groups, mm_lds, nullptr, MmNoExtra{}, acc);
+    } else {
+        const MmCols q = {reinterpret_cast<const char *>(x + j0), static_cast<uint32_t>(lp) * 2u,
+                          static_cast<uint32_t>(j0) * 2u, sp};
+        mm_loop<S, false>(p, q, MmScale{}, 0, groups, mm_lds, nullptr, AddX{a.a, i0}, acc);
+    }
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    constexpr int TM = 16 * S::FM, TN = 16 * S::FN, PART = TM * TN * 2;
+    static_assert(PART * S::PARTS * S::WM * S::WN <= 2 * S::UNIT * (S::QUAD ? 4 : 1),
+                  "a wave's part of the tile fits its part of the buffers");
+    char *lds = mm_lds.own<S>(wave);
 #pragma unroll
-    for (int i = 0; i < S::FM; ++i) {
-        const int64_t r = r0 + 16 * i;
+    for (int b = 0; b < S::PARTS; ++b) {
 #pragma unroll
-        for (int j = 0; j < S::FN; ++j) {
-            const int64_t c = c0 + 16 * j;
-            mm_f32x4 v = acc[i][j];
-            f16x4 h;
-            if constexpr (MODE == OR_MM_GRAM || MODE == OR_MM_POLY) {
-                _Float16 *d = a.ws + (MODE == OR_MM_GRAM ? mt.a : mt.b);
-                if constexpr (MODE == OR_MM_GRAM) {
-                    const float inv = 1.0f / (mt.scale * mt.scale);   // a power of two
+        for (int i = 0; i < S::FM; ++i) {
+            const int rl = 16 * i + (lane & 15);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) h[k] = static_cast<_Float16>(v[k] * inv);
-                } else {
+            for (int j = 0; j < S::FN; ++j) {
+                const int cl = 16 * j + (lane >> 4) * 4;
+                const mm_f32x4 v = acc.c[b][i][j];
+                u16x4 h;
+                if constexpr (MODE == OR_MM_POLY) {
+                    const int64_t r = i0 + S::part_row(wave, i) + (lane & 15);
+                    const int64_t c = j0 + S::part_col(wave, b) + cl;
                     const f16x4 gm = *reinterpret_cast<const f16x4 *>(pm + r * sp + c);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        h[k] = static_cast<_Float16>(
-                            __fmaf_rn(a.c, v[k], a.b * static_cast<float>(gm[k])));
-                }
-                *reinterpret_cast<f16x4 *>(d + r * sp + c) = h;
-                if (t.i != t.j) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) d[(c + k) * sp + r] = h[k];
-                }
-            } else {
-                const f16x4 xv = *reinterpret_cast<const f16x4 *>(x + r * lp + c);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = __fmaf_rn(a.a, static_cast<float>(xv[k]), v[k]);
-                if constexpr (MODE == OR_MM_STEP) {
-                    _Float16 *dx = a.ws + mt.x[a.cur ^ 1], *dt = a.ws + mt.xt[a.cur ^ 1];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        h[k] = static_cast<_Float16>(v[k]);
-                        dt[(c + k) * sp + r] = h[k];
-                    }
-                    *reinterpret_cast<f16x4 *>(dx + r * lp + c) = h;
+                        h[k] = out_bits(__fmaf_rn(a.c, v[k], a.b * static_cast<float>(gm[k])),
+                                        false);
                 } else {
-                    const float mul = mt.out_mul / mt.scale;
-                    uint16_t *o = static_cast<uint16_t *>(a.out) + mt.off;
-                    if (r >= mt.s) continue;
-                    uint16_t ob[4];
+                    // (both factors are powers of two but for out_mul)
+                    const float mul = MODE == OR_MM_GRAM ? 1.0f / (mt.scale * mt.scale)
+                                      : MODE == OR_MM_LAST ? mt.out_mul / mt.scale : 1.0f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) ob[k] = out_bits(v[k] * mul, bf16 != 0);
-                    if (!mt.tr && mt.vec && c + 4 <= mt.l) {
-                        *reinterpret_cast<uint2 *>(o + r * mt.l + c) =
-                            make_uint2(ob[0] | (static_cast<uint32_t>(ob[1]) << 16),
-                                       ob[2] | (static_cast<uint32_t>(ob[3]) << 16));
-                    } else {
+                    for (int k = 0; k < 4; ++k)
+                        h[k] = out_bits(v[k] * mul, MODE == OR_MM_LAST && bf16);
+                }
+                *reinterpret_cast<u16x4 *>(lds + b * PART + out_at<TN>(rl, cl >> 3) +
+                                           (cl & 4) * 2) = h;
+            }
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    // by rows, and for what is symmetric (off the diagonal) or turned by columns
+    uint16_t *d;
+    int ld, ldt, rows = 0x7fffffff, cols = 0x7fffffff, al = 8;
+    bool by_rows = true, by_cols = false;
+    if constexpr (MODE == OR_MM_GRAM || MODE == OR_MM_POLY) {
+        d = reinterpret_cast<uint16_t *>(a.ws + (MODE == OR_MM_GRAM ? mt.a : mt.b));
+        ld = ldt = sp;
+        by_cols = t.i != t.j;
+    } else if constexpr (MODE == OR_MM_STEP) {
+        d = reinterpret_cast<uint16_t *>(a.ws + mt.x[a.cur ^ 1]);
+        ld = ldt = lp;
+    } else {
+        d = static_cast<uint16_t *>(a.out) + mt.off;
+        ld = mt.l;
+        ldt = mt.s;
+        rows = mt.s;
+        cols = mt.l;
+        al = mt.align;
+        by_rows = !mt.tr;
+        by_cols = !by_rows;
+    }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (c + k < mt.l) o[mt.tr ? (c + k) * mt.s + r : r * mt.l + c + k] = ob[k];
-                    }
+    for (int b = 0; b < S::PARTS; ++b) {
+        const char *part = lds + b * PART;
+        const int c0 = j0 + S::part_col(wave, b);
+        if (by_rows) {
+            constexpr int CH = TN / 8, RI = 64 / CH;    // chunks per row, rows per pass
+#pragma unroll
+            for (int k = 0; k < TM / RI; ++k) {
+                const int rl = k * RI + lane / CH, chunk = lane % CH;
+                const u16x8 v = out_row<TN>(part, rl, chunk);
+                const int r = i0 + S::part_row(wave, rl >> 4) + (rl & 15), c = c0 + 8 * chunk;
+                if (r < rows && c < cols)
+                    store8(d + static_cast<int64_t>(r) * ld + c, v, cols - c, al);
+            }
+        }
+        if (by_cols) {
+#pragma unroll
+            for (int j = 0; j < S::FN; ++j) {
+#pragma unroll
+                for (int k = 0; k < TM / 32; ++k) {
+                    const u16x8 v = out_col<TN>(part, 32 * k, 16 * j);
+                    const int c = c0 + 16 * j + (lane & 15);
+                    const int r = i0 + S::part_row(wave, 2 * k) + 8 * (lane >> 4);
+                    if (r < rows && c < cols)
+                        store8(d + static_cast<int64_t>(c) * ldt + r, v, rows - r, al);
                 }
             }
         }
@@ -322,9 +435,9 @@ hipError_t launch_ortho_cast(const OrArgs &a, int64_t n, gq_dtype dt, hipStream_
 hipError_t launch_ortho_mm(const OrArgs &a, int64_t n, int tile, OrMode mode, gq_dtype out,
                            hipStream_t st) {
     const int bf16 = out == GQ_BF16;
-    if (tile == 256) mm_shape<MmShape<256, 256, 2, 4>>(a, n, mode, bf16, st);
-    else if (tile == 128) mm_shape<MmShape<128, 128, 2, 2>>(a, n, mode, bf16, st);
-    else mm_shape<MmShape<64, 64, 2, 2>>(a, n, mode, bf16, st);
+    if (tile == 256) mm_shape<MmBig>(a, n, mode, bf16, st);
+    else if (tile == 128) mm_shape<MmMid>(a, n, mode, bf16, st);
+    else mm_shape<MmSmall>(a, n, mode, bf16, st);
     return hipGetLastError();
 }
 

@@ -686,7 +686,7 @@ typedef struct gq_ortho gq_ortho;
  *             array of 3 * steps finite floats.
  * eps         finite, >= 0 (a common choice is 1e-7).
  * out_mul     NULL (1), or a host array of n_mats finite floats.
- * Allocates device memory (about 8 bytes per element, and 4 per element of
+ * Allocates device memory (about 4 bytes per element, and 4 per element of
  * the square of each shorter side, sides rounded up to the tile) and
  * synchronizes.  Errors: GQ_ERR_INVALID, GQ_ERR_HIP.
  */
