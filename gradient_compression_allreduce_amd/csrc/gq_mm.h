@@ -72,8 +72,10 @@ struct MmShape {
     static constexpr int PARTS = QUAD ? 2 : 1;
     static constexpr int FM = T / WM / 16, FN = T / WN / 16 / PARTS;
     static constexpr int UNIT = QUAD ? 128 * MM_STEP : 2 * T * MM_STEP;  // bytes of one buffer
-    static constexpr int SB = T > 128 ? T / 16 : 8;              // bytes of a scale row
-    static constexpr int SCALES = 2 * SB * 256;                  // scale bytes of two steps
+    static constexpr int PLANES = QUAD ? 4 : 2;                  // of MX4 scales
+    // scale bytes of two steps: a plane for every one or two waves (with tiles
+    // of 64 the planes of two waves are written and not read)
+    static constexpr int SCALES = WM * WN / (T >= 128 ? 2 : 1) * 2048;
     // first row of instruction row i, and first column of block b
     static __device__ __forceinline__ int part_row(int wave, int i) {
         if (QUAD) return (i >> 2) * 128 + wave / WN * 64 + (i & 3) * 16;
@@ -177,90 +179,132 @@ __device__ __forceinline__ int mm_cols_at(uint32_t row, uint32_t col) {
     return row * (BN * 2) + (((col >> 4) ^ mm_turn<BN>(row)) << 5) + (col & 15) * 2;
 }
 
-// The lane's 8 elements of K (32 * kk + 8 * (lane / 16) on) of columns c16 +
-// 16 j + lane % 16.  The reads and the wait for them are one asm block: the
-// compiler takes the builtin for a read that may touch any load to LDS under
-// way, and would wait for all of them before each.
+// f[kk][j]: the lane's 8 elements of K (32 * kk + 8 * (lane / 16) on) of column
+// c16 + 16 j + lane % 16, c16 a multiple of 32.  The reads and the wait for
+// them are one asm block: the compiler takes the builtin for a read that may
+// touch any load to LDS under way, and would wait for all of them before each.
+// mm_turn does not change from a row to the 4th and the 32nd after it, so
+// those are at fixed distances, and column 16 is one bit away.
 template <int BN, int FN>
-__device__ __forceinline__ void mm_frag_cols(const char *lds, int c16, int kk, int lane,
-                                             mm_i32x4 (&f)[FN]) {
+__device__ __forceinline__ void mm_frag_cols(const char *lds, int c16, int lane,
+                                             mm_i32x4 (&f)[2][FN]) {
     const int q = lane & 15;
-    uint32_t at[2 * FN];
+    constexpr int R4 = 4 * BN * 2, R32 = 32 * BN * 2;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint32_t row = kk * 32 + (lane >> 4) * 8 + t * 4 + (q >> 2);
-            const char *p = lds + mm_cols_at<BN>(row, c16 + 16 * j + (q & 3) * 4);
-            at[2 * j + t] = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)p));
-        }
-    }
-    mm_u32x2 h[2 * FN];
-    static_assert(FN == 2 || FN == 4, "columns per wave");
-    if constexpr (FN == 4) {
-        asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %9\n\t"
-                     "ds_read_b64_tr_b16 %2, %10\n\tds_read_b64_tr_b16 %3, %11\n\t"
-                     "ds_read_b64_tr_b16 %4, %12\n\tds_read_b64_tr_b16 %5, %13\n\t"
-                     "ds_read_b64_tr_b16 %6, %14\n\tds_read_b64_tr_b16 %7, %15\n\t"
+    for (int j = 0; j < FN; j += 2) {
+        const char *p =
+            lds + mm_cols_at<BN>((lane >> 4) * 8 + (q >> 2), c16 + 16 * j + (q & 3) * 4);
+        const uint32_t a0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)p));
+        const uint32_t a1 = a0 ^ 32u;
+        mm_u32x2 h[8];
+        asm volatile("ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:%10\n\t"
+                     "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:%10\n\t"
+                     "ds_read_b64_tr_b16 %4, %8 offset:%11\n\tds_read_b64_tr_b16 %5, %8 offset:%12\n\t"
+                     "ds_read_b64_tr_b16 %6, %9 offset:%11\n\tds_read_b64_tr_b16 %7, %9 offset:%12\n\t"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&v"(h[0]), "=&v"(h[1]), "=&v"(h[2]), "=&v"(h[3]), "=&v"(h[4]),
                        "=&v"(h[5]), "=&v"(h[6]), "=&v"(h[7])
-                     : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5]),
-                       "v"(at[6]), "v"(at[7])
+                     : "v"(a0), "v"(a1), "n"(R4), "n"(R32), "n"(R32 + R4)
                      : "memory");
-    } else {
-        asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %5\n\t"
-                     "ds_read_b64_tr_b16 %2, %6\n\tds_read_b64_tr_b16 %3, %7\n\t"
-                     "s_waitcnt lgkmcnt(0)"
-                     : "=&v"(h[0]), "=&v"(h[1]), "=&v"(h[2]), "=&v"(h[3])
-                     : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
-                     : "memory");
-    }
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-        f[j] = __builtin_bit_cast(mm_i32x4, __builtin_shufflevector(h[2 * j], h[2 * j + 1], 0, 1, 2, 3));
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                f[kk][j + i] = __builtin_bit_cast(
+                    mm_i32x4, __builtin_shufflevector(h[4 * kk + 2 * i], h[4 * kk + 2 * i + 1], 0, 1,
+                                                      2, 3));
+    }
 }
 
-// Scale bytes of the MX4 rows of a tile: thread t looks after row t of the
-// P rows followed by the Q rows, sixteen bytes for each two steps.  In LDS
-// the byte of block b and row 16 i + r lies at (16 b + r) * SB + i (SB bytes
-// for the at most SB values of i), so a lane's scales of all its P (and Q)
-// operands of a step are neighbours, and the matrix instructions pick them by
-// number.  Rows and blocks outside take the nearest one inside: their codes
-// read as zeros.
-struct MmScale {
-    const uint8_t *p;      // the row's scales
-    const uint8_t *ahead;  // the same, or with nb < 16 any sixteen readable bytes
-    int64_t nb;
+// Scale bytes of a tile's MX4 rows, for two steps (sixteen blocks) at a time.
+// In LDS they lie in planes of up to 128 rows (P's, then Q's): the byte of
+// block b and row 16 i + r at ((b / 4 * 16 + r) * 4 + b % 4) * 8 + i.  The
+// scales of all a lane's operands of a half step are neighbours then, which
+// the matrix instructions pick by number, and the lanes of a wave read 512
+// bytes in a row.  A thread looks after four rows 16 apart and four blocks: it
+// loads four bytes of each row and turns them, so that it writes four words.
+// Rows and blocks outside take the nearest inside: their codes read as zeros.
+constexpr int MM_PLANE = 2048;
+
+struct MmScale {           // (the same for all lanes of a wave)
+    const uint8_t *base;   // scales of the wave's operand, first row of the tile
+    const uint8_t *ahead;  // the same; with nb < 16 any bytes that can be read
+    int32_t pitch;         // nb; with nb < 16: 0
+    int32_t rows;          // rows inside
+    int32_t nb;
+    int32_t row;           // the wave's first row
+    int32_t at;            // where it writes
+    // a lane's rows are row + r + 16 i, its blocks of a group block .. block + 3
+    static __device__ __forceinline__ int r(int tid) { return tid & 15; }
+    static __device__ __forceinline__ int block(int tid) { return (tid >> 4 & 3) * 4; }
 };
 
-// The sixteen bytes of a group, any number of blocks.
+// For operands of m and n rows (scales sp, sq), tile (i0, j0); any: four bytes
+// or more that can be read.
+template <typename S>
+__device__ __forceinline__ MmScale mm_scale_of(const uint8_t *sp, const uint8_t *sq, int64_t i0,
+                                               int64_t j0, int64_t m, int64_t n, int64_t nb,
+                                               const uint8_t *any) {
+    constexpr int QUADS = S::T >= 128 ? 2 : 1;            // waves per plane
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int plane = wave / QUADS, quad = wave % QUADS;
+    constexpr int HALF = S::PLANES / 2;
+    const bool isp = plane < HALF;
+    const int64_t first = isp ? i0 : j0, all = isp ? m : n;
+    MmScale s;
+    s.base = (isp ? sp : sq) + first * nb;
+    s.ahead = nb < 16 ? any : s.base;
+    s.pitch = nb < 16 ? 0 : static_cast<int32_t>(nb);
+    s.rows = static_cast<int32_t>(all - first < S::T ? all - first : S::T);
+    s.nb = static_cast<int32_t>(nb);
+    s.row = plane % HALF * 128 + quad * 64;
+    s.at = plane * MM_PLANE + quad * 4;
+    return s;
+}
+
+// The first group, any number of blocks: byte k of word i is row i, block k.
 __device__ __forceinline__ mm_u32x4 mm_scale_any(const MmScale &s, int group) {
-    const int64_t b = static_cast<int64_t>(group) * 16;
+    const int tid = threadIdx.x;
     mm_u32x4 v = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t at = b + i < s.nb ? b + i : s.nb - 1;
-        v[i >> 2] |= static_cast<uint32_t>(s.p[at]) << (8 * (i & 3));
+    for (int i = 0; i < 4; ++i) {
+        int row = s.row + s.r(tid) + 16 * i;
+        row = row < s.rows ? row : s.rows - 1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int b = group * 16 + s.block(tid) + k;
+            const int64_t at = static_cast<int64_t>(row) * s.nb + (b < s.nb ? b : s.nb - 1);
+            v[i] |= static_cast<uint32_t>(s.base[at]) << (8 * k);
+        }
     }
     return v;
 }
 
-// The same for a later group (so nb > 16): one load of the sixteen bytes that
-// end no later than the row, and, apart so that the load stays in flight,
-// their shift down to the group's first (0 but in the row's last group).  A
-// group past the row's end reads what nobody uses.
+// A later group (so nb > 16), whose loads stay in flight: words that end no
+// later than the row, to be shifted down to the group's blocks when used (0
+// but in the row's last group).  A group past the row's end, which the last
+// group loads ahead, reads what nobody uses.
 __device__ __forceinline__ mm_u32x4 mm_scale_load(const MmScale &s, int group) {
-    const int64_t b = static_cast<int64_t>(group) * 16, last = s.nb > 16 ? s.nb - 16 : 0;
+    const int tid = mm_tid();
+    int b = group * 16 + s.block(tid);
+    b = b < s.pitch - 4 ? b : s.pitch - 4;
+    b = b < 0 ? 0 : b;
     mm_u32x4 v;
-    __builtin_memcpy(&v, s.ahead + (b < last ? b : last), 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int row = s.row + s.r(tid) + 16 * i;
+        row = row < s.rows ? row : s.rows - 1;
+        uint32_t w;
+        __builtin_memcpy(&w, s.ahead + static_cast<uint32_t>(row * s.pitch + b), 4);
+        v[i] = w;
+    }
     return v;
 }
 
 __device__ __forceinline__ mm_u32x4 mm_scale_shift(mm_u32x4 v, const MmScale &s, int group) {
-    const int64_t late = static_cast<int64_t>(group) * 16 - (s.nb - 16);
-    const int by = late <= 0 ? 0 : late > 15 ? 15 : static_cast<int>(late);
-    return __builtin_bit_cast(mm_u32x4, __builtin_bit_cast(unsigned __int128, v) >> (8 * by));
+    const int late = group * 16 + s.block(mm_tid()) - (s.nb - 4);
+    const uint32_t by = late <= 0 ? 0u : late > 3 ? 24u : 8u * late;
+    return v >> by;
 }
 
 // The bytes of rows 16 i + r for i in [first, first + F) (first a multiple of
@@ -270,7 +314,7 @@ template <int F>
 struct MmBytes {
     uint32_t w[2];
     __device__ __forceinline__ void read(const char *row, int first) {
-        const mm_u32x2 v = *reinterpret_cast<const mm_u32x2 *>(row + (first & ~7));
+        const mm_u32x2 v = *reinterpret_cast<const mm_u32x2 *>(row);
         w[0] = v.x;
         w[1] = v.y;
         if (F <= 4) w[0] = (first & 4) ? v.y : v.x;
@@ -296,11 +340,6 @@ __device__ __forceinline__ void mm_each(F &f) {
     }
 }
 
-template <int AT>
-__device__ __forceinline__ void mm_put_byte(uint32_t lds, uint32_t byte) {
-    asm volatile("ds_write_b8 %0, %1 offset:%2" ::"v"(lds), "v"(byte), "n"(AT) : "memory");
-}
-
 // Waits until at most N of the wave's loads are under way.
 template <int N>
 __device__ __forceinline__ void mm_wait() {
@@ -317,24 +356,29 @@ __device__ __forceinline__ void mm_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Writes the thread's scale bytes of a group to half `half` of the scales.
-// (in asm: of most of these writes the compiler does not see which array they
-// go to, and would wait for every load to LDS first)
+// Writes the thread's scale bytes of a group to half `half` of the scales:
+// word k of block k, byte i of row i.  (in asm: of these writes the compiler
+// does not see which array they go to, and would wait for every load to LDS
+// first)
 template <typename S>
-__device__ __forceinline__ void mm_put_scale(const char *scale, int half, mm_u32x4 v) {
-    const int t = mm_tid();
-    if (2 * S::T < S::THREADS && t >= 2 * S::T) return;
-    const bool isp = t < S::T;
-    const int row = isp ? t : t - S::T;
-    const char *d = scale + half * S::SCALES + (isp ? 0 : S::SB * 256) + (row & 15) * S::SB +
-                    (row >> 4);
+__device__ __forceinline__ void mm_put_scale(const char *scale, int half, const MmScale &s,
+                                             mm_u32x4 v) {
+    // a 4 x 4 matrix of bytes turned: pairs of rows, then pairs of pairs
+    const uint32_t lo01 = __builtin_amdgcn_perm(v[1], v[0], 0x05010400u);
+    const uint32_t lo23 = __builtin_amdgcn_perm(v[3], v[2], 0x05010400u);
+    const uint32_t hi01 = __builtin_amdgcn_perm(v[1], v[0], 0x07030602u);
+    const uint32_t hi23 = __builtin_amdgcn_perm(v[3], v[2], 0x07030602u);
+    const uint32_t w0 = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+    const uint32_t w1 = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+    const uint32_t w2 = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+    const uint32_t w3 = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+    const int tid = mm_tid();
+    const char *d = scale + half * S::SCALES + s.at + ((tid >> 4 & 3) * 64 + (tid & 15) * 4) * 8;
     const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)d));
-    auto put = [&](auto bc) {
-        constexpr int b = decltype(bc)::value;
-        mm_put_byte<b * 16 * S::SB>(at, v[b >> 2] >> (8 * (b & 3)));
-    };
-    mm_each<16>(put);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    asm volatile("ds_write_b32 %0, %1\n\tds_write_b32 %0, %2 offset:8\n\t"
+                 "ds_write_b32 %0, %3 offset:16\n\tds_write_b32 %0, %4 offset:24\n\t"
+                 "s_waitcnt lgkmcnt(0)" ::"v"(at), "v"(w0), "v"(w1), "v"(w2), "v"(w3)
+                 : "memory");
 }
 
 // c[i][j] += p[i] q[j] over one half step.
@@ -362,6 +406,12 @@ __device__ __forceinline__ void mm_block(const mm_i32x4 (&p)[FM], const mm_i32x4
                     __builtin_bit_cast(mm_f16x8, q[j]), __builtin_bit_cast(mm_f16x8, p[i]), c[i][j],
                     0, 0, 0);
     }
+}
+
+template <int N>
+__device__ __forceinline__ void mm_pin(mm_f32x4 *c, std::integral_constant<int, N>) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(c[i]));
 }
 
 // The LDS of a work group.  The buffers are arrays of their own, so that the
@@ -430,30 +480,33 @@ __device__ __forceinline__ void mm_two(const MmRows &p, const Q &q, const MmScal
     };
     auto compute = [&](const char *s, int half, int t, int step) {
         extra(acc, s + T * MM_STEP, step, 0);
+        mm_i32x4 fq[2][S::FN];
+        if constexpr (!ROWS) mm_frag_cols<T, S::FN>(s + T * MM_STEP, rn, lane, fq);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            mm_i32x4 fp[S::FM], fq[S::FN];
+            mm_i32x4 fp[S::FM];
             MmBytes<S::FM> sp = {};
             MmBytes<S::FN> sq = {};
             if constexpr (MX) {
-                const int br = (8 * t + 4 * kk + (lane >> 4)) * 16 + (lane & 15);
-                sp.read(scale + (half * S::SCALES + br * S::SB), rm / 16);
-                sq.read(scale + (half * S::SCALES + S::SB * 256 + br * S::SB), rn / 16);
+                const int at = half * S::SCALES + (2 * t + kk) * 512 + (lane & 15) * 32 +
+                               (lane >> 4) * 8;
+                sp.read(scale + at, rm / 16);
+                sq.read(scale + at + MM_PLANE, rn / 16);
             }
             if constexpr (ROWS) {
 #pragma unroll
-                for (int j = 0; j < S::FN; ++j) fq[j] = mm_frag(s + T * MM_STEP, rn + 16 * j, kk, lane);
+                for (int j = 0; j < S::FN; ++j)
+                    fq[kk][j] = mm_frag(s + T * MM_STEP, rn + 16 * j, kk, lane);
             }
 #pragma unroll
             for (int i = 0; i < S::FM; ++i) fp[i] = mm_frag(s, rm + 16 * i, kk, lane);
-            if constexpr (!ROWS) mm_frag_cols<T, S::FN>(s + T * MM_STEP, rn, kk, lane, fq);
             __builtin_amdgcn_s_setprio(1);
-            mm_block<MX>(fp, fq, sp.w, sq.w[0], acc.c[0]);
+            mm_block<MX>(fp, fq[kk], sp.w, sq.w[0], acc.c[0]);
             __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    if constexpr (MX) mm_put_scale<S>(scale, 0, mm_scale_any(sc, group0));
+    if constexpr (MX) mm_put_scale<S>(scale, 0, sc, mm_scale_any(sc, group0));
     load(u.u0, 2 * group0);
     for (int g = 0; g < groups; ++g) {
         const int step = 2 * (group0 + g), half = g & 1;
@@ -472,7 +525,7 @@ __device__ __forceinline__ void mm_two(const MmRows &p, const Q &q, const MmScal
         // into the other half, whose last readers passed this group's first
         // barrier; written before the next barrier
         if constexpr (MX)
-            mm_put_scale<S>(scale, (g + 1) & 1, mm_scale_shift(v, sc, group0 + g + 1));
+            mm_put_scale<S>(scale, (g + 1) & 1, sc, mm_scale_shift(v, sc, group0 + g + 1));
     }
     mm_wait<0>();
     __syncthreads();
@@ -499,8 +552,9 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
         for (int kk = 0; kk < 2; ++kk) {
             if constexpr (MX) {
                 MmBytes<4> b;
-                const int br = (8 * t + 4 * kk + (lane >> 4)) * 16 + (lane & 15);
-                b.read(scale + (half * S::SCALES + br * S::SB), 8 * h + rm / 16);
+                const int at = half * S::SCALES + (2 * t + kk) * 512 + (lane & 15) * 32 +
+                               (lane >> 4) * 8;
+                b.read(scale + at + h * MM_PLANE, rm / 16);
                 sp[kk][0] = b.w[0];
             }
 #pragma unroll
@@ -513,19 +567,21 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
         for (int kk = 0; kk < 2; ++kk) {
             if constexpr (MX) {
                 MmBytes<2> b;
-                const int br = (8 * t + 4 * kk + (lane >> 4)) * 16 + (lane & 15);
-                b.read(scale + (half * S::SCALES + S::SB * 256 + br * S::SB), 8 * h + rn / 16);
+                const int at = half * S::SCALES + (2 * t + kk) * 512 + (lane & 15) * 32 +
+                               (lane >> 4) * 8;
+                b.read(scale + at + (2 + h) * MM_PLANE, rn / 16);
                 sq[h][kk] = b.w[0];
             }
             if constexpr (ROWS) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) fq[h][kk][j] = mm_frag(s, rn + 16 * j, kk, lane);
-            } else {
-                mm_frag_cols<128, 2>(s, rn, kk, lane, fq[h][kk]);
             }
         }
+        if constexpr (!ROWS) mm_frag_cols<128, 2>(s, rn, lane, fq[h]);
     };
-    // quadrant (h, b): the instruction rows 4 h .. 4 h + 3 of block b
+    // quadrant (h, b): the instruction rows 4 h .. 4 h + 3 of block b.  (The
+    // sums are marked as changed: matrix instructions touch no memory, and
+    // across a branch the compiler would move them past the next barrier.)
     auto quadrant = [&](int h, int b) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -533,6 +589,8 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
             mm_f32x4(&c)[4][2] = *reinterpret_cast<mm_f32x4(*)[4][2]>(&acc.c[b][4 * h]);
             mm_block<MX>(fp[kk], fq[b][kk], sp[kk], sq[b][kk], c);
         }
+        if constexpr (!std::is_same<X, MmNoExtra>::value)
+            mm_pin(&acc.c[b][4 * h][0], std::integral_constant<int, 8>{});
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -565,7 +623,7 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
         quadrant(1, 1);
         quadrant(1, 0);
     };
-    if constexpr (MX) mm_put_scale<S>(scale, 0, mm_scale_any(sc, group0));
+    if constexpr (MX) mm_put_scale<S>(scale, 0, sc, mm_scale_any(sc, group0));
     const int first = 2 * group0;
     load_p(u.u0, first, 0);
     load_q(u.u1, first, 0);
@@ -583,7 +641,7 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
         // into the other half, whose last readers passed this group's first
         // barrier; written before the next barrier
         if constexpr (MX)
-            mm_put_scale<S>(scale, (g + 1) & 1, mm_scale_shift(v, sc, group0 + g + 1));
+            mm_put_scale<S>(scale, (g + 1) & 1, sc, mm_scale_shift(v, sc, group0 + g + 1));
     }
     mm_wait<0>();
     __syncthreads();

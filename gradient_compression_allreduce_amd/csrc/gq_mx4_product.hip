@@ -74,14 +74,7 @@ __global__ __launch_bounds__(S::THREADS) void k_mx4_product(const MxPArgs a) {
     const uint32_t bytes = static_cast<uint32_t>(a.nb) * MX_BYTES;
     const MmRows p = mm_rows(a.a, bytes, i0, a.m, S::T);
     const MmRows q = mm_rows(a.b, bytes, j0, a.n, S::T);
-    MmScale sc = {nullptr, nullptr, a.nb};
-    {
-        const int r = threadIdx.x;
-        const int64_t pr = i0 + r < a.m ? i0 + r : a.m - 1;
-        const int64_t qr = j0 + r - S::T < a.n ? j0 + r - S::T : a.n - 1;
-        sc.p = r < S::T ? a.sa + pr * a.nb : a.sb + qr * a.nb;
-        sc.ahead = a.nb > 16 ? sc.p : a.a;
-    }
+    const MmScale sc = mm_scale_of<S>(a.sa, a.sb, i0, j0, a.m, a.n, a.nb, a.a);
     MmAcc<S> acc = {};
     const int all = static_cast<int>((a.nb + 15) / 16);
     const int k0 = split * a.groups;
