@@ -20,8 +20,10 @@
 //     on the global side, in which chunk a lane asks for.
 //   * The instruction's first operand is Q and its second P: a lane then
 //     holds four consecutive columns of one row of C.
-//   * mm_loop (tiles of 128 and 64): two buffers of a step each; two or more
-//     work groups per compute unit cover each other's waits.
+//   * mm_two (tiles of 128 and 64): two buffers of a step each; two or five
+//     work groups per compute unit cover each other's waits.  On a ring of
+//     four buffers instead (tiles of 64 where there are few of them and latency
+//     counts) the loads run three steps ahead.
 //   * mm_quad (tiles of 256, one work group of eight waves per compute unit):
 //     each of P and Q is two halves of 128 rows with buffers of their own, and
 //     the waves go through the four quadrants of C together, so a half's
@@ -64,10 +66,12 @@ __device__ __forceinline__ int mm_tid() {
 // Tile shapes: T x T of C by WM x WN waves.  A wave's part of C is PARTS
 // blocks of FM x FN matrix instructions; block b, instruction row i and the
 // lane's row r (0 .. 15) are at part_row / part_col of the tile.
-template <int T_, int WM_, int WN_>
+// RING: four buffers instead of two.
+template <int T_, int WM_, int WN_, bool RING_ = false>
 struct MmShape {
     static constexpr int T = T_, WM = WM_, WN = WN_;
-    static constexpr bool QUAD = T == 256;
+    static constexpr bool QUAD = T == 256, RING = RING_;
+    static constexpr int BUFFERS = QUAD ? 8 : RING ? 4 : 2;
     static constexpr int THREADS = 64 * WM * WN;
     static constexpr int PARTS = QUAD ? 2 : 1;
     static constexpr int FM = T / WM / 16, FN = T / WN / 16 / PARTS;
@@ -89,6 +93,7 @@ struct MmShape {
 using MmBig = MmShape<256, 2, 4>;
 using MmMid = MmShape<128, 2, 2>;
 using MmSmall = MmShape<64, 2, 2>;
+using MmFew = MmShape<64, 2, 2, true>;
 
 // Rows [row0, row0 + tile) of an operand, `bytes` per row, as a buffer.
 struct MmRows {
@@ -416,12 +421,12 @@ __device__ __forceinline__ void mm_pin(mm_f32x4 *c, std::integral_constant<int, 
 
 // The LDS of a work group.  The buffers are arrays of their own, so that the
 // compiler sees that the loads under way do not touch what is being read.
-// (Tiles of 128 and 64 use the first two.)
+// (Tiles of 256 use all, a ring the first four, the others the first two.)
 #define MM_LDS(S)                                                                     \
     __shared__ __align__(128) char mm_u0[S::UNIT];                                    \
     __shared__ __align__(128) char mm_u1[S::UNIT];                                    \
-    __shared__ __align__(128) char mm_u2[S::QUAD ? S::UNIT : 16];                     \
-    __shared__ __align__(128) char mm_u3[S::QUAD ? S::UNIT : 16];                     \
+    __shared__ __align__(128) char mm_u2[S::BUFFERS > 2 ? S::UNIT : 16];              \
+    __shared__ __align__(128) char mm_u3[S::BUFFERS > 2 ? S::UNIT : 16];              \
     __shared__ __align__(128) char mm_u4[S::QUAD ? S::UNIT : 16];                     \
     __shared__ __align__(128) char mm_u5[S::QUAD ? S::UNIT : 16];                     \
     __shared__ __align__(128) char mm_u6[S::QUAD ? S::UNIT : 16];                     \
@@ -437,12 +442,12 @@ struct MmLds {
         uint32_t at = 0;
         char *const u[8] = {u0, u1, u2, u3, u4, u5, u6, u7};
 #pragma unroll
-        for (int k = 0; k < (S::QUAD ? 8 : 2); ++k) {
+        for (int k = 0; k < S::BUFFERS; ++k) {
             uint32_t a = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)u[k]));
             asm("" : "+s"(a));
-            if (k == (S::QUAD ? wave : wave >> 1)) at = a;
+            if (k == (S::BUFFERS > 2 ? wave : wave >> 1)) at = a;
         }
-        if (!S::QUAD) at += (wave & 1) * (S::UNIT / 2);
+        if (S::BUFFERS == 2) at += (wave & 1) * (S::UNIT / 2);
         return (char *)reinterpret_cast<mm_lds_void *>(at);
     }
 };
@@ -507,25 +512,51 @@ __device__ __forceinline__ void mm_two(const MmRows &p, const Q &q, const MmScal
         }
     };
     if constexpr (MX) mm_put_scale<S>(scale, 0, sc, mm_scale_any(sc, group0));
-    load(u.u0, 2 * group0);
-    for (int g = 0; g < groups; ++g) {
-        const int step = 2 * (group0 + g), half = g & 1;
-        mm_u32x4 v;
-        mm_wait<0>();
-        mm_barrier();
-        if constexpr (MX) v = mm_scale_load(sc, group0 + g + 1);
-        load(u.u1, step + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(u.u0, half, 0, step);
-        mm_wait<0>();
-        mm_barrier();
-        load(u.u0, step + 2);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(u.u1, half, 1, step + 1);
-        // into the other half, whose last readers passed this group's first
-        // barrier; written before the next barrier
-        if constexpr (MX)
-            mm_put_scale<S>(scale, (g + 1) & 1, sc, mm_scale_shift(v, sc, group0 + g + 1));
+    mm_u32x4 v;
+    if constexpr (S::RING) {
+        // four steps (two groups of scales) a round; an odd last group is
+        // followed by steps of zeros, so parts of K must be even
+        constexpr int L = 2 * T * 8 / S::THREADS;   // a wave's loads per step
+        const int first = 2 * group0;
+        load(u.u0, first);
+        load(u.u1, first + 1);
+        load(u.u2, first + 2);
+        auto one = [&](char *now, char *next, int step, int half, int t) {
+            mm_wait<2 * L>();
+            mm_barrier();
+            if (MX && t == 0) v = mm_scale_load(sc, step / 2 + 1);
+            load(next, step + 3);
+            __builtin_amdgcn_sched_barrier(0);
+            compute(now, half, t, step);
+            // into the other half, whose last readers passed this group's
+            // first barrier; written before the next barrier
+            if (MX && t == 1) mm_put_scale<S>(scale, half ^ 1, sc, mm_scale_shift(v, sc, step / 2 + 1));
+        };
+        for (int g = 0; g < groups; g += 2) {
+            const int step = first + 2 * g;
+            one(u.u0, u.u3, step, 0, 0);
+            one(u.u1, u.u0, step + 1, 0, 1);
+            one(u.u2, u.u1, step + 2, 1, 0);
+            one(u.u3, u.u2, step + 3, 1, 1);
+        }
+    } else {
+        load(u.u0, 2 * group0);
+        for (int g = 0; g < groups; ++g) {
+            const int step = 2 * (group0 + g), half = g & 1;
+            mm_wait<0>();
+            mm_barrier();
+            if constexpr (MX) v = mm_scale_load(sc, group0 + g + 1);
+            load(u.u1, step + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            compute(u.u0, half, 0, step);
+            mm_wait<0>();
+            mm_barrier();
+            load(u.u0, step + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            compute(u.u1, half, 1, step + 1);
+            if constexpr (MX)
+                mm_put_scale<S>(scale, (g + 1) & 1, sc, mm_scale_shift(v, sc, group0 + g + 1));
+        }
     }
     mm_wait<0>();
     __syncthreads();

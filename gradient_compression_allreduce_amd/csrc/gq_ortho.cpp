@@ -17,9 +17,10 @@ struct gq_ortho {
     int64_t n = 0;                 // elements of the flat buffers
     int64_t n_mats = 0;
     int32_t steps = 0;
-    int32_t tile = 0;
+    int32_t tile_g = 0, tile_x = 0;   // of G and Q, and of X
     float eps = 0.0f;
-    std::vector<float> coef;       // [steps][3]
+    OrSteps coef = {};
+    bool small = false;            // every matrix fits one work group
     int64_t ws_bytes = 0;
     char *d_mem = nullptr;         // one allocation: workspace, partials, tables
     _Float16 *d_ws = nullptr;
@@ -91,23 +92,40 @@ std::vector<OrTile> product_tiles(const std::vector<OrMat> &mats, int tile, bool
     return deal(tiles, runs);
 }
 
-// The plan's tile: the largest whose s x l products still give every compute
-// unit a tile.
-int choose_tile(const int64_t *rows, const int64_t *cols, int64_t n) {
+// Tiles of the products: `s` x `s` of G and Q (their upper halves), or s x l
+// of X.  The largest that still gives the device enough of them: one work
+// group per compute unit with tiles of 256, two with tiles of 128.
+int choose_tile(const int64_t *rows, const int64_t *cols, int64_t n, bool gram) {
     for (const int t : {256, 128}) {
         int64_t tiles = 0;
-        for (int64_t i = 0; i < n; ++i)
-            tiles += ((rows[i] + t - 1) / t) * ((cols[i] + t - 1) / t);
-        if (tiles >= kCus) return t;
+        for (int64_t i = 0; i < n; ++i) {
+            const int64_t s = (std::min(rows[i], cols[i]) + t - 1) / t;
+            const int64_t l = (std::max(rows[i], cols[i]) + t - 1) / t;
+            tiles += gram ? s * (s + 1) / 2 : s * l;
+        }
+        if (tiles >= (t == 256 ? kCus : 2 * kCus)) return t;
     }
     return 64;
+}
+
+// Whether every matrix fits one work group.  64 x 147 (fp32, momentum, five
+// steps): 26 us in one launch, 64 us in 17 of tiles, which the host takes 53 us
+// to issue.  (64 x 1024 would take 141 us in one work group's LDS: tiles.)
+bool fits_small(const int64_t *rows, const int64_t *cols, int64_t n) {
+    for (int64_t i = 0; i < n; ++i)
+        if (std::min(rows[i], cols[i]) > OR_SMALL_S || std::max(rows[i], cols[i]) > OR_SMALL_L)
+            return false;
+    return true;
 }
 
 gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_rows,
                        const int64_t *h_cols, int64_t n_mats, int32_t steps, const float *coef,
                        float eps, const float *out_mul, gq_ortho **out) {
     std::vector<OrMat> mats(static_cast<size_t>(n_mats));
-    const int tile = choose_tile(h_rows, h_cols, n_mats);
+    const bool small = fits_small(h_rows, h_cols, n_mats);
+    const int tile_g = small ? 64 : choose_tile(h_rows, h_cols, n_mats, true);
+    const int tile_x = small ? 64 : choose_tile(h_rows, h_cols, n_mats, false);
+    const int tile = std::max(tile_g, tile_x);      // what the sides are rounded up to
     std::vector<OrTile> tab[OR_TABLES];
     int64_t at = 0, parts = 0;
     for (int64_t i = 0; i < n_mats; ++i) {
@@ -124,6 +142,7 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
         m.scale = std::exp2(std::round(0.5f * std::log2(static_cast<float>(m.l))));
         m.out_mul = out_mul ? out_mul[i] : 1.0f;
         m.align = (m.off | m.cols) % 8 == 0 ? 8 : (m.off | m.cols) % 4 == 0 ? 4 : 1;
+        if (small) continue;    // neither workspace nor tables
         const int64_t xl = static_cast<int64_t>(m.sp) * m.lp, al = static_cast<int64_t>(m.sp) * m.sp;
         for (int k = 0; k < 2; ++k) {
             m.x[k] = at;
@@ -148,14 +167,19 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
             return arg_fail(GQ_ERR_INVALID, op, "more than %lld tiles: too many elements",
                             static_cast<long long>(kMaxTiles));
     }
-    tab[OR_GRAM] = product_tiles(mats, tile, true);
-    tab[OR_X] = product_tiles(mats, tile, false);
+    if (!small) {
+        tab[OR_GRAM] = product_tiles(mats, tile_g, true);
+        tab[OR_X] = product_tiles(mats, tile_x, false);
+    }
     gq_ortho *P = new gq_ortho;
     P->steps = steps;
-    P->tile = tile;
+    P->tile_g = tile_g;
+    P->tile_x = tile_x;
     P->eps = eps;
     static const float quintic[3] = {3.4445f, -4.7750f, 2.0315f};
-    for (int32_t k = 0; k < 3 * steps; ++k) P->coef.push_back(coef ? coef[k] : quintic[k % 3]);
+    P->coef.steps = steps;
+    for (int32_t k = 0; k < 3 * steps; ++k) P->coef.coef[k] = coef ? coef[k] : quintic[k % 3];
+    P->small = small;
     P->n_mats = n_mats;
     P->n = h_off[n_mats - 1] + h_rows[n_mats - 1] * h_cols[n_mats - 1];
     hipError_t e = hipGetDevice(&P->device);
@@ -259,7 +283,7 @@ gq_status gq_ortho_info(const gq_ortho *p, int64_t *n, int64_t *n_mats, int64_t 
     if (n) *n = p->n;
     if (n_mats) *n_mats = p->n_mats;
     if (bytes) *bytes = p->ws_bytes;
-    if (tile) *tile = p->tile;
+    if (tile) *tile = p->tile_x;
     return arg_ok();
 }
 
@@ -298,22 +322,24 @@ gq_status gq_ortho_step(gq_ortho *p, const void *g, gq_dtype dt, float in_mul, f
     a.mu = mu;
     a.eps = p->eps;
     a.nesterov = nesterov != 0;
+    if (p->small)
+        return arg_launch(op, launch_ortho_small(a, p->coef, p->n_mats, dt, out_dt, st));
     a.tiles = p->d_tiles[OR_NORM];
     hipError_t e = launch_ortho_norm(a, p->n_tiles[OR_NORM], dt, st);
     a.tiles = p->d_tiles[OR_CAST];
     if (e == hipSuccess) e = launch_ortho_cast(a, p->n_tiles[OR_CAST], dt, st);
     for (int32_t k = 0; k < p->steps && e == hipSuccess; ++k) {
-        a.a = p->coef[3 * k];
-        a.b = p->coef[3 * k + 1];
-        a.c = p->coef[3 * k + 2];
+        a.a = p->coef.coef[3 * k];
+        a.b = p->coef.coef[3 * k + 1];
+        a.c = p->coef.coef[3 * k + 2];
         a.cur = k & 1;
         a.tiles = p->d_tiles[OR_GRAM];
-        e = launch_ortho_mm(a, p->n_tiles[OR_GRAM], p->tile, OR_MM_GRAM, out_dt, st);
+        e = launch_ortho_mm(a, p->n_tiles[OR_GRAM], p->tile_g, OR_MM_GRAM, out_dt, st);
         if (e == hipSuccess)
-            e = launch_ortho_mm(a, p->n_tiles[OR_GRAM], p->tile, OR_MM_POLY, out_dt, st);
+            e = launch_ortho_mm(a, p->n_tiles[OR_GRAM], p->tile_g, OR_MM_POLY, out_dt, st);
         a.tiles = p->d_tiles[OR_X];
         if (e == hipSuccess)
-            e = launch_ortho_mm(a, p->n_tiles[OR_X], p->tile,
+            e = launch_ortho_mm(a, p->n_tiles[OR_X], p->tile_x,
                                 k + 1 < p->steps ? OR_MM_STEP : OR_MM_LAST, out_dt, st);
     }
     return arg_launch(op, e);

@@ -48,13 +48,23 @@ struct OrArgs {
     int32_t cur;        // which of x[] is read
 };
 
+// The coefficients (a, b, c) of every step.
+struct OrSteps {
+    float coef[3 * GQ_ORTHO_MAX_STEPS];
+    int32_t steps;
+};
+
 enum OrTable { OR_NORM = 0, OR_CAST = 1, OR_GRAM = 2, OR_X = 3, OR_TABLES = 4 };
-enum OrMode { OR_MM_GRAM = 0, OR_MM_POLY = 1, OR_MM_STEP = 2, OR_MM_LAST = 3 };
+enum OrMode { OR_MM_GRAM = 0, OR_MM_POLY = 1, OR_MM_STEP = 2, OR_MM_LAST = 3, OR_MM_LAST_BF16 = 4 };
 
 constexpr int OR_CAST_TILE = 64;
 
 hipError_t launch_ortho_norm(const OrArgs &a, int64_t n, gq_dtype dt, hipStream_t s);
 hipError_t launch_ortho_cast(const OrArgs &a, int64_t n, gq_dtype dt, hipStream_t s);
+// n matrices with s <= OR_SMALL_S and l <= OR_SMALL_L, one work group each.
+constexpr int OR_SMALL_S = 64, OR_SMALL_L = 256;
+hipError_t launch_ortho_small(const OrArgs &a, const OrSteps &st, int64_t n, gq_dtype dt,
+                              gq_dtype out, hipStream_t s);
 hipError_t launch_ortho_mm(const OrArgs &a, int64_t n, int tile, OrMode mode, gq_dtype out,
                            hipStream_t s);
 

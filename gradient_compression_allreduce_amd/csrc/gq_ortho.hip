@@ -3,6 +3,7 @@
 //   X <- u / (|u|_F + eps);  G = X X^T;  Q = b G + c G G;  X <- a X + Q X.
 //   k_ortho_norm  momentum, and each matrix's sum of squares in binary64;
 //   k_ortho_cast  X in fp16 from u and the sum of squares;
+//   k_ortho_small the whole update of a matrix that fits one work group's LDS;
 //   k_ortho_mm    the three products of a step over the tiles of all
 //                 matrices together (gq_mm.h: the tile loop), the polynomial
 //                 and the update in its epilogue.
@@ -27,6 +28,11 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int OR_BLOCK = 256;
+// Launches of up to this many tiles of 64 run on a ring of four buffers, two
+// work groups per compute unit, longer ones on two buffers and five work
+// groups.  One 1024 x 1024 matrix (136 and 256 tiles, five steps): 162 us on
+// the ring, 196 on two buffers; one 2048 x 2048 (528 and 1024): 484 and 419.
+constexpr int64_t OR_FEW = 512;
 
 struct bf16_t { uint16_t bits; };
 
@@ -279,8 +285,9 @@ struct AddX {
 //      OR_MM_STEP: X <- a X + Q X     (K: rows of X)
 //      OR_MM_LAST: the same into the caller's output
 template <typename S, int MODE>
-__global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a, int bf16) {
+__global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a) {
     MM_LDS(S);
+    constexpr bool LAST = MODE >= OR_MM_LAST;
     const OrTile t = a.tiles[blockIdx.x];
     if (t.mat < 0) return;
     const OrMat &mt = a.mats[t.mat];
@@ -302,7 +309,7 @@ __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a, int bf1
     }
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     constexpr int TM = 16 * S::FM, TN = 16 * S::FN, PART = TM * TN * 2;
-    static_assert(PART * S::PARTS * S::WM * S::WN <= 2 * S::UNIT * (S::QUAD ? 4 : 1),
+    static_assert(PART * S::PARTS * S::WM * S::WN <= S::UNIT * S::BUFFERS,
                   "a wave's part of the tile fits its part of the buffers");
     char *lds = mm_lds.own<S>(wave);
 #pragma unroll
@@ -326,10 +333,10 @@ __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a, int bf1
                 } else {
                     // (both factors are powers of two but for out_mul)
                     const float mul = MODE == OR_MM_GRAM ? 1.0f / (mt.scale * mt.scale)
-                                      : MODE == OR_MM_LAST ? mt.out_mul / mt.scale : 1.0f;
+                                      : LAST ? mt.out_mul / mt.scale : 1.0f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        h[k] = out_bits(v[k] * mul, MODE == OR_MM_LAST && bf16);
+                        h[k] = out_bits(v[k] * mul, MODE == OR_MM_LAST_BF16);
                 }
                 *reinterpret_cast<u16x4 *>(lds + b * PART + out_at<TN>(rl, cl >> 3) +
                                            (cl & 4) * 2) = h;
@@ -347,7 +354,7 @@ __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a, int bf1
         d = reinterpret_cast<uint16_t *>(a.ws + (MODE == OR_MM_GRAM ? mt.a : mt.b));
         ld = ldt = sp;
         by_cols = t.i != t.j;
-    } else if constexpr (MODE == OR_MM_STEP) {
+    } else if constexpr (!LAST) {
         d = reinterpret_cast<uint16_t *>(a.ws + mt.x[a.cur ^ 1]);
         ld = ldt = lp;
     } else {
@@ -391,14 +398,198 @@ __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a, int bf1
     }
 }
 
+// ---- small matrices ----------------------------------------------------------------
+// All steps of a matrix with s <= 64 and l <= LP in one work group of eight
+// waves, X, G and Q in LDS: one launch instead of 2 + 3 T, which for such
+// sizes are all latency (64 x 147, five steps: see the figures at the rule in
+// gq_ortho.cpp).  The arithmetic is that of the tiled kernels.
+//   G and Q: each wave takes two of the sixteen 16 x 16 blocks;
+//   X: each wave takes every eighth block of 16 columns, and as a block of
+//   a X + Q X needs those columns alone, writes it in place.
+// In LDS the 16-byte chunks of row r lie at chunk ^ (r & 7).
+__device__ __forceinline__ int sm_at(int r, int col, int pitch) {
+    return r * pitch * 2 + (((col >> 3) ^ (r & 7)) << 4) + (col & 7) * 2;
+}
+
+// Elements k0 + 8 * (lane / 16) on of row r16 + lane % 16.
+__device__ __forceinline__ mm_f16x8 sm_row(const char *m, int r16, int k0, int pitch) {
+    const int lane = threadIdx.x & 63;
+    return *reinterpret_cast<const mm_f16x8 *>(
+        m + sm_at(r16 + (lane & 15), k0 + 8 * (lane >> 4), pitch));
+}
+
+// Elements k0 + 8 * (lane / 16) on of column c16 + lane % 16.
+__device__ __forceinline__ mm_f16x8 sm_col(const char *m, int c16, int k0, int pitch) {
+    const int lane = threadIdx.x & 63, q = lane & 15;
+    mm_i16x4 h[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const char *p = m + sm_at(k0 + 8 * (lane >> 4) + 4 * t + (q >> 2), c16 + 4 * (q & 3), pitch);
+        h[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_i16x4 *)p);
+    }
+    return __builtin_bit_cast(mm_f16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <typename T, int LP>
+__global__ __launch_bounds__(512) void k_ortho_small(const OrArgs a, const OrSteps st, int bf16) {
+    __shared__ __align__(128) char xs[64 * LP * 2];
+    __shared__ __align__(128) char gs[64 * 64 * 2];
+    __shared__ __align__(128) char qs[64 * 64 * 2];
+    __shared__ double sh[8];
+    const OrMat &mt = a.mats[blockIdx.x];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lp = (mt.l + 63) & ~63;           // columns in use, a multiple of 64
+    const int rows = mt.rows, cols = mt.cols;
+    const T *g = static_cast<const T *>(a.g) + mt.off;
+    float *mom = a.m ? a.m + mt.off : nullptr;
+    // momentum and the sum of squares.  The matrix as it lies, 64 x LP or LP x
+    // 64, is cut into rows of 64 elements, which the waves take in turn; u
+    // stays in registers.
+    constexpr int PER = LP / 8;                 // elements per lane
+    const int across = mt.tr ? 1 : LP / 64;     // rows of 64 elements per row
+    float u[PER];
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int piece = i * 8 + wave, r = piece / across, c = piece % across * 64 + lane;
+        u[i] = 0.0f;
+        if (r < rows && c < cols) {
+            const int e = r * cols + c;
+            u[i] = __fmul_rn(to_f32(g[e]), a.in_mul);
+            if (mom) {
+                const float m = __fadd_rn(__fmul_rn(a.mu, mom[e]), u[i]);
+                mom[e] = m;
+                u[i] = a.nesterov ? __fadd_rn(u[i], __fmul_rn(a.mu, m)) : m;
+            }
+        }
+        sum += static_cast<double>(u[i]) * static_cast<double>(u[i]);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    if (lane == 0) sh[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += sh[i];
+    const double mul = static_cast<double>(mt.scale) /
+                       (__dsqrt_rn(sum) + static_cast<double>(a.eps));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int piece = i * 8 + wave, r = piece / across, c = piece % across * 64 + lane;
+        // zeros around the matrix, whatever the norm
+        const bool in = r < rows && c < cols;
+        const _Float16 h = static_cast<_Float16>(in ? static_cast<float>(u[i] * mul) : 0.0f);
+        const int xr = mt.tr ? c : r, xc = mt.tr ? r : c;
+        if (xc < lp) *reinterpret_cast<_Float16 *>(xs + sm_at(xr, xc, lp)) = h;
+    }
+    __syncthreads();
+    const float inv = 1.0f / (mt.scale * mt.scale);     // a power of two
+    const int bi = (wave >> 1) * 16, bj = (wave & 1) * 32;   // the wave's blocks of G and Q
+    for (int k = 0; k < st.steps; ++k) {
+        const float ca = st.coef[3 * k], cb = st.coef[3 * k + 1], cc = st.coef[3 * k + 2];
+        mm_f32x4 acc[2] = {};
+        for (int k1 = 0; k1 < lp; k1 += 64) {
+            mm_f16x8 p[2], q[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                p[h] = sm_row(xs, bi, k1 + 32 * h, lp);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) q[h][j] = sm_row(xs, bj + 16 * j, k1 + 32 * h, lp);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[h][j], p[h], acc[j], 0, 0, 0);
+        }
+        const int r = bi + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = bj + 16 * j + (lane >> 4) * 4;
+            f16x4 h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = static_cast<_Float16>(acc[j][i] * inv);
+            *reinterpret_cast<f16x4 *>(gs + sm_at(r, c, 64)) = h;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[j] = mm_f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k0 = 0; k0 < 64; k0 += 32) {
+            const mm_f16x8 p = sm_row(gs, bi, k0, 64);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(sm_row(gs, bj + 16 * j, k0, 64), p,
+                                                                acc[j], 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = bj + 16 * j + (lane >> 4) * 4;
+            const f16x4 gm = *reinterpret_cast<const f16x4 *>(gs + sm_at(r, c, 64));
+            f16x4 h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                h[i] = static_cast<_Float16>(__fmaf_rn(cc, acc[j][i], cb * static_cast<float>(gm[i])));
+            *reinterpret_cast<f16x4 *>(qs + sm_at(r, c, 64)) = h;
+        }
+        __syncthreads();
+        const bool last = k + 1 == st.steps;
+        for (int c16 = wave * 16; c16 < lp; c16 += 128) {
+            mm_f32x4 x[4] = {};
+#pragma unroll
+            for (int k0 = 0; k0 < 64; k0 += 32) {
+                const mm_f16x8 q = sm_col(xs, c16, k0, lp);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q, sm_row(qs, 16 * i, k0, 64), x[i],
+                                                                  0, 0, 0);
+            }
+            const int c = c16 + (lane >> 4) * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int xr = 16 * i + (lane & 15);
+                f16x4 *px = reinterpret_cast<f16x4 *>(xs + sm_at(xr, c, lp));
+                const f16x4 xv = *px;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[i][e] = __fmaf_rn(ca, static_cast<float>(xv[e]), x[i][e]);
+                if (!last) {
+                    f16x4 h;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = static_cast<_Float16>(x[i][e]);
+                    *px = h;
+                } else if (xr < mt.s) {
+                    const float om = mt.out_mul / mt.scale;
+                    uint16_t *o = static_cast<uint16_t *>(a.out) + mt.off;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < mt.l)
+                            o[mt.tr ? (c + e) * mt.s + xr : xr * mt.l + c + e] =
+                                out_bits(x[i][e] * om, bf16 != 0);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T>
+void small_typed(const OrArgs &a, const OrSteps &st, int64_t n, int bf16, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(n));
+    hipLaunchKernelGGL((k_ortho_small<T, OR_SMALL_L>), grid, dim3(512), 0, s, a, st, bf16);
+}
+
 template <typename S>
-void mm_shape(const OrArgs &a, int64_t n, OrMode mode, int bf16, hipStream_t st) {
+void mm_shape(const OrArgs &a, int64_t n, OrMode mode, bool bf16, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(n)), blk(S::THREADS);
     switch (mode) {
-    case OR_MM_GRAM: hipLaunchKernelGGL((k_ortho_mm<S, OR_MM_GRAM>), grid, blk, 0, st, a, bf16); break;
-    case OR_MM_POLY: hipLaunchKernelGGL((k_ortho_mm<S, OR_MM_POLY>), grid, blk, 0, st, a, bf16); break;
-    case OR_MM_STEP: hipLaunchKernelGGL((k_ortho_mm<S, OR_MM_STEP>), grid, blk, 0, st, a, bf16); break;
-    case OR_MM_LAST: hipLaunchKernelGGL((k_ortho_mm<S, OR_MM_LAST>), grid, blk, 0, st, a, bf16); break;
+    case OR_MM_GRAM: hipLaunchKernelGGL((k_ortho_mm<S, OR_MM_GRAM>), grid, blk, 0, st, a); break;
+    case OR_MM_POLY: hipLaunchKernelGGL((k_ortho_mm<S, OR_MM_POLY>), grid, blk, 0, st, a); break;
+    case OR_MM_STEP: hipLaunchKernelGGL((k_ortho_mm<S, OR_MM_STEP>), grid, blk, 0, st, a); break;
+    default:
+        if (bf16) hipLaunchKernelGGL((k_ortho_mm<S, OR_MM_LAST_BF16>), grid, blk, 0, st, a);
+        else hipLaunchKernelGGL((k_ortho_mm<S, OR_MM_LAST>), grid, blk, 0, st, a);
     }
 }
 
@@ -432,12 +623,22 @@ hipError_t launch_ortho_cast(const OrArgs &a, int64_t n, gq_dtype dt, hipStream_
     return hipGetLastError();
 }
 
+hipError_t launch_ortho_small(const OrArgs &a, const OrSteps &st, int64_t n, gq_dtype dt,
+                              gq_dtype out, hipStream_t s) {
+    const int bf16 = out == GQ_BF16;
+    if (dt == GQ_F32) small_typed<float>(a, st, n, bf16, s);
+    else if (dt == GQ_F16) small_typed<__half>(a, st, n, bf16, s);
+    else small_typed<bf16_t>(a, st, n, bf16, s);
+    return hipGetLastError();
+}
+
 hipError_t launch_ortho_mm(const OrArgs &a, int64_t n, int tile, OrMode mode, gq_dtype out,
                            hipStream_t st) {
-    const int bf16 = out == GQ_BF16;
+    const bool bf16 = out == GQ_BF16;
     if (tile == 256) mm_shape<MmBig>(a, n, mode, bf16, st);
     else if (tile == 128) mm_shape<MmMid>(a, n, mode, bf16, st);
-    else mm_shape<MmSmall>(a, n, mode, bf16, st);
+    else if (n > OR_FEW) mm_shape<MmSmall>(a, n, mode, bf16, st);
+    else mm_shape<MmFew>(a, n, mode, bf16, st);
     return hipGetLastError();
 }
 

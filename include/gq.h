@@ -699,8 +699,8 @@ gq_status gq_ortho_create(const int64_t *h_off, const int64_t *h_rows, const int
 gq_status gq_ortho_destroy(gq_ortho *p);
 
 /* Elements of the flat buffers (the end of the last matrix), matrices, bytes
- * of device memory, and rows and columns of an output tile (informational);
- * any pointer may be NULL. */
+ * of device memory, and rows and columns of a tile of X (informational); any
+ * pointer may be NULL. */
 gq_status gq_ortho_info(const gq_ortho *p, int64_t *n, int64_t *n_mats, int64_t *bytes,
                         int32_t *tile);
 

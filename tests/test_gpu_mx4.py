@@ -141,7 +141,8 @@ def test_reduce(gq, W):
 
 PRODUCTS = [(1, 1, 1), (1, 1, 33), (3, 5, 31), (16, 16, 128), (17, 33, 100), (64, 64, 256),
             (65, 63, 257), (7, 1000, 1024), (128, 130, 513), (300, 200, 4096), (64, 147, 4000),
-            (1, 30, 4096), (1000, 24, 2000), (513, 511, 640), (1100, 4200, 300)]
+            (1, 30, 4096), (1000, 24, 2000), (513, 511, 640), (1100, 4200, 300), (70, 60, 2600),
+            (4000, 4097, 520), (2049, 2050, 33)]
 
 
 def _product(gq, rng, m, n, k, dt, add, split, gap, offset, lo, hi, nan=0.0):
