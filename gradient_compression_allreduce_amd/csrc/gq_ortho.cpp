@@ -25,6 +25,7 @@ struct gq_ortho {
     char *d_mem = nullptr;         // one allocation: workspace, partials, tables
     _Float16 *d_ws = nullptr;
     double *d_part = nullptr;
+    float *d_sums = nullptr;       // partial sums of G where its K is split
     OrMat *d_mats = nullptr;
     OrTile *d_tiles[OR_TABLES] = {};
     int64_t n_tiles[OR_TABLES] = {};
@@ -62,39 +63,92 @@ std::vector<OrTile> deal(const std::vector<OrTile> &tiles, std::vector<Run> runs
     }
     size_t longest = 0;
     for (const auto &v : queue) longest = std::max(longest, v.size());
-    std::vector<OrTile> out(8 * longest, OrTile{-1, 0, 0});
+    std::vector<OrTile> out(8 * longest, OrTile{-1, 0, 0, -1, 0, 0});
     for (int x = 0; x < 8; ++x)
         for (size_t i = 0; i < queue[x].size(); ++i) out[8 * i + x] = queue[x][i];
     while (!out.empty() && out.back().mat < 0) out.pop_back();
     return out;
 }
 
-// Tiles of all matrices' s x s (upper half) or s x l outputs.
-std::vector<OrTile> product_tiles(const std::vector<OrMat> &mats, int tile, bool gram) {
+// Adds the runs of 32 among the tiles from `first` on, of `cost` each.
+void add_runs(std::vector<Run> &runs, int64_t first, int64_t end, int64_t cost) {
+    for (int64_t f = first; f < end; f += 32)
+        runs.push_back({f, std::min<int64_t>(32, end - f), cost});
+}
+
+// Tiles of all matrices' s x l outputs.
+std::vector<OrTile> x_tiles(const std::vector<OrMat> &mats, int tile) {
     std::vector<OrTile> tiles;
     std::vector<Run> runs;
     for (size_t m = 0; m < mats.size(); ++m) {
         const int ts = mats[m].sp / tile, tl = mats[m].lp / tile;
         const int64_t first = static_cast<int64_t>(tiles.size());
-        if (gram) {
-            for (int i = 0; i < ts; ++i)
-                for (int j = i; j < ts; ++j) tiles.push_back({static_cast<int32_t>(m), i, j});
-        } else {
-            for (int i0 = 0; i0 < ts; i0 += 8)
-                for (int j = 0; j < tl; ++j)
-                    for (int i = i0; i < std::min(ts, i0 + 8); ++i)
-                        tiles.push_back({static_cast<int32_t>(m), i, j});
-        }
-        const int64_t cost = gram ? mats[m].lp : mats[m].sp;
-        for (int64_t f = first; f < static_cast<int64_t>(tiles.size()); f += 32)
-            runs.push_back({f, std::min<int64_t>(32, static_cast<int64_t>(tiles.size()) - f), cost});
+        for (int i0 = 0; i0 < ts; i0 += 8)
+            for (int j = 0; j < tl; ++j)
+                for (int i = i0; i < std::min(ts, i0 + 8); ++i)
+                    tiles.push_back({static_cast<int32_t>(m), i, j, -1, 0, 0});
+        add_runs(runs, first, static_cast<int64_t>(tiles.size()), mats[m].sp);
     }
     return deal(tiles, runs);
 }
 
+// Tiles of the upper halves of all matrices' s x s outputs: for G, with K split
+// where it is long and there are few tiles, for the joins of what was split,
+// and for Q.  Returns the number of partial sums.  K goes into parts of 1024
+// columns or more, as many as give two work groups per compute unit; 1024 x
+// 30522: see the figures at choose_tile.
+int64_t g_tiles(const std::vector<OrMat> &mats, int tile, std::vector<OrTile> &gram,
+                std::vector<OrTile> &join, std::vector<OrTile> &poly) {
+    int64_t total = 0, parts = 0;
+    for (const OrMat &m : mats) total += static_cast<int64_t>(m.sp / tile) * (m.sp / tile + 1) / 2;
+    const int64_t want = tile == 64 ? 2 * kCus / total : 1;
+    std::vector<OrTile> g, q;
+    std::vector<Run> gr, qr;
+    for (size_t m = 0; m < mats.size(); ++m) {
+        const int ts = mats[m].sp / tile;
+        const int64_t groups = (mats[m].lp + 127) / 128;
+        const int64_t splits = std::max<int64_t>(1, std::min(want, groups / 8));
+        // (an even number of groups a part: the loop's rounds are of two)
+        const int64_t per = splits == 1 ? groups : round_up((groups + splits - 1) / splits, 2);
+        const int64_t count = (groups + per - 1) / per;
+        const int64_t g0 = static_cast<int64_t>(g.size()), q0 = static_cast<int64_t>(q.size());
+        for (int i = 0; i < ts; ++i) {
+            for (int j = i; j < ts; ++j) {
+                OrTile t = {static_cast<int32_t>(m), i, j, -1, 0, static_cast<int32_t>(groups)};
+                q.push_back(t);
+                if (count == 1) {
+                    g.push_back(t);
+                    continue;
+                }
+                t.part = static_cast<int32_t>(parts);
+                t.count = static_cast<int32_t>(count);
+                join.push_back(t);
+                for (int64_t k = 0; k < count; ++k) {
+                    t.part = static_cast<int32_t>(parts++);
+                    t.first = static_cast<int32_t>(k * per);
+                    t.count = static_cast<int32_t>(std::min(per, groups - k * per));
+                    g.push_back(t);
+                }
+            }
+        }
+        add_runs(gr, g0, static_cast<int64_t>(g.size()), per);
+        add_runs(qr, q0, static_cast<int64_t>(q.size()), mats[m].sp);
+    }
+    gram = deal(g, gr);
+    poly = deal(q, qr);
+    return parts;
+}
+
 // Tiles of the products: `s` x `s` of G and Q (their upper halves), or s x l
 // of X.  The largest that still gives the device enough of them: one work
-// group per compute unit with tiles of 256, two with tiles of 128.
+// group per compute unit with tiles of 256, two with tiles of 128.  Measured,
+// us a call of five steps on fp32 gradients with momentum, tiles of G / of X:
+//                       64/64 128/128 256/256  the choice
+//   one 2048 x 2048       419     513     989  64/64
+//   4 of 1024 x 4096      699     652     996  64/256: 584
+//   16 of 1024 x 1024     857     691     696  128/256: 648
+//   one 4096 x 4096      2565    2012    2047  128/256: 1832
+//   one 8192 x 8192     20962   13479   11760  256/256
 int choose_tile(const int64_t *rows, const int64_t *cols, int64_t n, bool gram) {
     for (const int t : {256, 128}) {
         int64_t tiles = 0;
@@ -158,18 +212,20 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
         m.part = static_cast<int32_t>(parts);
         m.parts = static_cast<int32_t>((elems + m.chunk - 1) / m.chunk);
         parts += m.parts;
-        for (int32_t p = 0; p < m.parts; ++p) tab[OR_NORM].push_back({static_cast<int32_t>(i), p, 0});
+        for (int32_t p = 0; p < m.parts; ++p) 
+            tab[OR_NORM].push_back({static_cast<int32_t>(i), p, 0, -1, 0, 0});
         const int rp = m.tr ? m.lp : m.sp, cp = m.tr ? m.sp : m.lp;
         for (int r = 0; r < rp / OR_CAST_TILE; ++r)
             for (int c = 0; c < cp / OR_CAST_TILE; ++c)
-                tab[OR_CAST].push_back({static_cast<int32_t>(i), r, c});
+                tab[OR_CAST].push_back({static_cast<int32_t>(i), r, c, -1, 0, 0});
         if (static_cast<int64_t>(tab[OR_CAST].size()) >= kMaxTiles)
             return arg_fail(GQ_ERR_INVALID, op, "more than %lld tiles: too many elements",
                             static_cast<long long>(kMaxTiles));
     }
+    int64_t sums = 0;
     if (!small) {
-        tab[OR_GRAM] = product_tiles(mats, tile_g, true);
-        tab[OR_X] = product_tiles(mats, tile_x, false);
+        sums = g_tiles(mats, tile_g, tab[OR_GRAM], tab[OR_JOIN], tab[OR_POLY]);
+        tab[OR_X] = x_tiles(mats, tile_x);
     }
     gq_ortho *P = new gq_ortho;
     P->steps = steps;
@@ -187,6 +243,8 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
     int64_t size = round_up(at * 2, 256);
     const int64_t part_at = size;
     size += round_up(parts * 8, 256);
+    const int64_t sums_at = size;
+    size += sums * tile_g * tile_g * 4;
     const int64_t mats_at = size;
     size += round_up(static_cast<int64_t>(mats.size() * sizeof(OrMat)), 256);
     int64_t tab_at[OR_TABLES];
@@ -200,6 +258,7 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
     if (e == hipSuccess) {
         P->d_ws = reinterpret_cast<_Float16 *>(P->d_mem);
         P->d_part = reinterpret_cast<double *>(P->d_mem + part_at);
+        P->d_sums = reinterpret_cast<float *>(P->d_mem + sums_at);
         P->d_mats = reinterpret_cast<OrMat *>(P->d_mem + mats_at);
         e = hipMemcpy(P->d_mats, mats.data(), mats.size() * sizeof(OrMat), hipMemcpyHostToDevice);
     }
@@ -315,6 +374,7 @@ gq_status gq_ortho_step(gq_ortho *p, const void *g, gq_dtype dt, float in_mul, f
     a.mats = p->d_mats;
     a.ws = p->d_ws;
     a.part = p->d_part;
+    a.sums = p->d_sums;
     a.g = g;
     a.m = momentum;
     a.out = out;
@@ -335,8 +395,12 @@ gq_status gq_ortho_step(gq_ortho *p, const void *g, gq_dtype dt, float in_mul, f
         a.cur = k & 1;
         a.tiles = p->d_tiles[OR_GRAM];
         e = launch_ortho_mm(a, p->n_tiles[OR_GRAM], p->tile_g, OR_MM_GRAM, out_dt, st);
+        a.tiles = p->d_tiles[OR_JOIN];
+        if (e == hipSuccess && p->n_tiles[OR_JOIN] > 0)
+            e = launch_ortho_mm(a, p->n_tiles[OR_JOIN], p->tile_g, OR_MM_JOIN, out_dt, st);
+        a.tiles = p->d_tiles[OR_POLY];
         if (e == hipSuccess)
-            e = launch_ortho_mm(a, p->n_tiles[OR_GRAM], p->tile_g, OR_MM_POLY, out_dt, st);
+            e = launch_ortho_mm(a, p->n_tiles[OR_POLY], p->tile_g, OR_MM_POLY, out_dt, st);
         a.tiles = p->d_tiles[OR_X];
         if (e == hipSuccess)
             e = launch_ortho_mm(a, p->n_tiles[OR_X], p->tile_x,

@@ -32,6 +32,10 @@ struct OrMat {
 // A tile of a launch (mat < 0: none, it only keeps the order of the XCDs).
 struct OrTile {
     int32_t mat, i, j;
+    // G = X X^T: the tile's share of K, in units of 128 columns of X, and where
+    // its partial sums go (part < 0: the whole sum is the tile).  Joining:
+    // the first of the tile's partial sums and, in count, how many.
+    int32_t part, first, count;
 };
 
 struct OrArgs {
@@ -39,6 +43,7 @@ struct OrArgs {
     const OrTile *tiles;
     _Float16 *ws;
     double *part;
+    float *sums;        // partial sums of tiles of G, tile * tile floats each
     const void *g;
     float *m;           // NULL: no momentum
     void *out;
@@ -54,8 +59,10 @@ struct OrSteps {
     int32_t steps;
 };
 
-enum OrTable { OR_NORM = 0, OR_CAST = 1, OR_GRAM = 2, OR_X = 3, OR_TABLES = 4 };
-enum OrMode { OR_MM_GRAM = 0, OR_MM_POLY = 1, OR_MM_STEP = 2, OR_MM_LAST = 3, OR_MM_LAST_BF16 = 4 };
+enum OrTable { OR_NORM = 0, OR_CAST = 1, OR_GRAM = 2, OR_JOIN = 3, OR_POLY = 4, OR_X = 5, OR_TABLES = 6 };
+enum OrMode {
+    OR_MM_GRAM = 0, OR_MM_POLY = 1, OR_MM_STEP = 2, OR_MM_LAST = 3, OR_MM_LAST_BF16 = 4, OR_MM_JOIN = 5
+};
 
 constexpr int OR_CAST_TILE = 64;
 

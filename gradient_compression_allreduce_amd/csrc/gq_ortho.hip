@@ -283,11 +283,14 @@ struct AddX {
 // MODE OR_MM_GRAM: G = X X^T          (K: columns of X)
 //      OR_MM_POLY: Q = b G + c G G    (G = G^T)
 //      OR_MM_STEP: X <- a X + Q X     (K: rows of X)
-//      OR_MM_LAST: the same into the caller's output
+//      OR_MM_LAST, OR_MM_LAST_BF16: the same into the caller's output
+//      OR_MM_JOIN: G from the partial sums that OR_MM_GRAM left of tiles whose
+//                  K it split, added in the order of K
 template <typename S, int MODE>
 __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a) {
     MM_LDS(S);
-    constexpr bool LAST = MODE >= OR_MM_LAST;
+    constexpr bool LAST = MODE == OR_MM_LAST || MODE == OR_MM_LAST_BF16;
+    constexpr bool TO_G = MODE == OR_MM_GRAM || MODE == OR_MM_JOIN;
     const OrTile t = a.tiles[blockIdx.x];
     if (t.mat < 0) return;
     const OrMat &mt = a.mats[t.mat];
@@ -296,18 +299,38 @@ __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a) {
     const _Float16 *x = a.ws + mt.x[a.cur];
     const _Float16 *pm = MODE == OR_MM_GRAM ? x : a.ws + (MODE == OR_MM_POLY ? mt.a : mt.b);
     const int kdim = MODE == OR_MM_GRAM ? lp : sp;
-    const MmRows p = mm_rows(pm, kdim * 2, i0, sp, S::T);
     MmAcc<S> acc = {};
-    const int groups = (kdim + 127) / 128;
-    if constexpr (MODE == OR_MM_GRAM || MODE == OR_MM_POLY) {
-        const MmRows q = mm_rows(pm, kdim * 2, j0, sp, S::T);
-        mm_loop<S, false>(p, q, MmScale{}, 0, groups, mm_lds, nullptr, MmNoExtra{}, acc);
-    } else {
-        const MmCols q = {reinterpret_cast<const char *>(x + j0), static_cast<uint32_t>(lp) * 2u,
-                          static_cast<uint32_t>(j0) * 2u, sp};
-        mm_loop<S, false>(p, q, MmScale{}, 0, groups, mm_lds, nullptr, AddX{a.a, i0}, acc);
-    }
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    constexpr int SUMS = S::PARTS * S::FM * S::FN;      // groups of four sums per lane
+    auto at = [&](int part, int k) {                    // a lane's k-th four of a partial sum
+        return reinterpret_cast<mm_f32x4 *>(a.sums + static_cast<int64_t>(part) * (S::T * S::T)) +
+               (wave * SUMS + k) * 64 + lane;
+    };
+    mm_f32x4 *flat = &acc.c[0][0][0];
+    if constexpr (MODE == OR_MM_JOIN) {
+        for (int p = 0; p < t.count; ++p)
+#pragma unroll
+            for (int k = 0; k < SUMS; ++k) flat[k] += *at(t.part + p, k);
+    } else {
+        const MmRows p = mm_rows(pm, kdim * 2, i0, sp, S::T);
+        const int groups = (kdim + 127) / 128;
+        if constexpr (MODE == OR_MM_GRAM) {
+            const MmRows q = mm_rows(pm, kdim * 2, j0, sp, S::T);
+            mm_loop<S, false>(p, q, MmScale{}, t.first, t.count, mm_lds, nullptr, MmNoExtra{}, acc);
+            if (t.part >= 0) {
+#pragma unroll
+                for (int k = 0; k < SUMS; ++k) *at(t.part, k) = flat[k];
+                return;
+            }
+        } else if constexpr (MODE == OR_MM_POLY) {
+            const MmRows q = mm_rows(pm, kdim * 2, j0, sp, S::T);
+            mm_loop<S, false>(p, q, MmScale{}, 0, groups, mm_lds, nullptr, MmNoExtra{}, acc);
+        } else {
+            const MmCols q = {reinterpret_cast<const char *>(x + j0), static_cast<uint32_t>(lp) * 2u,
+                              static_cast<uint32_t>(j0) * 2u, sp};
+            mm_loop<S, false>(p, q, MmScale{}, 0, groups, mm_lds, nullptr, AddX{a.a, i0}, acc);
+        }
+    }
     constexpr int TM = 16 * S::FM, TN = 16 * S::FN, PART = TM * TN * 2;
     static_assert(PART * S::PARTS * S::WM * S::WN <= S::UNIT * S::BUFFERS,
                   "a wave's part of the tile fits its part of the buffers");
@@ -332,7 +355,7 @@ __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a) {
                                         false);
                 } else {
                     // (both factors are powers of two but for out_mul)
-                    const float mul = MODE == OR_MM_GRAM ? 1.0f / (mt.scale * mt.scale)
+                    const float mul = TO_G ? 1.0f / (mt.scale * mt.scale)
                                       : LAST ? mt.out_mul / mt.scale : 1.0f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -350,8 +373,8 @@ __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a) {
     uint16_t *d;
     int ld, ldt, rows = 0x7fffffff, cols = 0x7fffffff, al = 8;
     bool by_rows = true, by_cols = false;
-    if constexpr (MODE == OR_MM_GRAM || MODE == OR_MM_POLY) {
-        d = reinterpret_cast<uint16_t *>(a.ws + (MODE == OR_MM_GRAM ? mt.a : mt.b));
+    if constexpr (TO_G || MODE == OR_MM_POLY) {
+        d = reinterpret_cast<uint16_t *>(a.ws + (TO_G ? mt.a : mt.b));
         ld = ldt = sp;
         by_cols = t.i != t.j;
     } else if constexpr (!LAST) {
@@ -634,6 +657,11 @@ hipError_t launch_ortho_small(const OrArgs &a, const OrSteps &st, int64_t n, gq_
 
 hipError_t launch_ortho_mm(const OrArgs &a, int64_t n, int tile, OrMode mode, gq_dtype out,
                            hipStream_t st) {
+    if (mode == OR_MM_JOIN) {   // tiles of 64 (the sums lie alike for both of their shapes)
+        hipLaunchKernelGGL((k_ortho_mm<MmSmall, OR_MM_JOIN>), dim3(static_cast<unsigned>(n)),
+                           dim3(MmSmall::THREADS), 0, st, a);
+        return hipGetLastError();
+    }
     const bool bf16 = out == GQ_BF16;
     if (tile == 256) mm_shape<MmBig>(a, n, mode, bf16, st);
     else if (tile == 128) mm_shape<MmMid>(a, n, mode, bf16, st);

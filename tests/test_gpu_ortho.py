@@ -82,7 +82,7 @@ def _gradients(rng, shapes, kind):
 
 
 SHAPES = [[(1, 1)], [(1, 7), (7, 1), (5, 5)], [(64, 147)], [(1000, 64), (33, 1024), (64, 64)],
-          [(64, 256), (200, 63)], [(64, 1025)], [(65, 300)], [(147, 64), (64, 64), (65, 63)],
+          [(64, 256), (200, 63)], [(64, 1025)], [(65, 300)], [(40, 5000)], [(4100, 130), (70, 2100)], [(147, 64), (64, 64), (65, 63)],
           [(31, 200), (200, 31), (129, 129), (100, 1000)], [(300, 700), (700, 300)],
           [(256, 512)] * 3, [(1024, 1100), (1030, 1000)]]
 
