@@ -1,7 +1,6 @@
 // gq_mx4.hip -- gfx950 kernels of the microscaled 4-bit gradient exchange:
 //   k_mx4_quantize       codes and scales of W ranks' gradients, blocks along
-//                        contiguous 16-byte aligned rows;
-//   k_mx4_quantize_any   the same for rows of any alignment;
+//                        the rows;
 //   k_mx4_quantize_cols  blocks down the columns (the transposed matrix's
 //                        codes), as a product over the rows reads them;
 //   k_mx4_reduce         the rank-order fp32 sum of W ranks' codes and, fused
@@ -18,7 +17,7 @@ namespace {
 
 constexpr int MXQ_BLOCK = 256;
 constexpr int MXQ_SLOTS = 4;      // 16-byte slots per lane in flight
-constexpr int MXT_WAVES = 8;      // transposed: 8 x 16 bytes = one line per column
+constexpr int MXT_BLOCKS = 8;     // transposed: 8 x 16 bytes = one line per column
 constexpr int MXR_BLOCK = 256;
 constexpr int MXR_RG = 8;         // ranks loaded together
 constexpr uint32_t kAbs = 0x7fffffffu;
@@ -26,14 +25,9 @@ constexpr int64_t MX_MAX_GRID = 1 << 20;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 
 struct bf16_t { uint16_t bits; };
-
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(bf16_t v) {
-    return __uint_as_float(static_cast<uint32_t>(v.bits) << 16);
-}
 
 template <typename T>
 __device__ __forceinline__ float slot_f32(const u32x4 &r, int k);
@@ -50,6 +44,12 @@ template <>
 __device__ __forceinline__ float slot_f32<bf16_t>(const u32x4 &r, int k) {
     const uint32_t w = r[k >> 1];
     return __uint_as_float((k & 1) ? w & 0xffff0000u : w << 16);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t load_bits(const T *p) {
+    if constexpr (sizeof(T) == 4) return *reinterpret_cast<const uint32_t *>(p);
+    else return *reinterpret_cast<const uint16_t *>(p);
 }
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
@@ -78,6 +78,22 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m) {
 // of input; the 8 (fp32) or 4 (16-bit) lanes that hold a block combine their
 // maxima by lane permutes and write 2 or 4 bytes of codes each.  A row's
 // slots are counted up to whole blocks; those past its end read as zeros.
+// Rows may start at any element: a slot is one load of 16 bytes either way, and
+// the last, short one of a row is the 16 bytes that end with the row, shifted.
+
+// The bytes of v from byte n on (0 < n < 16), zeros behind them.
+__device__ __forceinline__ u32x4 drop_bytes(const u32x4 &v, int n) {
+    const uint64_t lo = (static_cast<uint64_t>(v[1]) << 32) | v[0];
+    const uint64_t hi = (static_cast<uint64_t>(v[3]) << 32) | v[2];
+    const int s = 8 * (n & 7);
+    const uint64_t l = s ? lo >> s | hi << (64 - s) : lo, h = hi >> s;
+    const uint64_t x = n >= 8 ? h : l, y = n >= 8 ? 0 : h;
+    return u32x4{static_cast<uint32_t>(x), static_cast<uint32_t>(x >> 32),
+                 static_cast<uint32_t>(y), static_cast<uint32_t>(y >> 32)};
+}
+
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;     // at any element
+
 template <typename T, bool MUL, bool ROWS>
 __global__ __launch_bounds__(MXQ_BLOCK) void k_mx4_quantize(const MxQArgs a) {
     constexpr int V = 16 / sizeof(T);
@@ -89,37 +105,51 @@ __global__ __launch_bounds__(MXQ_BLOCK) void k_mx4_quantize(const MxQArgs a) {
     const int64_t chunk = MXQ_BLOCK * MXQ_SLOTS;
     for (int64_t c0 = blockIdx.x * chunk; c0 < total; c0 += gridDim.x * chunk) {
         u32x4 raw[MXQ_SLOTS];
-#pragma unroll
-        for (int s = 0; s < MXQ_SLOTS; ++s) {
+        int over[MXQ_SLOTS];            // elements past the row's end
+        auto place = [&](int s, int64_t &col) {
             const int64_t j = c0 + s * MXQ_BLOCK + threadIdx.x;
-            int64_t row = 0, col = j * V;
+            int64_t row = 0;
+            col = j * V;
             if (ROWS) {   // total < 2^32 here
                 const uint32_t r32 = static_cast<uint32_t>(j) / static_cast<uint32_t>(spr);
                 row = r32;
                 col = static_cast<int64_t>(static_cast<uint32_t>(j) -
                                            r32 * static_cast<uint32_t>(spr)) * V;
             }
-            const T *p = x + row * a.ld + col;
             raw[s] = u32x4{0, 0, 0, 0};
-            if (j < total) {
-                if (col + V <= a.cols) {
-                    raw[s] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
-                } else {
+            over[s] = 0;
+            return j < total && col < a.cols ? x + row * a.ld + col : nullptr;
+        };
+        if (a.cols >= V) {
 #pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        if (col + k >= a.cols) continue;
-                        if constexpr (V == 4)
-                            raw[s][k] = reinterpret_cast<const uint32_t *>(p)[k];
-                        else
-                            raw[s][k >> 1] |= static_cast<uint32_t>(
-                                reinterpret_cast<const uint16_t *>(p)[k]) << (16 * (k & 1));
-                    }
+            for (int s = 0; s < MXQ_SLOTS; ++s) {
+                int64_t col;
+                const T *p = place(s, col);
+                if (p) {
+                    if (col + V > a.cols) over[s] = static_cast<int>(col + V - a.cols);
+                    raw[s] = __builtin_nontemporal_load(
+                        reinterpret_cast<const u32x4_any *>(p - over[s]));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < MXQ_SLOTS; ++s) {
+                int64_t col;
+                const T *p = place(s, col);
+#pragma unroll
+                for (int k = 0; k < V - 1; ++k) {
+                    if (!p || k >= a.cols) continue;
+                    if constexpr (V == 4)
+                        raw[s][k] = load_bits(p + k);
+                    else
+                        raw[s][k >> 1] |= load_bits(p + k) << (16 * (k & 1));
                 }
             }
         }
 #pragma unroll
         for (int s = 0; s < MXQ_SLOTS; ++s) {
             const int64_t j = c0 + s * MXQ_BLOCK + threadIdx.x;
+            if (over[s] > 0) raw[s] = drop_bytes(raw[s], over[s] * static_cast<int>(sizeof(T)));
             float g[V];
             uint32_t m = 0;
 #pragma unroll
@@ -148,121 +178,96 @@ __global__ __launch_bounds__(MXQ_BLOCK) void k_mx4_quantize(const MxQArgs a) {
     }
 }
 
-// Rows of any start and length: half a wave takes a block, one element per
-// lane (coalesced loads of the element's size, no alignment needed).
-template <typename T, bool MUL>
-__global__ __launch_bounds__(MXQ_BLOCK) void k_mx4_quantize_any(const MxQArgs a) {
-    constexpr int UB = 4;   // blocks in flight per half wave
-    const int w = blockIdx.y;
-    const T *x = static_cast<const T *>(a.x[w]);
-    const int e = threadIdx.x & 31;
-    const int64_t total = a.rows * a.nb;
-    const int64_t half = static_cast<int64_t>(blockIdx.x) * (MXQ_BLOCK / 32) + (threadIdx.x >> 5);
-    const int64_t halves = static_cast<int64_t>(gridDim.x) * (MXQ_BLOCK / 32);
-    for (int64_t i0 = half * UB; i0 < total; i0 += halves * UB) {
-        float g[UB];
-        int64_t row = i0 / a.nb, b = i0 - row * a.nb;
-#pragma unroll
-        for (int u = 0; u < UB; ++u) {
-            const int64_t col = b * MX_BLOCK + e;
-            g[u] = 0.0f;
-            if (i0 + u < total && col < a.cols) g[u] = to_f32(x[row * a.ld + col]);
-            if (++b == a.nb) {
-                b = 0;
-                ++row;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < UB; ++u) {
-            if (MUL) g[u] = __fmul_rn(g[u], a.in_mul);
-            const uint32_t s = mx_byte(group_max<32>(__float_as_uint(g[u]) & kAbs));
-            const float v = g[u] * mx_mult(s);
-            const float next = __uint_as_float(dpp<0xB1>(__float_as_uint(v)));
-            uint32_t code = mx_code2<0>(0u, v, next) & 0xffu;
-            if (s == 255u) code = 0u;
-            if (i0 + u < total) {
-                if ((e & 1) == 0)
-                    a.q[w][(i0 + u) * MX_BYTES + (e >> 1)] = static_cast<uint8_t>(code);
-                if (e == 0) a.scale[w][i0 + u] = static_cast<uint8_t>(s);
-            }
-        }
-    }
-}
-
 // ---- quantize, columns ------------------------------------------------------
-// A wave takes 32 rows of 64 * F columns: every lane holds F whole blocks in
-// registers, so no lane needs another's maximum.  The eight waves of a work
-// group take consecutive blocks of the same columns, so the 16-byte stores of
-// a column fill a 128-byte line in the L2 cache.  F elements are one 16-byte
-// load where every row is aligned for it, otherwise F = 1.
-template <typename T, bool MUL, int F>
-__device__ __forceinline__ void quantize_cols(const MxQArgs &a, int64_t b, int64_t col) {
+// A wave takes a block of 64 * F columns: a lane loads one word (F elements)
+// of each of its 32 rows, and holds F whole blocks in registers, so no lane
+// needs another's maximum.  A work group's eight waves take eight blocks of the
+// same columns or, where there are no more than 4, 2 or 1 blocks (BW), as many of
+// 2, 4 or 8 times the columns.  Their codes and scales leave through LDS, a
+// column's (up to 128 bytes of codes) together.
+typedef uint32_t __attribute__((aligned(2))) u32_any;
+typedef uint64_t __attribute__((aligned(1))) u64_any;
+
+template <typename T, bool MUL>
+__global__ __launch_bounds__(64 * MXT_BLOCKS) void k_mx4_quantize_cols(const MxQArgs a,
+                                                                       int64_t col_groups,
+                                                                       int64_t n_groups, int lbw) {
+    constexpr int F = 4 / sizeof(T);
+    // piece (column * BW + block) at piece ^ (piece / 8 / F % 8)
+    __shared__ u32x4 codes[64 * F * MXT_BLOCKS];
+    __shared__ uint64_t scales[64 * F * MXT_BLOCKS / 8];
+    const int bw = 1 << lbw;
+    auto slot = [](int piece) { return piece ^ (piece >> (F == 2 ? 4 : 3) & 7); };
     const int w = blockIdx.y;
     const T *x = static_cast<const T *>(a.x[w]);
-    const int64_t r0 = b * MX_BLOCK;
-    const T *p = x + r0 * a.ld + col;
-    const bool whole = r0 + MX_BLOCK <= a.rows && col + F <= a.cols;
-    u32x4 raw[F > 1 ? MX_BLOCK : 1];
-    float one[F > 1 ? 1 : MX_BLOCK];
-#pragma unroll
-    for (int i = 0; i < MX_BLOCK; ++i) {
-        if constexpr (F > 1) {
-            raw[i] = u32x4{0, 0, 0, 0};
-            if (whole) {
-                raw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + i * a.ld));
-            } else if (r0 + i < a.rows) {
-#pragma unroll
-                for (int k = 0; k < F; ++k) {
-                    if (col + k >= a.cols) continue;
-                    const T *e = p + i * a.ld + k;
-                    if constexpr (F == 4)
-                        raw[i][k] = *reinterpret_cast<const uint32_t *>(e);
-                    else
-                        raw[i][k >> 1] |= static_cast<uint32_t>(
-                            *reinterpret_cast<const uint16_t *>(e)) << (16 * (k & 1));
-                }
-            }
-        } else {
-            one[i] = r0 + i < a.rows ? to_f32(p[i * a.ld]) : 0.0f;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < F; ++k) {
-        if (col + k >= a.cols) break;
-        auto get = [&](int i) {
-            float g;
-            if constexpr (F > 1) g = slot_f32<T>(raw[i], k);
-            else g = one[i];
-            return MUL ? __fmul_rn(g, a.in_mul) : g;
-        };
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < MX_BLOCK; ++i) m = umax(m, __float_as_uint(get(i)) & kAbs);
-        const uint32_t s = mx_byte(m);
-        const float mul = mx_mult(s);
-        u32x4 code;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t c = mx_code2<0>(0u, get(8 * i) * mul, get(8 * i + 1) * mul);
-            c = mx_code2<1>(c, get(8 * i + 2) * mul, get(8 * i + 3) * mul);
-            c = mx_code2<2>(c, get(8 * i + 4) * mul, get(8 * i + 5) * mul);
-            c = mx_code2<3>(c, get(8 * i + 6) * mul, get(8 * i + 7) * mul);
-            code[i] = s == 255u ? 0u : c;
-        }
-        const int64_t o = (col + k) * a.nb + b;
-        *reinterpret_cast<u32x4 *>(a.q[w] + o * MX_BYTES) = code;
-        a.scale[w][o] = static_cast<uint8_t>(s);
-    }
-}
-
-template <typename T, bool MUL, int F>
-__global__ __launch_bounds__(64 * MXT_WAVES) void k_mx4_quantize_cols(const MxQArgs a,
-                                                                      int64_t col_groups,
-                                                                      int64_t n_groups) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     for (int64_t i = blockIdx.x; i < n_groups; i += gridDim.x) {
-        const int64_t b = i / col_groups * MXT_WAVES + (threadIdx.x >> 6);
-        const int64_t col = (i % col_groups * 64 + (threadIdx.x & 63)) * F;
-        if (b < a.nb && col < a.cols) quantize_cols<T, MUL, F>(a, b, col);
+        const int64_t b0 = i / col_groups * bw;
+        const int64_t c0 = i % col_groups * (64 * F * MXT_BLOCKS >> lbw);
+        const int cw = (wave >> lbw) * 64 * F + lane * F, bk = wave & (bw - 1);
+        const int64_t r0 = (b0 + bk) * MX_BLOCK, col = c0 + cw;
+        // columns past the last one take its word, and are not stored
+        const int64_t cc = col + F <= a.cols ? col : a.cols - F;
+        const int valid = a.rows - r0 < MX_BLOCK ? static_cast<int>(a.rows - r0) : MX_BLOCK;
+        uint32_t raw[MX_BLOCK];
+        if (valid == MX_BLOCK && cc >= 0) {
+            const T *p = x + r0 * a.ld + cc;
+#pragma unroll
+            for (int k = 0; k < MX_BLOCK; ++k)
+                raw[k] = *reinterpret_cast<const u32_any *>(p + k * a.ld);
+        } else {
+#pragma unroll
+            for (int k = 0; k < MX_BLOCK; ++k) {
+                raw[k] = 0;
+                if (k >= valid) continue;
+                const T *p = x + (r0 + k) * a.ld;
+                if (cc >= 0) raw[k] = *reinterpret_cast<const u32_any *>(p + cc);
+                else raw[k] = static_cast<uint32_t>(load_bits(p)) << 16;    // one column
+            }
+        }
+        if (F == 2 && cc < col) {       // the last of an odd number
+#pragma unroll
+            for (int k = 0; k < MX_BLOCK; ++k) raw[k] >>= 16;
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            auto get = [&](int k) {
+                const float g = slot_f32<T>(u32x4{raw[k], 0, 0, 0}, f);
+                return MUL ? __fmul_rn(g, a.in_mul) : g;
+            };
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < MX_BLOCK; ++k) m = umax(m, __float_as_uint(get(k)) & kAbs);
+            const uint32_t s = mx_byte(m);
+            const float mul = mx_mult(s);
+            u32x4 code;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t c = mx_code2<0>(0u, get(8 * k) * mul, get(8 * k + 1) * mul);
+                c = mx_code2<1>(c, get(8 * k + 2) * mul, get(8 * k + 3) * mul);
+                c = mx_code2<2>(c, get(8 * k + 4) * mul, get(8 * k + 5) * mul);
+                c = mx_code2<3>(c, get(8 * k + 6) * mul, get(8 * k + 7) * mul);
+                code[k] = s == 255u ? 0u : c;
+            }
+            const int piece = ((cw + f) << lbw) + bk;
+            codes[slot(piece)] = code;
+            reinterpret_cast<uint8_t *>(scales)[piece] = static_cast<uint8_t>(s);
+        }
+        __syncthreads();
+        const bool whole = b0 + MXT_BLOCKS <= a.nb;     // eight scales of a column together
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            const int piece = f * 64 * MXT_BLOCKS + threadIdx.x;
+            const int64_t c = c0 + (piece >> lbw), k = b0 + (piece & (bw - 1));
+            if (c >= a.cols || k >= a.nb) continue;
+            reinterpret_cast<u32x4 *>(a.q[w])[c * a.nb + k] = codes[slot(piece)];
+            if (!whole)
+                a.scale[w][c * a.nb + k] = reinterpret_cast<const uint8_t *>(scales)[piece];
+        }
+        if (whole && threadIdx.x < 64 * F && c0 + threadIdx.x < a.cols)
+            *reinterpret_cast<u64_any *>(a.scale[w] + (c0 + threadIdx.x) * a.nb + b0) =
+                scales[threadIdx.x];
+        __syncthreads();
     }
 }
 
@@ -323,7 +328,9 @@ __global__ __launch_bounds__(MXR_BLOCK) void k_mx4_reduce(const MxRArgs a) {
         }
         int64_t row = 0, b = j;
         if (!FLAT) {
-            row = j / a.nb;
+            row = total <= 0xffffffffu
+                      ? static_cast<uint32_t>(j) / static_cast<uint32_t>(a.nb)
+                      : j / a.nb;
             b = j - row * a.nb;
         }
         if (CODES) {
@@ -379,13 +386,24 @@ __global__ __launch_bounds__(MXR_BLOCK) void k_mx4_reduce(const MxRArgs a) {
                     }
                 }
             } else {
-                for (int i = 0; i < 32; ++i) {
-                    const int blk = 2 * i + (lane >> 5), k = lane & 31;
-                    const int64_t jj = w0 + blk;
-                    if (jj >= total) break;
-                    const float v = my[8 * blk + ((k >> 2) ^ (blk & 7))][k & 3];
-                    const int64_t rr = jj / a.nb, cc = (jj - rr * a.nb) * MX_BLOCK + k;
-                    if (cc < a.cols) a.r[rr * a.cols + cc] = v;
+                // a block's place and length, from the lane that summed it;
+                // rows start at any element
+                const int64_t first = row * a.cols + b * MX_BLOCK;
+                const int64_t left = in ? a.cols - b * MX_BLOCK : 0;
+                const int len = static_cast<int>(left < MX_BLOCK ? left : MX_BLOCK);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int blk = i * 8 + (lane >> 3), p = lane & 7;
+                    const f32x4 v = my[8 * blk + (p ^ (blk & 7))];
+                    const int64_t e = __shfl(first, blk, 64) + 4 * p;
+                    const int n = __shfl(len, blk, 64) - 4 * p;
+                    if (n >= 4) {
+                        __builtin_nontemporal_store(v, reinterpret_cast<f32x4_any *>(a.r + e));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 3; ++k)
+                            if (k < n) a.r[e + k] = v[k];
+                    }
                 }
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -403,22 +421,15 @@ int64_t groups(int64_t work, int64_t per) {
 template <typename T, bool MUL>
 hipError_t quantize_typed(const MxQArgs &in, bool transpose, hipStream_t st) {
     MxQArgs a = in;
-    constexpr int V = 16 / sizeof(T);
-    constexpr int64_t L = MX_BLOCK / V;
-    const bool wide = a.ld % V == 0;    // every row starts 16-byte aligned
+    constexpr int64_t L = MX_BLOCK * sizeof(T) / 16;     // slots per block
     const unsigned W = static_cast<unsigned>(a.W);
     if (transpose) {
         a.nb = (a.rows + MX_BLOCK - 1) / MX_BLOCK;
-        const int64_t per = 64 * (wide ? V : 1);
-        const int64_t cg = (a.cols + per - 1) / per;
-        const int64_t n = cg * ((a.nb + MXT_WAVES - 1) / MXT_WAVES);
-        const dim3 grid(static_cast<unsigned>(groups(n, 1)), W);
-        if (wide)
-            hipLaunchKernelGGL((k_mx4_quantize_cols<T, MUL, V>), grid, dim3(64 * MXT_WAVES), 0, st,
-                               a, cg, n);
-        else
-            hipLaunchKernelGGL((k_mx4_quantize_cols<T, MUL, 1>), grid, dim3(64 * MXT_WAVES), 0, st,
-                               a, cg, n);
+        const int lbw = a.nb > 4 ? 3 : a.nb > 2 ? 2 : a.nb > 1 ? 1 : 0;
+        const int64_t C = 64 * 4 / sizeof(T) * MXT_BLOCKS >> lbw, bw = 1 << lbw;
+        const int64_t cg = (a.cols + C - 1) / C, n = cg * ((a.nb + bw - 1) / bw);
+        hipLaunchKernelGGL((k_mx4_quantize_cols<T, MUL>), dim3(static_cast<unsigned>(groups(n, 1)), W),
+                           dim3(64 * MXT_BLOCKS), 0, st, a, cg, n, lbw);
         return hipGetLastError();
     }
     a.nb = (a.cols + MX_BLOCK - 1) / MX_BLOCK;
@@ -427,18 +438,26 @@ hipError_t quantize_typed(const MxQArgs &in, bool transpose, hipStream_t st) {
         a.nb *= a.rows;
         a.rows = 1;
     }
-    const int64_t slots = a.rows * a.nb * L;
-    if (a.rows == 1) {
-        const dim3 grid(static_cast<unsigned>(groups(slots, MXQ_BLOCK * MXQ_SLOTS)), W);
-        hipLaunchKernelGGL((k_mx4_quantize<T, MUL, false>), grid, dim3(MXQ_BLOCK), 0, st, a);
-    } else if (wide && slots < (int64_t{1} << 32) - MXQ_BLOCK * MXQ_SLOTS) {
-        const dim3 grid(static_cast<unsigned>(groups(slots, MXQ_BLOCK * MXQ_SLOTS)), W);
-        hipLaunchKernelGGL((k_mx4_quantize<T, MUL, true>), grid, dim3(MXQ_BLOCK), 0, st, a);
-    } else {
-        const dim3 grid(static_cast<unsigned>(groups(a.rows * a.nb, MXQ_BLOCK / 32 * 4)), W);
-        hipLaunchKernelGGL((k_mx4_quantize_any<T, MUL>), grid, dim3(MXQ_BLOCK), 0, st, a);
+    // the rows of a launch hold less than 2^32 slots, or it is of one row
+    int64_t left = a.rows, most = ((int64_t{1} << 32) - MXQ_BLOCK * MXQ_SLOTS - 1) / (a.nb * L);
+    if (most < 1) most = 1;
+    while (left > 0) {
+        a.rows = left < most ? left : most;
+        const dim3 grid(static_cast<unsigned>(groups(a.rows * a.nb * L, MXQ_BLOCK * MXQ_SLOTS)), W);
+        if (a.rows == 1)
+            hipLaunchKernelGGL((k_mx4_quantize<T, MUL, false>), grid, dim3(MXQ_BLOCK), 0, st, a);
+        else
+            hipLaunchKernelGGL((k_mx4_quantize<T, MUL, true>), grid, dim3(MXQ_BLOCK), 0, st, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        left -= a.rows;
+        for (unsigned w = 0; w < W && left > 0; ++w) {
+            a.x[w] = static_cast<const T *>(a.x[w]) + a.rows * a.ld;
+            a.q[w] += a.rows * a.nb * MX_BYTES;
+            a.scale[w] += a.rows * a.nb;
+        }
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 template <typename T>

@@ -297,3 +297,103 @@ def test_weight_gradient_exchange_run(gq):
         assert all(torch.equal(t, e) for t, e in zip((r, so, qo), eager)), i
         step()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_short_rows_and_columns(gq, dt):
+    """Every length around the pieces that the kernels load (1 to 17 elements
+    and one more or less than 64 lanes), rows that start at any element, and
+    1 to 9 blocks down the columns."""
+    rng = np.random.default_rng(12)
+    shapes = [(r, c) for r in (2, 9) for c in range(1, 18)] + [(3, 61), (3, 63), (2, 127)]
+    shapes += [(r, c) for r in (31, 33, 64, 65, 97, 160, 257, 290) for c in (1, 2, 63, 65, 129, 300)]
+    for rows, cols in shapes:
+        for gap in (0, 1, 2):
+            say("short", dt, rows, cols, "gap", gap)
+            wide = torch.full((rows, cols + gap), float("nan"), dtype=TORCH[dt])
+            wide[:, :cols] = _values(rng, rows, cols, dt)
+            wide = wide.cuda()
+            x = wide[:, :cols].float().cpu().numpy()
+            for transpose in (False, True):
+                s_ref, q_ref = ref.quantize(x.T if transpose else x)
+                qr, qc = (cols, rows) if transpose else (rows, cols)
+                n, b = gq.gq_mx4_sizes(qr, qc)
+                sc, q = _out(n), _out(b)
+                gq.gq_mx4_quantize([wide[:, :cols]], [sc], [q], transpose=transpose)
+                _same(sc[:n], s_ref, "scale")
+                _same(q[:b], q_ref, "codes")
+                _guards(sc, q)
+                out = torch.full((rows * cols + GUARD,), -7.0, device="cuda")
+                gq.gq_mx4_reduce_dequant([q[:b]], [sc[:n]], qr, qc, out)
+                _same_f32(out[:rows * cols], ref.reduce([s_ref], [q_ref], qc), "values")
+                assert bool((out[rows * cols:] == -7).all())
+
+
+def test_more_than_32_bits(gq):
+    """Places above 2^32: elements of one long row, pieces of many short rows,
+    and elements of the matrix that a product writes into.  The values are
+    +-2^e and +-1.5 * 2^e, which a block of one element holds exactly, and,
+    with e the same over a block, longer ones too."""
+    def values(n):
+        i = torch.arange(n, device="cuda", dtype=torch.int32)
+        x = torch.where((i & 1) == 0, 1.0, 1.5).bfloat16()
+        x *= torch.where((i & 64) == 0, 1.0, -1.0).bfloat16()
+        x *= torch.where((i & 4096) == 0, 1.0, 2.0 ** -9).bfloat16()
+        return x
+
+    tile = values(1 << 20)
+    n = (1 << 32) + 100
+    x = tile.repeat(n // tile.numel() + 1)[:n]
+    say("one row of", n)
+    ns, nc = gq.gq_mx4_sizes(1, n)
+    s, q = (torch.zeros(k, dtype=torch.uint8, device="cuda") for k in (ns, nc))
+    r = torch.zeros(n, device="cuda")
+    gq.gq_mx4_quantize([x], [s], [q])
+    gq.gq_mx4_reduce_dequant([q], [s], 1, n, r)
+    for lo in range(0, n, 1 << 30):
+        assert torch.equal(r[lo:lo + (1 << 30)], x[lo:lo + (1 << 30)].float()), lo
+    del x, s, q, r
+    torch.cuda.empty_cache()
+    rows = (1 << 30) + 77
+    x = tile.repeat(rows // tile.numel() + 1)[:rows].view(rows, 1)
+    say("rows of one", rows)
+    ns, nc = gq.gq_mx4_sizes(rows, 1)
+    s, q = (torch.zeros(k, dtype=torch.uint8, device="cuda") for k in (ns, nc))
+    r = torch.zeros(rows, device="cuda")
+    gq.gq_mx4_quantize([x], [s], [q])
+    gq.gq_mx4_reduce_dequant([q], [s], rows, 1, r)
+    assert torch.equal(r, x.view(-1).float())
+    del x, s, q, r
+    torch.cuda.empty_cache()
+    m, k, ldc = 70, 300, 1 << 26
+    say("product", m, m, k, "row stride", ldc)
+    rng = np.random.default_rng(13)
+    sa, qa = _random_codes(rng, m, k, 126, 129)
+    a = ref.decode(sa, qa, k)
+    big = torch.zeros(m * ldc, device="cuda")
+    gq.gq_mx4_product(_dev(qa), _dev(sa), _dev(qa), _dev(sa), k, big.view(m, ldc)[:, :m])
+    assert np.array_equal(big.view(m, ldc)[:, :m].double().cpu().numpy(), a @ a.T)
+    big.view(m, ldc)[:, :m] = 0
+    assert not bool(big.any())
+
+
+def test_two_streams_at_once(gq):
+    """Calls on two streams at once, which share their inputs and nothing
+    else, and each with a workspace of its own."""
+    rng = np.random.default_rng(14)
+    m, n, k = 100, 90, 6000
+    sa, qa = _random_codes(rng, m, k, 120, 130)
+    sb, qb = _random_codes(rng, n, k, 120, 130)
+    args = [_dev(v) for v in (qa, sa, qb, sb)]
+    need = gq.gq_mx4_product_workspace(m, n, k)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in streams]
+    c = [torch.zeros(m, n, device="cuda") for _ in streams]
+    want = torch.zeros(m, n, device="cuda")
+    gq.gq_mx4_product(*args, k, want, workspace=ws[0])
+    torch.cuda.synchronize()
+    for i in range(20):
+        for j, st in enumerate(streams):
+            gq.gq_mx4_product(*args, k, c[j], workspace=ws[j], stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(c[0], want) and torch.equal(c[1], want)
