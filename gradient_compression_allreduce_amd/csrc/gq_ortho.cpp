@@ -96,7 +96,7 @@ std::vector<OrTile> x_tiles(const std::vector<OrMat> &mats, int tile) {
 // where it is long and there are few tiles, for the joins of what was split,
 // and for Q.  Returns the number of partial sums.  K goes into parts of 1024
 // columns or more, as many as give two work groups per compute unit; 1024 x
-// 30522: see the figures at choose_tile.
+// 30522: see the figures at choose_tiles.
 int64_t g_tiles(const std::vector<OrMat> &mats, int tile, std::vector<OrTile> &gram,
                 std::vector<OrTile> &join, std::vector<OrTile> &poly) {
     int64_t total = 0, parts = 0;
@@ -139,27 +139,51 @@ int64_t g_tiles(const std::vector<OrMat> &mats, int tile, std::vector<OrTile> &g
     return parts;
 }
 
-// Tiles of the products: `s` x `s` of G and Q (their upper halves), or s x l
-// of X.  The largest that still gives the device enough of them: one work
-// group per compute unit with tiles of 256, two with tiles of 128.  Measured,
-// us a call of five steps on fp32 gradients with momentum, tiles of G / of X:
+// Tiles of the products: `g` of the s x s G and Q (their upper halves), `x` of
+// the s x l X.  Sides are rounded up to the larger.  A size must give the
+// device enough tiles: one work group per compute unit with tiles of 256, two
+// with tiles of 128 (64: any number).  Of the pairs that do, the one that takes
+// least time at the rates of the tile loops (128: 1.56 and 256: 1.78 times that
+// of 64, as one 8192 x 8192 shows), the padding counted.  Measured, us a call of
+// five steps on fp32 gradients with momentum, g / x:
 //                       64/64 128/128 256/256  the choice
 //   one 2048 x 2048       419     513     989  64/64
 //   4 of 1024 x 4096      699     652     996  64/256: 584
 //   16 of 1024 x 1024     857     691     696  128/256: 648
 //   one 4096 x 4096      2565    2012    2047  128/256: 1832
 //   one 8192 x 8192     20962   13479   11760  256/256
-int choose_tile(const int64_t *rows, const int64_t *cols, int64_t n, bool gram) {
-    for (const int t : {256, 128}) {
-        int64_t tiles = 0;
-        for (int64_t i = 0; i < n; ++i) {
-            const int64_t s = (std::min(rows[i], cols[i]) + t - 1) / t;
-            const int64_t l = (std::max(rows[i], cols[i]) + t - 1) / t;
-            tiles += gram ? s * (s + 1) / 2 : s * l;
+struct Tiles {
+    int g, x;
+};
+
+Tiles choose_tiles(const int64_t *rows, const int64_t *cols, int64_t n) {
+    const int size[3] = {64, 128, 256};
+    const double rate[3] = {1.0, 1.56, 1.78};
+    const int64_t enough[3] = {1, 2 * kCus, kCus};
+    Tiles best = {64, 64};
+    double least = 0.0;
+    for (int kg = 0; kg < 3; ++kg) {
+        for (int kx = 0; kx < 3; ++kx) {
+            const int64_t g = size[kg], x = size[kx], pad = std::max(g, x);
+            int64_t n_g = 0, n_x = 0;
+            double time = 0.0;
+            for (int64_t i = 0; i < n; ++i) {
+                const int64_t s = round_up(std::min(rows[i], cols[i]), pad);
+                const int64_t l = round_up(std::max(rows[i], cols[i]), pad);
+                const int64_t upper = s / g * (s / g + 1) / 2;
+                n_g += upper;
+                n_x += s / x * (l / x);
+                time += static_cast<double>(upper * g * g) * static_cast<double>(l + s) / rate[kg] +
+                        static_cast<double>(s * s) * static_cast<double>(l) / rate[kx];
+            }
+            if (n_g < enough[kg] || n_x < enough[kx]) continue;
+            if (least == 0.0 || time < least) {
+                least = time;
+                best = {static_cast<int>(g), static_cast<int>(x)};
+            }
         }
-        if (tiles >= (t == 256 ? kCus : 2 * kCus)) return t;
     }
-    return 64;
+    return best;
 }
 
 // Whether every matrix fits one work group.  64 x 147 (fp32, momentum, five
@@ -177,8 +201,8 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
                        float eps, const float *out_mul, gq_ortho **out) {
     std::vector<OrMat> mats(static_cast<size_t>(n_mats));
     const bool small = fits_small(h_rows, h_cols, n_mats);
-    const int tile_g = small ? 64 : choose_tile(h_rows, h_cols, n_mats, true);
-    const int tile_x = small ? 64 : choose_tile(h_rows, h_cols, n_mats, false);
+    const Tiles chosen = small ? Tiles{64, 64} : choose_tiles(h_rows, h_cols, n_mats);
+    const int tile_g = chosen.g, tile_x = chosen.x;
     const int tile = std::max(tile_g, tile_x);      // what the sides are rounded up to
     std::vector<OrTile> tab[OR_TABLES];
     int64_t at = 0, parts = 0;

@@ -80,6 +80,13 @@ __device__ __forceinline__ double block_sum(double v, double *sh) {
     return r;
 }
 
+// What takes u to X as it is stored, in binary64: the norm's reciprocal may lie
+// outside the range of binary32.  (A zero matrix stays zero without an eps, too.)
+__device__ __forceinline__ double or_mul(float scale, double sum, float eps) {
+    const double norm = __dsqrt_rn(sum) + static_cast<double>(eps);
+    return norm == 0.0 ? 0.0 : static_cast<double>(scale) / norm;
+}
+
 // ---- momentum and sums of squares ---------------------------------------------
 // A work group takes one chunk of a matrix, cut at multiples of four elements
 // of the flat buffers (whose starts are 16-byte aligned).
@@ -134,9 +141,7 @@ __global__ __launch_bounds__(OR_BLOCK) void k_ortho_cast(const OrArgs a) {
     double sum = 0.0;
     for (int i = threadIdx.x; i < mt.parts; i += OR_BLOCK) sum += a.part[mt.part + i];
     sum = block_sum(sum, sh);
-    // in binary64: the norm's reciprocal may lie outside the range of binary32
-    const double mul = static_cast<double>(mt.scale) /
-                       (__dsqrt_rn(sum) + static_cast<double>(a.eps));
+    const double mul = or_mul(mt.scale, sum, a.eps);
     const T *g = static_cast<const T *>(a.g);
     const int c = (threadIdx.x & 15) * 4;
     _Float16 *x = a.ws + mt.x[0];
@@ -495,8 +500,7 @@ __global__ __launch_bounds__(512) void k_ortho_small(const OrArgs a, const OrSte
     sum = 0.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += sh[i];
-    const double mul = static_cast<double>(mt.scale) /
-                       (__dsqrt_rn(sum) + static_cast<double>(a.eps));
+    const double mul = or_mul(mt.scale, sum, a.eps);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int piece = i * 8 + wave, r = piece / across, c = piece % across * 64 + lane;

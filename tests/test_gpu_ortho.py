@@ -266,3 +266,45 @@ def test_reduce_then_step_run(gq):
         step()
         torch.cuda.synchronize()
         assert torch.equal(out, first), i
+
+
+def test_zero_without_eps(gq):
+    """A zero matrix gives 0 with eps = 0 too, and leaves the others alone."""
+    rng = np.random.default_rng(15)
+    for shapes in ([(20, 30), (30, 20), (5, 5)], [(70, 300), (300, 70), (65, 65)]):
+        off, n = _plan_inputs(shapes, 0)
+        flat = rng.standard_normal(n).astype(np.float32)
+        flat[:off[1]] = 0.0
+        plan = gq.gq_ortho_create(shapes, eps=0.0)
+        res = torch.full((n,), 7.0, dtype=torch.float16, device="cuda")
+        gq.gq_ortho_step(plan, torch.from_numpy(flat).cuda(), res)
+        assert bool((res[:off[1]] == 0).all())
+        for o, (r, c) in list(zip(off, shapes))[1:]:
+            want, bound = iterate(flat[o:o + r * c].reshape(r, c).astype(np.float64), [COEF] * 5, 0.0)
+            _check(res[o:o + r * c].double().cpu().numpy().reshape(r, c), want, bound, "f16")
+
+
+def test_many_matrices_far_apart(gq):
+    """Hundreds of small matrices of few rows, and one whose elements lie
+    above 2^32 in the flat buffers."""
+    rng = np.random.default_rng(16)
+    shapes = [(64, 300)] * 150 + [(1, 400)] * 150 + [(90, 40)]
+    off, n = _plan_inputs(shapes, 0)
+    off[-1] += 1 << 32
+    n += 1 << 32
+    parts = [(rng.standard_normal(s) * 1e-3).astype(np.float32) for s in shapes]
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    for o, p in zip(off, parts):
+        g[o:o + p.size] = torch.from_numpy(p.reshape(-1)).cuda()
+    plan = gq.gq_ortho_create(shapes, off)
+    assert gq.gq_ortho_info(plan)["n"] == n
+    res = torch.full((n,), 7.0, dtype=torch.bfloat16, device="cuda")
+    gq.gq_ortho_step(plan, g, res)
+    for i in (0, 77, 149, 150, 151, 299, 300):
+        o, (r, c) = off[i], shapes[i]
+        say("matrix", i, r, c, "at", int(o))
+        u = g[o:o + r * c].double().cpu().numpy().reshape(r, c)
+        want, bound = iterate(u, [COEF] * 5)
+        _check(res[o:o + r * c].double().cpu().numpy().reshape(r, c), want, bound, "bf16")
+    end = off[-2] + 400
+    assert bool((res[end:end + (1 << 20)] == 7).all()) and bool((res[off[-1] - 1000:off[-1]] == 7).all())
