@@ -80,6 +80,7 @@ struct MmShape {
     // scale bytes of two steps: a plane for every one or two waves (with tiles
     // of 64 the planes of two waves are written and not read)
     static constexpr int SCALES = WM * WN / (T >= 128 ? 2 : 1) * 2048;
+    static constexpr int SCALE_LDS = QUAD ? 4 * SCALES : 2 * SCALES;    // what is held at one time
     // first row of instruction row i, and first column of block b
     static __device__ __forceinline__ int part_row(int wave, int i) {
         if (QUAD) return (i >> 2) * 128 + wave / WN * 64 + (i & 3) * 16;
@@ -221,7 +222,7 @@ __device__ __forceinline__ void mm_frag_cols(const char *lds, int c16, int lane,
     }
 }
 
-// Scale bytes of a tile's MX4 rows, for two steps (sixteen blocks) at a time.
+// Scale bytes of a tile's MX4 rows, by groups of two steps (sixteen blocks).
 // In LDS they lie in planes of up to 128 rows (P's, then Q's): the byte of
 // block b and row 16 i + r at ((b / 4 * 16 + r) * 4 + b % 4) * 8 + i.  The
 // scales of all a lane's operands of a half step are neighbours then, which
@@ -233,7 +234,7 @@ constexpr int MM_PLANE = 2048;
 
 struct MmScale {           // (the same for all lanes of a wave)
     const uint8_t *base;   // scales of the wave's operand, first row of the tile
-    const uint8_t *ahead;  // the same; with nb < 16 any bytes that can be read
+    const uint8_t *ahead;  // the same; with nb < 16 any 16 bytes that can be read
     int32_t pitch;         // nb; with nb < 16: 0
     int32_t rows;          // rows inside
     int32_t nb;
@@ -244,8 +245,8 @@ struct MmScale {           // (the same for all lanes of a wave)
     static __device__ __forceinline__ int block(int tid) { return (tid >> 4 & 3) * 4; }
 };
 
-// For operands of m and n rows (scales sp, sq), tile (i0, j0); any: four bytes
-// or more that can be read.
+// For operands of m and n rows (scales sp, sq), tile (i0, j0); any: 16 bytes
+// that can be read.
 template <typename S>
 __device__ __forceinline__ MmScale mm_scale_of(const uint8_t *sp, const uint8_t *sq, int64_t i0,
                                                int64_t j0, int64_t m, int64_t n, int64_t nb,
@@ -263,7 +264,7 @@ __device__ __forceinline__ MmScale mm_scale_of(const uint8_t *sp, const uint8_t 
     s.rows = static_cast<int32_t>(all - first < S::T ? all - first : S::T);
     s.nb = static_cast<int32_t>(nb);
     s.row = plane % HALF * 128 + quad * 64;
-    s.at = plane * MM_PLANE + quad * 4;
+    s.at = plane * MM_PLANE * (S::QUAD ? 4 : 1) + quad * 4;
     return s;
 }
 
@@ -312,6 +313,57 @@ __device__ __forceinline__ mm_u32x4 mm_scale_shift(mm_u32x4 v, const MmScale &s,
     return v >> by;
 }
 
+// Tiles of 256: the scales of four groups (2048 elements of K) at once.  16
+// bytes a row and group are an eighth of a line of the L2 cache each time, as
+// many requests as half the codes are.  At 8192 x 8192, us with K = 1024 / 8192 /
+// 32768: group by group 98 / 323 / 1130, four at once 84 / 297 / 1032.  A lane's
+// 16 bytes of four rows are one group's, so a wave's loads are of 64 bytes a
+// row.  (They are not held twice: the waves meet once more before new ones are
+// written.)
+struct MmScale4 {
+    mm_u32x4 v[4];      // byte k of row i: block k of the group
+};
+
+typedef mm_u32x4 __attribute__((aligned(1))) mm_u32x4_any;
+
+__device__ __forceinline__ int mm_scale4_block(int group) {
+    return (group + (mm_tid() >> 4 & 3)) * 16;
+}
+
+// Four groups of a row of 16 blocks or more: bytes that end no later than the
+// row, to be shifted down to the group's blocks when used.  Behind the last
+// group: bytes that nobody uses.
+__device__ __forceinline__ MmScale4 mm_scale4_load(const MmScale &s, int group) {
+    const int tid = mm_tid();
+    int b = mm_scale4_block(group);
+    b = b < s.pitch - 16 ? b : s.pitch - 16;
+    b = b < 0 ? 0 : b;
+    MmScale4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int row = s.row + s.r(tid) + 16 * i;
+        row = row < s.rows ? row : s.rows - 1;
+        w.v[i] = *reinterpret_cast<const mm_u32x4_any *>(s.ahead +
+                                                         static_cast<uint32_t>(row * s.pitch + b));
+    }
+    return w;
+}
+
+__device__ __forceinline__ void mm_scale4_shift(MmScale4 &w, const MmScale &s, int group) {
+    const int late = mm_scale4_block(group) - (s.nb - 16);
+    const int by = late <= 0 ? 0 : late < 16 ? late : 16;
+    const int bits = 8 * (by & 7);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t lo = (static_cast<uint64_t>(w.v[i][1]) << 32) | w.v[i][0];
+        const uint64_t hi = (static_cast<uint64_t>(w.v[i][3]) << 32) | w.v[i][2];
+        const uint64_t l = bits ? lo >> bits | hi << (64 - bits) : lo, h = hi >> bits;
+        const uint64_t x = by >= 16 ? 0 : by >= 8 ? h : l, y = by >= 8 ? 0 : h;
+        w.v[i] = mm_u32x4{static_cast<uint32_t>(x), static_cast<uint32_t>(x >> 32),
+                          static_cast<uint32_t>(y), static_cast<uint32_t>(y >> 32)};
+    }
+}
+
 // The bytes of rows 16 i + r for i in [first, first + F) (first a multiple of
 // F): F <= 4 in w[0], otherwise in both.  (Always one read of eight bytes:
 // of that one the compiler keeps what it may alias.)
@@ -319,7 +371,9 @@ template <int F>
 struct MmBytes {
     uint32_t w[2];
     __device__ __forceinline__ void read(const char *row, int first) {
-        const mm_u32x2 v = *reinterpret_cast<const mm_u32x2 *>(row);
+        pick(*reinterpret_cast<const mm_u32x2 *>(row), first);
+    }
+    __device__ __forceinline__ void pick(mm_u32x2 v, int first) {
         w[0] = v.x;
         w[1] = v.y;
         if (F <= 4) w[0] = (first & 4) ? v.y : v.x;
@@ -361,29 +415,66 @@ __device__ __forceinline__ void mm_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Writes the thread's scale bytes of a group to half `half` of the scales:
-// word k of block k, byte i of row i.  (in asm: of these writes the compiler
-// does not see which array they go to, and would wait for every load to LDS
-// first)
+// A 4 x 4 matrix of bytes turned: pairs of rows, then pairs of pairs.
+__device__ __forceinline__ mm_u32x4 mm_turn4(uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+    const uint32_t lo01 = __builtin_amdgcn_perm(v1, v0, 0x05010400u);
+    const uint32_t lo23 = __builtin_amdgcn_perm(v3, v2, 0x05010400u);
+    const uint32_t hi01 = __builtin_amdgcn_perm(v1, v0, 0x07030602u);
+    const uint32_t hi23 = __builtin_amdgcn_perm(v3, v2, 0x07030602u);
+    return mm_u32x4{__builtin_amdgcn_perm(lo23, lo01, 0x05040100u),
+                    __builtin_amdgcn_perm(lo23, lo01, 0x07060302u),
+                    __builtin_amdgcn_perm(hi23, hi01, 0x05040100u),
+                    __builtin_amdgcn_perm(hi23, hi01, 0x07060302u)};
+}
+
+// Writes the thread's scale bytes of four blocks: word k of block k (PITCH bytes
+// apart), byte i of row i.  (in asm: of these writes the compiler does not see
+// which array they go to, and would wait for every load to LDS first.  They have
+// to be waited for: mm_put_wait.)
+template <int OFFSET, int PITCH>
+__device__ __forceinline__ void mm_put_words(uint32_t at, mm_u32x4 w) {
+    asm volatile("ds_write_b32 %0, %1 offset:%5\n\tds_write_b32 %0, %2 offset:%6\n\t"
+                 "ds_write_b32 %0, %3 offset:%7\n\tds_write_b32 %0, %4 offset:%8"
+                 ::"v"(at), "v"(w[0]), "v"(w[1]), "v"(w[2]), "v"(w[3]), "n"(OFFSET),
+                 "n"(OFFSET + PITCH), "n"(OFFSET + 2 * PITCH), "n"(OFFSET + 3 * PITCH)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mm_put_wait() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// The thread's bytes of a group, to half `half` of the scales.
 template <typename S>
 __device__ __forceinline__ void mm_put_scale(const char *scale, int half, const MmScale &s,
                                              mm_u32x4 v) {
-    // a 4 x 4 matrix of bytes turned: pairs of rows, then pairs of pairs
-    const uint32_t lo01 = __builtin_amdgcn_perm(v[1], v[0], 0x05010400u);
-    const uint32_t lo23 = __builtin_amdgcn_perm(v[3], v[2], 0x05010400u);
-    const uint32_t hi01 = __builtin_amdgcn_perm(v[1], v[0], 0x07030602u);
-    const uint32_t hi23 = __builtin_amdgcn_perm(v[3], v[2], 0x07030602u);
-    const uint32_t w0 = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
-    const uint32_t w1 = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
-    const uint32_t w2 = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
-    const uint32_t w3 = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
     const int tid = mm_tid();
     const char *d = scale + half * S::SCALES + s.at + ((tid >> 4 & 3) * 64 + (tid & 15) * 4) * 8;
+    mm_put_words<0, 8>(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)d)),
+                       mm_turn4(v[0], v[1], v[2], v[3]));
+    mm_put_wait();
+}
+
+// The thread's bytes of four groups, each to a quarter of its plane.  Here the
+// byte of block b and row 16 i + r is at ((b / 8 * 4 + b % 4) * 16 + r) * 16 +
+// b / 4 % 2 * 8 + i: a lane reads both half steps' scales at once.
+__device__ __forceinline__ void mm_put_scale4(const char *scale, const MmScale &s,
+                                              const MmScale4 &w) {
+    const int tid = mm_tid();
+    const char *d = scale + s.at + (tid >> 4 & 3) * MM_PLANE + (tid & 15) * 16;
     const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)d));
-    asm volatile("ds_write_b32 %0, %1\n\tds_write_b32 %0, %2 offset:8\n\t"
-                 "ds_write_b32 %0, %3 offset:16\n\tds_write_b32 %0, %4 offset:24\n\t"
-                 "s_waitcnt lgkmcnt(0)" ::"v"(at), "v"(w0), "v"(w1), "v"(w2), "v"(w3)
-                 : "memory");
+    mm_put_words<0, 256>(at, mm_turn4(w.v[0][0], w.v[1][0], w.v[2][0], w.v[3][0]));
+    mm_put_words<8, 256>(at, mm_turn4(w.v[0][1], w.v[1][1], w.v[2][1], w.v[3][1]));
+    mm_put_words<1024, 256>(at, mm_turn4(w.v[0][2], w.v[1][2], w.v[2][2], w.v[3][2]));
+    mm_put_words<1032, 256>(at, mm_turn4(w.v[0][3], w.v[1][3], w.v[2][3], w.v[3][3]));
+    mm_put_wait();
+}
+
+// The same of rows of one group, of which the thread has four blocks.
+__device__ __forceinline__ void mm_put_scale4_few(const char *scale, const MmScale &s, mm_u32x4 v) {
+    const int tid = mm_tid(), c = tid >> 4 & 3;
+    const char *d = scale + s.at + (c >> 1) * 1024 + (tid & 15) * 16 + (c & 1) * 8;
+    mm_put_words<0, 256>(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((mm_lds_void *)d)),
+                         mm_turn4(v[0], v[1], v[2], v[3]));
+    mm_put_wait();
 }
 
 // c[i][j] += p[i] q[j] over one half step.
@@ -576,33 +667,25 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
     auto load_q = [&](char *s, int step, int h) { mm_load<128, S::THREADS>(q, s, step, 128 * h); };
     // one half of P (four instruction rows) and both of Q, of both half steps
     mm_i32x4 fp[2][4], fq[2][2][2];
-    uint32_t sp[2][2] = {}, sq[2][2] = {};
-    auto read_p = [&](const char *s, int half, int t, int h) {
+    mm_u32x4 sp = {}, sq[2] = {};      // their scales, as read: both half steps'
+    auto read_scale = [&](int plane, int quarter, int t, int lane) {
+        return *reinterpret_cast<const mm_u32x4 *>(scale + (plane * 4 + quarter) * MM_PLANE +
+                                                   t * 1024 + lane * 16);
+    };
+    auto read_p = [&](const char *s, int quarter, int t, int h) {
         const int lane = mm_tid() & 63;
+        if constexpr (MX) sp = read_scale(h, quarter, t, lane);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            if constexpr (MX) {
-                MmBytes<4> b;
-                const int at = half * S::SCALES + (2 * t + kk) * 512 + (lane & 15) * 32 +
-                               (lane >> 4) * 8;
-                b.read(scale + at + h * MM_PLANE, rm / 16);
-                sp[kk][0] = b.w[0];
-            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) fp[kk][i] = mm_frag(s, rm + 16 * i, kk, lane);
         }
     };
-    auto read_q = [&](const char *s, int half, int t, int h) {
+    auto read_q = [&](const char *s, int quarter, int t, int h) {
         const int lane = mm_tid() & 63;
+        if constexpr (MX) sq[h] = read_scale(2 + h, quarter, t, lane);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-            if constexpr (MX) {
-                MmBytes<2> b;
-                const int at = half * S::SCALES + (2 * t + kk) * 512 + (lane & 15) * 32 +
-                               (lane >> 4) * 8;
-                b.read(scale + at + (2 + h) * MM_PLANE, rn / 16);
-                sq[h][kk] = b.w[0];
-            }
             if constexpr (ROWS) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) fq[h][kk][j] = mm_frag(s, rn + 16 * j, kk, lane);
@@ -618,7 +701,11 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             mm_f32x4(&c)[4][2] = *reinterpret_cast<mm_f32x4(*)[4][2]>(&acc.c[b][4 * h]);
-            mm_block<MX>(fp[kk], fq[b][kk], sp[kk], sq[b][kk], c);
+            MmBytes<4> bp;
+            MmBytes<2> bq;
+            bp.pick(mm_u32x2{sp[2 * kk], sp[2 * kk + 1]}, rm / 16);
+            bq.pick(mm_u32x2{sq[b][2 * kk], sq[b][2 * kk + 1]}, rn / 16);
+            mm_block<MX>(fp[kk], fq[b][kk], bp.w, bq.w[0], c);
         }
         if constexpr (!std::is_same<X, MmNoExtra>::value)
             mm_pin(&acc.c[b][4 * h][0], std::integral_constant<int, 8>{});
@@ -628,13 +715,13 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
     // A step: each half is loaded again, for the step after next, once all
     // waves have read it into registers.  Loads are in the order P0 Q0 Q1 P1
     // of each step, and the waits leave those in flight that are not needed.
-    auto step_of = [&](char *p0, char *q0, char *q1, char *p1, char *other_p1, int step, int half,
+    auto step_of = [&](char *p0, char *q0, char *q1, char *p1, char *other_p1, int step, int quarter,
                        int t) {
         mm_wait<5 * L>();       // P0, Q0 here; Q1, P1 and three of the next step may not be
         mm_barrier();
         load_p(other_p1, step + 1, 1);
-        read_p(p0, half, t, 0);
-        read_q(q0, half, t, 0);
+        read_p(p0, quarter, t, 0);
+        read_q(q0, quarter, t, 0);
         extra(acc, q0, step, 0);
         __builtin_amdgcn_sched_barrier(0);
         quadrant(0, 0);
@@ -642,19 +729,27 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
         mm_barrier();
         load_p(p0, step + 2, 0);
         load_q(q0, step + 2, 0);
-        read_q(q1, half, t, 1);
+        read_q(q1, quarter, t, 1);
         extra(acc, q1, step, 1);
         __builtin_amdgcn_sched_barrier(0);
         quadrant(0, 1);
         mm_wait<6 * L>();       // P1
         mm_barrier();
         load_q(q1, step + 2, 1);
-        read_p(p1, half, t, 1);
+        read_p(p1, quarter, t, 1);
         __builtin_amdgcn_sched_barrier(0);
         quadrant(1, 1);
         quadrant(1, 0);
     };
-    if constexpr (MX) mm_put_scale<S>(scale, 0, sc, mm_scale_any(sc, group0));
+    if constexpr (MX) {
+        if (sc.nb < 16) {
+            mm_put_scale4_few(scale, sc, mm_scale_any(sc, 0));
+        } else {
+            MmScale4 w = mm_scale4_load(sc, group0);
+            mm_scale4_shift(w, sc, group0);
+            mm_put_scale4(scale, sc, w);
+        }
+    }
     const int first = 2 * group0;
     load_p(u.u0, first, 0);
     load_q(u.u1, first, 0);
@@ -663,16 +758,27 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
     load_p(u.u4, first + 1, 0);
     load_q(u.u5, first + 1, 0);
     load_q(u.u6, first + 1, 1);
-    for (int g = 0; g < groups; ++g) {
-        const int step = first + 2 * g, half = g & 1;
-        mm_u32x4 v;
-        step_of(u.u0, u.u1, u.u2, u.u3, u.u7, step, half, 0);
-        if constexpr (MX) v = mm_scale_load(sc, group0 + g + 1);
-        step_of(u.u4, u.u5, u.u6, u.u7, u.u3, step + 1, half, 1);
-        // into the other half, whose last readers passed this group's first
-        // barrier; written before the next barrier
-        if constexpr (MX)
-            mm_put_scale<S>(scale, (g + 1) & 1, sc, mm_scale_shift(v, sc, group0 + g + 1));
+    auto even = [&](int g) { step_of(u.u0, u.u1, u.u2, u.u3, u.u7, first + 2 * g, g & 3, 0); };
+    auto odd = [&](int g) { step_of(u.u4, u.u5, u.u6, u.u7, u.u3, first + 2 * g + 1, g & 3, 1); };
+    if constexpr (MX) {
+        for (int g0 = 0; g0 < groups; g0 += 4) {
+            const int last = groups - g0 < 4 ? groups - 1 : g0 + 3;
+            for (int g = g0; g < last; ++g) {
+                even(g);
+                odd(g);
+            }
+            even(last);
+            MmScale4 w = mm_scale4_load(sc, group0 + g0 + 4);
+            odd(last);
+            mm_barrier();       // all waves have read the last of the four groups
+            mm_scale4_shift(w, sc, group0 + g0 + 4);
+            mm_put_scale4(scale, sc, w);    // written before the next barrier
+        }
+    } else {
+        for (int g = 0; g < groups; ++g) {
+            even(g);
+            odd(g);
+        }
     }
     mm_wait<0>();
     __syncthreads();

@@ -63,7 +63,7 @@ __device__ __forceinline__ void store4(void *c, int64_t at, mm_f32x4 v, int n, b
 template <typename S, gq_dtype DT>
 __global__ __launch_bounds__(S::THREADS) void k_mx4_product(const MxPArgs a) {
     MM_LDS(S);
-    __shared__ __align__(128) char mm_scale[2 * S::SCALES];
+    __shared__ __align__(128) char mm_scale[S::SCALE_LDS];
     const int tm = static_cast<int>((a.m + S::T - 1) / S::T);
     const int tn = static_cast<int>((a.n + S::T - 1) / S::T);
     int t = mm_xcd(blockIdx.x, gridDim.x);
