@@ -32,7 +32,7 @@ gq_status check_product(const char *op, int64_t m, int64_t n, int64_t k) {
 }
 
 int64_t product_workspace(int64_t m, int64_t n, int64_t k) {
-    const MxPlan p = mx4_product_plan(m, n, k);
+    const MxPlan p = mx4_product_plan(m, n, k, true);
     return p.splits > 1 ? int64_t{4} * p.splits * m * n : 0;
 }
 

@@ -28,7 +28,8 @@ struct MxPArgs {
     int32_t add;
 };
 
-MxPlan mx4_product_plan(int64_t m, int64_t n, int64_t k);
+// split: K may be split (there is a workspace).
+MxPlan mx4_product_plan(int64_t m, int64_t n, int64_t k, bool split);
 hipError_t launch_mx4_product(const MxPArgs &a, int64_t k, gq_dtype dt, hipStream_t s);
 
 }  // namespace gq

@@ -148,34 +148,65 @@ hipError_t product_shape(const MxPArgs &a, gq_dtype dt, hipStream_t st) {
 
 }  // namespace
 
-// The tile and the number of parts of K for an m x n x k product: the
-// largest tile that gives every compute unit one, and where even the
-// smallest gives too few, K in as many parts (of at least 1024 elements
-// each) as fill them.
-MxPlan mx4_product_plan(int64_t m, int64_t n, int64_t k) {
+// The tile and the number of parts of K for an m x n x k product: of tiles of
+// 256, 128 and 64, with K whole or in as many parts (of 1024 elements or more)
+// as fill the compute units, the one that takes least time by
+//   start + work groups per compute unit * steps * step  (+ what the join moves),
+// start and step (256 elements of K) in us as they were measured alone.  Measured,
+// us, tile / parts (* the choice):
+//   1024 x 3000 x 1024      64/1  16.2   128/1  11.5*  256/1  17.2
+//   1000 x 2048 x 8192      64/1  36.4   128/1  34.2   128/2  29.5*  256/1  63
+//   1024 x 1024 x 16384     64/1  38.7   128/1  60.7   128/4  30.1*  256/1 115
+//   4096 x 1024 x 4096      64/1  39.4   128/1  22.8*  256/1  39.1   256/4  39.1
+//   4096 x 1024 x 16384     64/1 129     128/1  74.4   256/1 118     256/4  64.6*
+//   3500 x 4096 x 8192      64/1 205     128/1 108     256/1  74.1*  256/2 111
+//   7 x 30522 x 8192        64/1  36.3*  128/1  40.9   256/1  58.7   256/2  40.6
+//   512 x 512 x 8192        64/1  20.1    64/4  13.7*  128/1  33.2   256/1  63
+MxPlan mx4_product_plan(int64_t m, int64_t n, int64_t k, bool split) {
+    static const struct { int tile; double start, step; } kinds[3] = {
+        {256, 11.0, 1.85}, {128, 8.5, 1.0}, {64, 6.5, 0.52}};
+    constexpr double kJoin = 3.0, kBytes = 7e6;     // us a launch, bytes a us
     MxPArgs a{};
     a.m = m;
     a.n = n;
     const int64_t groups = ((k + MX_BLOCK - 1) / MX_BLOCK + 15) / 16;
-    MxPlan p{};
-    p.tile = tiles(a, 256) >= MX_CUS ? 256 : tiles(a, 128) >= MX_CUS ? 128 : 64;
-    const int64_t t = tiles(a, p.tile);
-    int64_t splits = t >= MX_CUS ? 1 : MX_CUS / t;
-    if (splits > groups / 2) splits = groups / 2;
-    if (splits < 1) splits = 1;
-    const int64_t per = (groups + splits - 1) / splits;
-    p.groups = static_cast<int32_t>(per);
-    p.splits = static_cast<int32_t>((groups + per - 1) / per);
-    return p;
+    MxPlan best{};
+    double least = 0.0;
+    for (const auto &kind : kinds) {
+        const int64_t t = tiles(a, kind.tile);
+        int64_t parts = split && t < MX_CUS ? MX_CUS / t : 1;
+        if (parts > groups / 2) parts = groups / 2;
+        for (const int64_t want : {int64_t{1}, parts}) {
+            if (want < 1) continue;
+            // (an even number of groups a part: the ring's rounds are of two)
+            const int64_t per = want == 1 ? groups : ((groups + want - 1) / want + 1) / 2 * 2;
+            const int64_t splits = (groups + per - 1) / per;
+            const double rounds = static_cast<double>((t * splits + MX_CUS - 1) / MX_CUS);
+            double us = kind.start + rounds * 2.0 * static_cast<double>(per) * kind.step;
+            if (splits > 1)
+                us += kJoin + static_cast<double>(2 * splits + 1) * 4.0 * static_cast<double>(m) *
+                                  static_cast<double>(n) / kBytes;
+            if (least == 0.0 || us < least) {
+                least = us;
+                best = {kind.tile, static_cast<int32_t>(splits), static_cast<int32_t>(per)};
+            }
+        }
+    }
+    return best;
 }
 
 hipError_t launch_mx4_product(const MxPArgs &in, int64_t k, gq_dtype dt, hipStream_t st) {
     MxPArgs a = in;
-    const MxPlan p = mx4_product_plan(a.m, a.n, k);
-    a.splits = a.part ? p.splits : 1;
-    a.groups = a.splits > 1 ? p.groups : static_cast<int32_t>((a.nb + 15) / 16);
+    const MxPlan p = mx4_product_plan(a.m, a.n, k, a.part != nullptr);
+    a.splits = p.splits;
+    a.groups = p.groups;
     if (p.tile == 256) return product_shape<MmBig>(a, dt, st);
     if (p.tile == 128) return product_shape<MmMid>(a, dt, st);
+    // Up to two tiles of 64 per compute unit: a ring of four buffers.  16 x 4096 x
+    // 16384 21.0 -> 16.0 us, 1024 x 1024 x 16384 53 -> 36 us; but its rounds are
+    // of two groups: 1024 x 1024 x 512 5.6 us, 6.3 on the ring.
+    const bool even = a.groups % 2 == 0 || a.groups > 4;
+    if (even && tiles(a, 64) * a.splits <= 2 * MX_CUS) return product_shape<MmFew>(a, dt, st);
     return product_shape<MmSmall>(a, dt, st);
 }
 
