@@ -28,9 +28,11 @@
 //     each of P and Q is two halves of 128 rows with buffers of their own, and
 //     the waves go through the four quadrants of C together, so a half's
 //     buffer is free again after the first quadrant that reads it and its
-//     next load starts then, one and a half steps ahead.  (fp16 at 8192^3:
-//     1.24-1.28 PFLOP/s, 1.21 with the two whole buffers, and 1.24 for the
-//     library's product; 4 bits: 3.9 PFLOP/s, 3.75.)
+//     next load starts then, one and a half steps ahead.  (The loop alone,
+//     fp16 at 8192^3: 1.24-1.28 PFLOP/s, 1.21 with the two whole buffers, and
+//     1.17-1.28 for the library's product.  The two waves of a SIMD taking
+//     turns, one reading while the other multiplies, with a barrier more for
+//     each quadrant: 5 percent slower in 4 bits and 3 - 7 in fp16.)
 #pragma once
 
 #include <hip/hip_runtime.h>

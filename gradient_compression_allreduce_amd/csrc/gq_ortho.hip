@@ -89,7 +89,8 @@ __device__ __forceinline__ double or_mul(float scale, double sum, float eps) {
 
 // ---- momentum and sums of squares ---------------------------------------------
 // A work group takes one chunk of a matrix, cut at multiples of four elements
-// of the flat buffers (whose starts are 16-byte aligned).
+// of the flat buffers (whose starts are 16-byte aligned).  Bound by HBM: 335M
+// fp16 gradients with momentum 575 us, 5.8 TB/s.
 template <typename T, bool MOM>
 __global__ __launch_bounds__(OR_BLOCK) void k_ortho_norm(const OrArgs a) {
     __shared__ double sh[OR_BLOCK / 64];
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(OR_BLOCK) void k_ortho_norm(const OrArgs a) {
 // A work group takes a 64 x 64 tile of the padded matrix as it lies in the
 // gradient, and writes it to X, turned in LDS where X is the transpose.  Each
 // work group adds up its matrix's partial sums itself, always in the same
-// order.
+// order.  Bound by HBM: 335M elements from the momentum 455 us, 4.4 TB/s.
 template <typename T, bool MOM>
 __global__ __launch_bounds__(OR_BLOCK) void k_ortho_cast(const OrArgs a) {
     __shared__ double sh[OR_BLOCK / 64];
@@ -291,6 +292,11 @@ struct AddX {
 //      OR_MM_LAST, OR_MM_LAST_BF16: the same into the caller's output
 //      OR_MM_JOIN: G from the partial sums that OR_MM_GRAM left of tiles whose
 //                  K it split, added in the order of K
+// 97 matrices of 1024 x 1024 and 48 of 1024 x 4096, tiles of 256, us a launch: G
+// 379 (0.81 PFLOP/s of the upper half), Q 258 (0.60), X 743 (0.83), the last X 751.
+// With K = 1024 a tile's loop is 16 steps, and filling the buffers and writing the
+// tile out are a third of its time (X without its loop 220, of that 150 the
+// stores); one work group per compute unit leaves nobody to cover them.
 template <typename S, int MODE>
 __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a) {
     MM_LDS(S);
