@@ -397,3 +397,42 @@ def test_two_streams_at_once(gq):
             gq.gq_mx4_product(*args, k, c[j], workspace=ws[j], stream=st)
     torch.cuda.synchronize()
     assert torch.equal(c[0], want) and torch.equal(c[1], want)
+
+
+def _exact_on_device(gq, m, n, k, split, seed):
+    """Scales 126 and 127: terms are multiples of 2^-4 of at most 36, and for
+    k <= 8192 their sums below 2^19, so every order of binary32 sums is exact,
+    this product's and the library's (of the decoded values) alike."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    nb = ref.blocks(k)
+
+    def operand(rows):
+        q = torch.randint(0, 256, (rows, nb * 16), dtype=torch.uint8, device="cuda", generator=gen)
+        left = k - 32 * (nb - 1)            # elements of the last block
+        last = q[:, (nb - 1) * 16:]
+        last[:, (left + 1) // 2:] = 0
+        if left % 2:
+            last[:, left // 2] &= 15
+        s = torch.randint(126, 128, (rows * nb,), dtype=torch.uint8, device="cuda", generator=gen)
+        x = torch.empty(rows, k, device="cuda")
+        gq.gq_mx4_reduce_dequant([q.reshape(-1)], [s], rows, k, x.view(-1))
+        return q.reshape(-1), s, x
+
+    qa, sa, a = operand(m)
+    qb, sb, b = operand(n)
+    c = torch.full((m, n), -7.0, device="cuda")
+    ws = None
+    if split:
+        ws = torch.empty(gq.gq_mx4_product_workspace(m, n, k) + 16, dtype=torch.uint8, device="cuda")
+    gq.gq_mx4_product(qa, sa, qb, sb, k, c, workspace=ws)
+    assert torch.equal(c, torch.mm(a, b.t().contiguous())), (m, n, k, split)
+
+
+def test_product_every_tile_and_length(gq):
+    """Few and many tiles of each size, with K whole and in parts, and lengths
+    around one, two, four and five groups of sixteen blocks."""
+    for m, n in ((40, 50), (300, 200), (1000, 1100), (1030, 3000), (3499, 4095)):
+        for k in (1, 100, 480, 511, 512, 530, 1100, 2047, 2048, 2049, 2100, 2600, 3500, 6200, 8192):
+            for split in (False, True):
+                say("exact on the device", m, n, k, "split", split)
+                _exact_on_device(gq, m, n, k, split, m + k)
