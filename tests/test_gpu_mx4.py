@@ -436,3 +436,27 @@ def test_product_every_tile_and_length(gq):
             for split in (False, True):
                 say("exact on the device", m, n, k, "split", split)
                 _exact_on_device(gq, m, n, k, split, m + k)
+
+
+def test_product_nan_scale_of_every_tile(gq):
+    """NaN scales in inner and in last rows and blocks reach their own row or
+    column and nothing else, whatever lies behind the matrix."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for m, n in ((40, 50), (1030, 3000), (3499, 4095)):
+        for k in (96, 500, 530, 2049, 2600):
+            say("nan", m, n, k)
+            nb = ref.blocks(k)
+            q = [torch.randint(0, 256, (r * nb * 16,), dtype=torch.uint8, device="cuda",
+                               generator=gen) for r in (m, n)]
+            s = [torch.full((r, nb), 127, dtype=torch.uint8, device="cuda") for r in (m, n)]
+            rows, cols = [3, 17, m - 1], [7, 20, n - 1]
+            for t, at in ((s[0], rows), (s[1], cols)):
+                t[at[0], 1] = 255
+                t[at[1], nb - 1] = 255
+                t[at[2], nb - 1] = 255
+            c = torch.zeros(m, n, device="cuda")
+            gq.gq_mx4_product(q[0], s[0].view(-1), q[1], s[1].view(-1), k, c)
+            want = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+            want[rows, :] = True
+            want[:, cols] = True
+            assert torch.equal(torch.isnan(c), want)
