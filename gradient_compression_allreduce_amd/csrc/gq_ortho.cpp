@@ -141,26 +141,30 @@ int64_t g_tiles(const std::vector<OrMat> &mats, int tile, std::vector<OrTile> &g
 
 // Tiles of the products: `g` of the s x s G and Q (their upper halves), `x` of
 // the s x l X.  Sides are rounded up to the larger.  A size must give the
-// device enough tiles: one work group per compute unit with tiles of 256, two
-// with tiles of 128 (64: any number).  Of the pairs that do, the one that takes
-// least time at the rates of the tile loops (128: 1.56 and 256: 1.78 times that
-// of 64, as one 8192 x 8192 shows), the padding counted.  (Without it 300 of 64 x
-// 512 took tiles of 256 and 690 us, not 168.)  Measured, us a call of
-// five steps on fp32 gradients with momentum, g / x:
-//                       64/64 128/128 256/256  the choice
-//   one 2048 x 2048       419     513     989  64/64
-//   4 of 1024 x 4096      699     652     996  64/256: 584
-//   16 of 1024 x 1024     857     691     696  128/256: 648
-//   one 4096 x 4096      2565    2012    2047  128/256: 1832
-//   one 8192 x 8192     20962   13479   11760  256/256
+// device enough tiles: one work group per compute unit with tiles of 256, nearly
+// two with tiles of 128 (64: any number).  Of the pairs that do, the one that
+// takes least time by what a tile costs a compute unit: its start (filling the
+// buffers, writing it out) and 64 of K a step, in us, fitted to times of the pairs
+// below.  Measured, us a call of five steps on fp32 gradients with momentum, g / x:
+//                            64/64  64/128 128/128 128/256 256/256
+//   one 2048 x 2048            419*            513             989
+//   4 of 1024 x 4096           699             652             996   (64/256: 584*)
+//   16 of 1024 x 1024          857             691     648*    696
+//   one 4096 x 4096           2565            2012    1832*   2047
+//   one 8192 x 8192          20962           13479           11760*
+//   24 of 768 x 768            579     547     489     453*
+//   36 of 256 x 2304           370     358*    414     429
+//   60 of 200 x 1000           274     263*    284     272
+//   300 of 64 x 512            168*                    690
+//   ResNet-152's 156          1247    1126*   1200    1228
 struct Tiles {
     int g, x;
 };
 
 Tiles choose_tiles(const int64_t *rows, const int64_t *cols, int64_t n) {
     const int size[3] = {64, 128, 256};
-    const double rate[3] = {1.0, 1.56, 1.78};
-    const int64_t enough[3] = {1, 2 * kCus, kCus};
+    const double start[3] = {0.5, 2.5, 15.0}, step[3] = {0.2, 0.65, 1.9};
+    const int64_t enough[3] = {1, 15 * kCus / 8, kCus};
     Tiles best = {64, 64};
     double least = 0.0;
     for (int kg = 0; kg < 3; ++kg) {
@@ -171,11 +175,14 @@ Tiles choose_tiles(const int64_t *rows, const int64_t *cols, int64_t n) {
             for (int64_t i = 0; i < n; ++i) {
                 const int64_t s = round_up(std::min(rows[i], cols[i]), pad);
                 const int64_t l = round_up(std::max(rows[i], cols[i]), pad);
-                const int64_t upper = s / g * (s / g + 1) / 2;
+                const int64_t upper = s / g * (s / g + 1) / 2, all = s / x * (l / x);
                 n_g += upper;
-                n_x += s / x * (l / x);
-                time += static_cast<double>(upper * g * g) * static_cast<double>(l + s) / rate[kg] +
-                        static_cast<double>(s * s) * static_cast<double>(l) / rate[kx];
+                n_x += all;
+                // G over l, Q and X over s
+                const double steps = static_cast<double>(l + s) / 64.0;
+                time += static_cast<double>(upper) * (2.0 * start[kg] + steps * step[kg]);
+                time += static_cast<double>(all) *
+                        (start[kx] + static_cast<double>(s) / 64.0 * step[kx]);
             }
             if (n_g < enough[kg] || n_x < enough[kx]) continue;
             if (least == 0.0 || time < least) {
