@@ -65,7 +65,7 @@ __device__ __forceinline__ uint32_t mx_byte(uint32_t m) {
 }
 
 // 2^(127 - s): what an element is multiplied by before it is coded.  0 for
-// a NaN block (its codes are cleared by mx_pack's caller).
+// a NaN block (the caller clears its codes).
 __device__ __forceinline__ float mx_mult(uint32_t s) {
     return s == 255u ? 0.0f : __uint_as_float((254u - s) << 23);
 }

@@ -244,7 +244,7 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
         m.part = static_cast<int32_t>(parts);
         m.parts = static_cast<int32_t>((elems + m.chunk - 1) / m.chunk);
         parts += m.parts;
-        for (int32_t p = 0; p < m.parts; ++p) 
+        for (int32_t p = 0; p < m.parts; ++p)
             tab[OR_NORM].push_back({static_cast<int32_t>(i), p, 0, -1, 0, 0});
         const int rp = m.tr ? m.lp : m.sp, cp = m.tr ? m.sp : m.lp;
         for (int r = 0; r < rp / OR_CAST_TILE; ++r)
