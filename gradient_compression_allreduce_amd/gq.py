@@ -208,18 +208,20 @@ def gq_version():
     return lib.gq_version().decode()
 
 
-_RAW = []
+_RAW = ()
 
 
 def _raw_stream():
     """torch's current stream on the current device, as an address.  (The
     stream object that torch.cuda.current_stream() makes costs 3 us, as much
     as the launch that follows; the address alone 0.2 us.)"""
+    global _RAW
     if not _RAW:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _RAW.append(raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
-        _RAW.append(getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
+        raw = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        dev = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _RAW = (raw, dev)      # whole at once: another thread may be here too
     return _RAW[0](_RAW[1]())
 
 
@@ -289,19 +291,21 @@ _TORCH = {}
 
 
 def _dt():
-    """(float32, float16, int8, int32, uint32, int64, float64) torch dtypes."""
+    """The torch dtypes that the guards accept, by kind."""
     if not _TORCH:
         import torch
-        _TORCH["f32"] = (torch.float32,)
-        _TORCH["f16"] = (torch.float16,)
-        _TORCH["grad"] = (torch.float32, torch.float16)
-        _TORCH["i8"] = (torch.int8,)
-        _TORCH["bits"] = (torch.int32, torch.uint32)
-        _TORCH["i64"] = (torch.int64,)
-        _TORCH["f64"] = (torch.float64,)
-        _TORCH["u8"] = (torch.uint8,)
-        _TORCH["half"] = (torch.float16, torch.bfloat16)
-        _TORCH["code"] = {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16}
+        _TORCH.update({     # whole at once: another thread may be here too
+            "f32": (torch.float32,),
+            "f16": (torch.float16,),
+            "grad": (torch.float32, torch.float16),
+            "i8": (torch.int8,),
+            "bits": (torch.int32, torch.uint32),
+            "i64": (torch.int64,),
+            "f64": (torch.float64,),
+            "u8": (torch.uint8,),
+            "half": (torch.float16, torch.bfloat16),
+            "code": {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16},
+        })
     return _TORCH
 
 
