@@ -36,7 +36,9 @@ namespace {
 constexpr int64_t kMaxSide = 1 << 22;       // longer side (buffer bounds are 32 bits)
 constexpr int64_t kMaxShort = 1 << 15;      // shorter side
 constexpr int64_t kMaxMats = 1 << 20;
-constexpr int64_t kMaxTiles = int64_t{1} << 22;
+// Elements of a plan, sides rounded up to its tile: 2^22 tiles of 64 x 64, whose
+// tables the host builds (24 bytes a tile).
+constexpr int64_t kMaxPadded = int64_t{1} << 34;
 constexpr int64_t kCus = 256;
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -212,6 +214,15 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
     const Tiles chosen = small ? Tiles{64, 64} : choose_tiles(h_rows, h_cols, n_mats);
     const int tile_g = chosen.g, tile_x = chosen.x;
     const int tile = std::max(tile_g, tile_x);      // what the sides are rounded up to
+    // (before any table is built: theirs are the sizes that this bounds)
+    int64_t padded = 0;
+    for (int64_t i = 0; i < n_mats && !small; ++i) {
+        padded += round_up(h_rows[i], tile) * round_up(h_cols[i], tile);
+        if (padded >= kMaxPadded)
+            return arg_fail(GQ_ERR_INVALID, op,
+                            "2^34 elements or more with sides rounded up to %d (matrix %lld)", tile,
+                            static_cast<long long>(i));
+    }
     std::vector<OrTile> tab[OR_TABLES];
     int64_t at = 0, parts = 0;
     for (int64_t i = 0; i < n_mats; ++i) {
@@ -250,9 +261,6 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
         for (int r = 0; r < rp / OR_CAST_TILE; ++r)
             for (int c = 0; c < cp / OR_CAST_TILE; ++c)
                 tab[OR_CAST].push_back({static_cast<int32_t>(i), r, c, -1, 0, 0});
-        if (static_cast<int64_t>(tab[OR_CAST].size()) >= kMaxTiles)
-            return arg_fail(GQ_ERR_INVALID, op, "more than %lld tiles: too many elements",
-                            static_cast<long long>(kMaxTiles));
     }
     int64_t sums = 0;
     if (!small) {

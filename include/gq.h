@@ -680,7 +680,10 @@ typedef struct gq_ortho gq_ortho;
  *             x cols, row-major and contiguous, from element h_off[i] of the
  *             flat buffers on; offsets increase and matrices do not overlap.
  *             Elements between them are neither read nor written.  The
- *             shorter side is at most 2^15, the longer at most 2^22.
+ *             shorter side is at most 2^15, the longer at most 2^22, and all
+ *             matrices together, each side rounded up to the plan's tile (64,
+ *             128 or 256), have less than 2^34 elements (a plan whose matrices
+ *             are all at most 64 by 256, either way round, has no such limit).
  * steps       1 .. GQ_ORTHO_MAX_STEPS.
  * coef        NULL: (3.4445, -4.7750, 2.0315) in every step; otherwise a host
  *             array of 3 * steps finite floats.
