@@ -407,11 +407,14 @@ __device__ __forceinline__ void mm_wait() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// (a barrier alone: what the waves hand each other is in LDS, put there by
-// loads that have been waited for and writes that have been, and buffers are
-// reused after reads whose results have been used)
+// What the waves hand each other is in LDS, put there by loads and writes that
+// have been waited for.  Buffers are loaded again behind a barrier, so a wave
+// waits for its own reads here, wherever the compiler has put the matrix
+// instructions that use them.  (In the loops as they are compiled all results
+// have been used by then, so the wait costs nothing.)
 __device__ __forceinline__ void mm_barrier() {
     __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -697,7 +700,8 @@ __device__ __forceinline__ void mm_quad(const MmRows &p, const Q &q, const MmSca
     };
     // quadrant (h, b): the instruction rows 4 h .. 4 h + 3 of block b.  (The
     // sums are marked as changed: matrix instructions touch no memory, and
-    // across a branch the compiler would move them past the next barrier.)
+    // across a branch the compiler would move them past the next barrier and
+    // hold their operands until then.)
     auto quadrant = [&](int h, int b) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
