@@ -386,6 +386,13 @@ gq_status gq_ortho_info(const gq_ortho *p, int64_t *n, int64_t *n_mats, int64_t 
     return arg_ok();
 }
 
+gq_status gq_ortho_tiles(const gq_ortho *p, int32_t *tile_g, int32_t *tile_x) {
+    if (!p) return arg_fail(GQ_ERR_INVALID, "gq_ortho_tiles", "plan is NULL");
+    if (tile_g) *tile_g = p->small ? 0 : p->tile_g;
+    if (tile_x) *tile_x = p->small ? 0 : p->tile_x;
+    return arg_ok();
+}
+
 gq_status gq_ortho_step(gq_ortho *p, const void *g, gq_dtype dt, float in_mul, float *momentum,
                         float mu, int32_t nesterov, gq_dtype out_dt, void *out, gq_stream stream) {
     const char *op = "gq_ortho_step";

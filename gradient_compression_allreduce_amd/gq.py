@@ -39,7 +39,7 @@ EXPORTS = ("gq_last_error", "gq_version", "gq_plan_chunks", "gq_units_create",
            "gq_chunker_destroy", "gq_chunker_update", "gq_chunker_predict", "gq_chunker_plan",
            "gq_mx4_sizes", "gq_mx4_quantize", "gq_mx4_reduce_dequant", "gq_mx4_reduce_requantize",
            "gq_mx4_product_workspace", "gq_mx4_product", "gq_ortho_create", "gq_ortho_destroy",
-           "gq_ortho_info", "gq_ortho_step")
+           "gq_ortho_info", "gq_ortho_tiles", "gq_ortho_step")
 GQ_STATS = 10
 STATS = ("max_abs_err", "max_abs_ref", "max_rel_err", "sum_abs_err", "sum_abs_ref",
          "mean_rel_err", "sum_dd", "sum_rr", "sum_dr", "cos")
@@ -146,6 +146,8 @@ def _load():
     L.gq_ortho_info.restype = st
     L.gq_ortho_info.argtypes = [vp, ctypes.POINTER(i64), ctypes.POINTER(i64), ctypes.POINTER(i64),
                                 ctypes.POINTER(i32)]
+    L.gq_ortho_tiles.restype = st
+    L.gq_ortho_tiles.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i32)]
     L.gq_ortho_step.restype = st
     L.gq_ortho_step.argtypes = [vp, vp, i32, f32, vp, f32, i32, i32, vp, vp]
     return L
@@ -937,6 +939,14 @@ def gq_ortho_info(plan):
     _check(lib.gq_ortho_info(plan.handle, ctypes.byref(n), ctypes.byref(c), ctypes.byref(b),
                              ctypes.byref(t)))
     return {"n": n.value, "n_mats": c.value, "bytes": b.value, "tile": t.value}
+
+
+def gq_ortho_tiles(plan):
+    """(rows and columns of a tile of G, of X) of a plan; (0, 0) where each
+    matrix takes one work group."""
+    g, x = ctypes.c_int32(0), ctypes.c_int32(0)
+    _check(lib.gq_ortho_tiles(plan.handle, ctypes.byref(g), ctypes.byref(x)))
+    return g.value, x.value
 
 
 def gq_ortho_step(plan, g, out, in_mul=1.0, momentum=None, mu=0.95, nesterov=True, stream=None):

@@ -707,6 +707,11 @@ gq_status gq_ortho_destroy(gq_ortho *p);
 gq_status gq_ortho_info(const gq_ortho *p, int64_t *n, int64_t *n_mats, int64_t *bytes,
                         int32_t *tile);
 
+/* Rows and columns of a tile of G and b G + c G G, and of X (informational);
+ * 0 and 0 for a plan whose matrices each take one work group.  Either pointer
+ * may be NULL. */
+gq_status gq_ortho_tiles(const gq_ortho *p, int32_t *tile_g, int32_t *tile_x);
+
 /*
  * gq_ortho_step -- one update of all of the plan's matrices.
  * g         device array of n elements of dt (GQ_F32, GQ_F16 or GQ_BF16),

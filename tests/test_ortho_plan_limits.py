@@ -46,3 +46,9 @@ def test_header_states_the_limit():
         text = f.read()
     doc = text[text.index("gq_ortho_create --"):text.index("gq_status gq_ortho_create(")]
     assert "2^34" in doc
+
+
+def test_tiles_of_no_plan():
+    from gradient_compression_allreduce_amd import gq
+    assert gq.lib.gq_ortho_tiles(None, None, None) == gq.GQ_ERR_INVALID
+    assert gq.gq_last_error().startswith("gq_ortho_tiles")
