@@ -11,9 +11,11 @@
 //   code = g * 2^(127 - s), an exact product except where it underflows to
 //          values far below 0.25, rounded half to even to a magnitude, above
 //          6 to 6 (the products are below 8); the sign is kept, of zeros too.
-// The conversions in both directions are the gfx950 instructions, which
-// agree with this definition for every code, every scale byte and every
-// value (checked exhaustively against it).
+// The conversions in both directions are the gfx950 instructions.
+// tests/test_gpu_mx4_conversions.py compares them with this definition for
+// every code at every scale byte, every binary32 magnitude below 8 at the
+// scale 1, and the ends of the rounding intervals with their neighbours at
+// every scale.
 #pragma once
 
 #include <hip/hip_runtime.h>
