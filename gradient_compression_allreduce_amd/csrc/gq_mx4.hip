@@ -60,16 +60,15 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
         __builtin_amdgcn_mov_dpp(static_cast<int>(v), CTRL, 0xf, 0xf, true));
 }
 
-// Max over aligned groups of 4, 8 or 32 lanes (every lane gets it): within
-// quads by quad permutes, then by mirrors of half rows and rows, whose other
-// half holds one value already.
+// Max over aligned groups of 4 or 8 lanes (every lane gets it): within quads by
+// quad permutes, then by the mirror of half a row, whose other half holds one
+// value already.
 template <int L>
 __device__ __forceinline__ uint32_t group_max(uint32_t m) {
+    static_assert(L == 4 || L == 8, "the lanes that hold a block");
     m = umax(m, dpp<0xB1>(m));                      // lanes 1 0 3 2
     m = umax(m, dpp<0x4E>(m));                      // lanes 2 3 0 1
-    if (L >= 8) m = umax(m, dpp<0x141>(m));         // half row mirrored
-    if (L >= 16) m = umax(m, dpp<0x140>(m));        // row mirrored
-    if (L >= 32) m = umax(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16, 64)));
+    if (L == 8) m = umax(m, dpp<0x141>(m));         // half row mirrored
     return m;
 }
 
