@@ -87,18 +87,6 @@ __device__ __forceinline__ double or_mul(float scale, double sum, float eps) {
     return norm == 0.0 ? 0.0 : static_cast<double>(scale) / norm;
 }
 
-// x to binary16 by way of binary32 but with one rounding: the 29 bits that a
-// binary32 number has no room for become one in its last bit, which then tells
-// x from the middle of two binary16 values.
-__device__ __forceinline__ _Float16 or_half(double x) {
-    constexpr uint32_t rest = 0x1fffffffu;
-    const uint64_t v = __builtin_bit_cast(uint64_t, x);
-    const uint32_t low = static_cast<uint32_t>(v);
-    const uint32_t odd = (low | ((low & rest) + rest)) & ~rest;
-    return static_cast<_Float16>(
-        static_cast<float>(__builtin_bit_cast(double, (v >> 32 << 32) | odd)));
-}
-
 // ---- momentum and sums of squares ---------------------------------------------
 // A work group takes one chunk of a matrix, cut at multiples of four elements
 // of the flat buffers (whose starts are 16-byte aligned).  Bound by HBM: 335M
@@ -162,11 +150,11 @@ __global__ __launch_bounds__(OR_BLOCK) void k_ortho_cast(const OrArgs a) {
     for (int i = 0; i < 4; ++i) {
         const int r = (threadIdx.x >> 4) + 16 * i;
         const int row = t.i * OR_CAST_TILE + r, col = t.j * OR_CAST_TILE + c;
-        f16x4 h = {};
+        f32x4 u = {0.f, 0.f, 0.f, 0.f};
         if (row < mt.rows) {
             const int64_t e = mt.off + static_cast<int64_t>(row) * mt.cols + col;
             const int n = mt.cols - col;    // elements of the row from col on
-            f32x4 gv = {0.f, 0.f, 0.f, 0.f}, mv = gv;
+            f32x4 gv = u, mv = u;
             const bool need_g = !MOM || a.nesterov;
             if (mt.align > 1 && n >= 4) {
                 if (need_g) gv = load4(g, e, e, e + 4);
@@ -182,11 +170,14 @@ __global__ __launch_bounds__(OR_BLOCK) void k_ortho_cast(const OrArgs a) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float gk = __fmul_rn(gv[k], a.in_mul);
-                const float u = !MOM ? gk : a.nesterov ? __fadd_rn(gk, __fmul_rn(a.mu, mv[k])) : mv[k];
+                u[k] = !MOM ? gk : a.nesterov ? __fadd_rn(gk, __fmul_rn(a.mu, mv[k])) : mv[k];
                 // nothing where there is no element, whatever the norm
-                h[k] = or_half(k < n ? u * mul : 0.0);
+                u[k] = k < n ? static_cast<float>(u[k] * mul) : 0.0f;
             }
         }
+        f16x4 h;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = static_cast<_Float16>(u[k]);
         if (mt.tr) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) turn[c + k][r] = h[k];
@@ -521,7 +512,7 @@ __global__ __launch_bounds__(512) void k_ortho_small(const OrArgs a, const OrSte
         const int piece = i * 8 + wave, r = piece / across, c = piece % across * 64 + lane;
         // zeros around the matrix, whatever the norm
         const bool in = r < rows && c < cols;
-        const _Float16 h = or_half(in ? u[i] * mul : 0.0);
+        const _Float16 h = static_cast<_Float16>(in ? static_cast<float>(u[i] * mul) : 0.0f);
         const int xr = mt.tr ? c : r, xc = mt.tr ? r : c;
         if (xc < lp) *reinterpret_cast<_Float16 *>(xs + sm_at(xr, xc, lp)) = h;
     }
