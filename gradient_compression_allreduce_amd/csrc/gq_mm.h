@@ -12,7 +12,7 @@
 //   * Loads go from global memory to LDS with no register in between
 //     (16 bytes per lane).  Rows, columns and chunks outside the matrix read as
 //     zeros by the buffer descriptor's bound; the number of steps is rounded
-//     up to an even one.
+//     up to an even one (on a ring of four buffers to a multiple of four).
 //   * In LDS the eight 16-byte chunks of row r are stored at chunk ^ (r & 7).
 //     A 16-byte LDS read serves the lanes 0-3, 12-15 and 20-27 together (and
 //     so on): with this order those sixteen fall into different banks.  A
@@ -20,8 +20,9 @@
 //     on the global side, in which chunk a lane asks for.
 //   * The instruction's first operand is Q and its second P: a lane then
 //     holds four consecutive columns of one row of C.
-//   * mm_two (tiles of 128 and 64): two buffers of a step each; two or five
-//     work groups per compute unit cover each other's waits.  On a ring of
+//   * mm_two (tiles of 128 and 64): two buffers of a step each; two work groups
+//     per compute unit with tiles of 128, five with tiles of 64 (three in MX4,
+//     whose scales take 16 KiB more) cover each other's waits.  On a ring of
 //     four buffers instead (tiles of 64 where there are few of them and latency
 //     counts) the loads run three steps ahead.
 //   * mm_quad (tiles of 256, one work group of eight waves per compute unit):
@@ -562,7 +563,7 @@ struct MmNoExtra {
 };
 
 // acc += the steps [2 * group0, 2 * (group0 + groups)) of the tile's product.
-// MX: the operands are MX4 and `scale` is an LDS array of 2 * S::SCALES bytes.
+// MX: the operands are MX4 and `scale` is an LDS array of S::SCALE_LDS bytes.
 // extra(acc, q, step, b) is called where the step's Q rows of block b lie at
 // q.  Every load has landed on return, and all waves have passed their last
 // read.
