@@ -26,6 +26,8 @@ struct gq_ortho {
     _Float16 *d_ws = nullptr;
     double *d_part = nullptr;
     float *d_sums = nullptr;       // partial sums of G where its K is split
+    float *d_diag = nullptr;
+    uint8_t *d_low = nullptr;
     OrMat *d_mats = nullptr;
     OrTile *d_tiles[OR_TABLES] = {};
     int64_t n_tiles[OR_TABLES] = {};
@@ -224,7 +226,7 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
                             static_cast<long long>(i));
     }
     std::vector<OrTile> tab[OR_TABLES];
-    int64_t at = 0, parts = 0;
+    int64_t at = 0, parts = 0, diags = 0, lows = 0;
     for (int64_t i = 0; i < n_mats; ++i) {
         OrMat &m = mats[static_cast<size_t>(i)];
         std::memset(&m, 0, sizeof m);
@@ -249,6 +251,10 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
         at += al;
         m.b = at;
         at += al;
+        m.low = lows;
+        if (steps >= OR_LOW_STEPS) lows += xl;
+        m.diag = diags;
+        diags += 2 * static_cast<int64_t>(m.sp);
         // at most 1024 partial sums a matrix, of at least 8192 elements
         const int64_t elems = (m.off & 3) + static_cast<int64_t>(m.rows) * m.cols;
         m.chunk = std::max<int64_t>(8192, round_up((elems + 1023) / 1024, 4));
@@ -285,6 +291,10 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
     size += round_up(parts * 8, 256);
     const int64_t sums_at = size;
     size += sums * tile_g * tile_g * 4;
+    const int64_t diag_at = size;
+    size += round_up(diags * 4, 256);
+    const int64_t low_at = size;
+    size += round_up(lows, 256);
     const int64_t mats_at = size;
     size += round_up(static_cast<int64_t>(mats.size() * sizeof(OrMat)), 256);
     int64_t tab_at[OR_TABLES];
@@ -299,6 +309,8 @@ gq_status ortho_create(const char *op, const int64_t *h_off, const int64_t *h_ro
         P->d_ws = reinterpret_cast<_Float16 *>(P->d_mem);
         P->d_part = reinterpret_cast<double *>(P->d_mem + part_at);
         P->d_sums = reinterpret_cast<float *>(P->d_mem + sums_at);
+        P->d_diag = reinterpret_cast<float *>(P->d_mem + diag_at);
+        P->d_low = reinterpret_cast<uint8_t *>(P->d_mem + low_at);
         P->d_mats = reinterpret_cast<OrMat *>(P->d_mem + mats_at);
         e = hipMemcpy(P->d_mats, mats.data(), mats.size() * sizeof(OrMat), hipMemcpyHostToDevice);
     }
@@ -422,6 +434,10 @@ gq_status gq_ortho_step(gq_ortho *p, const void *g, gq_dtype dt, float in_mul, f
     a.ws = p->d_ws;
     a.part = p->d_part;
     a.sums = p->d_sums;
+    a.diag = p->d_diag;
+    a.low = p->d_low;
+    a.tile_x = p->tile_x;
+    a.low_out = p->steps >= OR_LOW_STEPS;
     a.g = g;
     a.m = momentum;
     a.out = out;
@@ -440,6 +456,8 @@ gq_status gq_ortho_step(gq_ortho *p, const void *g, gq_dtype dt, float in_mul, f
         a.b = p->coef.coef[3 * k + 1];
         a.c = p->coef.coef[3 * k + 2];
         a.cur = k & 1;
+        a.low_in = p->steps - k >= OR_LOW_STEPS;
+        a.low_out = p->steps - k - 1 >= OR_LOW_STEPS;
         a.tiles = p->d_tiles[OR_GRAM];
         e = launch_ortho_mm(a, p->n_tiles[OR_GRAM], p->tile_g, OR_MM_GRAM, out_dt, st);
         a.tiles = p->d_tiles[OR_JOIN];

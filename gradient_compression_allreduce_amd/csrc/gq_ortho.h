@@ -12,12 +12,17 @@ namespace gq {
 // One matrix of a plan.  X is the matrix itself or, where it has more rows
 // than columns, its transpose: s x l with s <= l, padded with zeros to
 // sp x lp (multiples of the plan's tile).  Offsets are fp16 elements of the
-// plan's workspace; X is held twice, read and written in turn.
+// plan's workspace.  X is the sum of two numbers: x, in fp16, which the products
+// read, held twice, read and written in turn; and y, most of what x leaves of
+// it, in 8 bits (gq_ortho.hip), which only the tile's own work group reads and
+// writes.
 struct OrMat {
     int64_t off;        // first element in the flat gradient, momentum and output
     int64_t x[2];       // [sp][lp]
     int64_t a;          // [sp][sp]
     int64_t b;          // [sp][sp]
+    int64_t low;        // bytes: y, [tiles of X][tile * tile], a tile as or_quad orders it
+    int64_t diag;       // floats: the diagonals of G and of Q, sp each
     int64_t chunk;      // elements (a multiple of 4) per partial sum of squares
     int32_t rows, cols;
     int32_t s, l, sp, lp;
@@ -44,6 +49,8 @@ struct OrArgs {
     _Float16 *ws;
     double *part;
     float *sums;        // partial sums of tiles of G, tile * tile floats each
+    float *diag;
+    uint8_t *low;
     const void *g;
     float *m;           // NULL: no momentum
     void *out;
@@ -51,6 +58,9 @@ struct OrArgs {
     float a, b, c;      // the step's coefficients
     int32_t nesterov;
     int32_t cur;        // which of x[] is read
+    int32_t tile_x;     // of X
+    int32_t low_in;     // whether the X that is read has a y, and the one written
+    int32_t low_out;
 };
 
 // The coefficients (a, b, c) of every step.
@@ -65,6 +75,8 @@ enum OrMode {
 };
 
 constexpr int OR_CAST_TILE = 64;
+// X has a y while at least this many steps are to come.
+constexpr int OR_LOW_STEPS = 3;
 
 hipError_t launch_ortho_norm(const OrArgs &a, int64_t n, gq_dtype dt, hipStream_t s);
 hipError_t launch_ortho_cast(const OrArgs &a, int64_t n, gq_dtype dt, hipStream_t s);

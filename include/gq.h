@@ -663,13 +663,15 @@ gq_status gq_mx4_product(const uint8_t *a, const uint8_t *a_scale, const uint8_t
  *     G = X X^T;  X <- a X + (b G + c G G) X
  *     (on the transpose where a matrix has more rows than columns)
  *   out = out_mul * X
- * X, G and b G + c G G are rounded to binary16 each time they are stored;
- * products are summed in binary32.  A rounding of X (2^-12 of its norm) grows
- * by at most the step's largest slope, a = 3.4445 for singular values near 0
- * in the default coefficients: for gradients whose small singular values are
- * below about 1/500 of the largest, those directions of the result carry
- * that noise.  A zero matrix gives 0; inf or NaN makes its own matrix NaN and
- * no other. */
+ * G and b G + c G G are rounded to binary16 each time they are stored, but for
+ * their diagonals, which are binary32.  Products take X rounded to binary16;
+ * X itself keeps 5 bits more while three steps or more are to come, and is
+ * binary32 where a plan takes one work group per matrix.  Products are summed
+ * in binary32.  For the default
+ * coefficients the result is 4e-4 to 1e-3 (Frobenius norm) from the exact
+ * iteration's, 2e-3 to 4e-3 where the gradient's directions beyond the first few
+ * have 1/256 of its norm, and the output's rounding more.  A zero matrix gives 0;
+ * inf or NaN makes its own matrix NaN and no other. */
 
 typedef struct gq_ortho gq_ortho;
 
@@ -689,7 +691,7 @@ typedef struct gq_ortho gq_ortho;
  *             array of 3 * steps finite floats.
  * eps         finite, >= 0 (a common choice is 1e-7).
  * out_mul     NULL (1), or a host array of n_mats finite floats.
- * Allocates device memory (about 4 bytes per element, and 4 per element of
+ * Allocates device memory (about 5 bytes per element, and 4 per element of
  * the square of each shorter side, sides rounded up to the tile) and
  * synchronizes.  Errors: GQ_ERR_INVALID, GQ_ERR_HIP.
  */

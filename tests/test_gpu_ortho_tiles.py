@@ -5,8 +5,11 @@ Exact cases.  X holds 4^k entries of +-2^-k and zeros, so the norm is exact.
 With the coefficients (3, -2, 256) and k = 5 or 6, G = X X^T, Q = -2 G + 256 G G
 and 3 X + Q X are whole multiples of 2^(-2k), 2^(8-4k) and 2^(8-5k) and stay
 below 2^24 of them (asserted for every matrix), so every binary32 sum is exact
-in any order, and G, Q, X and the output are fixed to the bit by one rounding
-each.  Steps with (1, 0, 0) before and behind hand X on.
+in any order.  The results are then fixed to the bit by the roundings of what is
+stored: G and Q in binary16 but for their diagonals, X in binary16 and, while
+three steps or more are to come, 8 bits of what that leaves, and the output.
+Steps with (1, 0, 0) before and behind, and one with (3, 0, 0) that shows the 8
+bits, hand X on.
 """
 import numpy as np
 import pytest
@@ -62,11 +65,18 @@ def _want(x, k, out_mul, out):
     x = (x.t().contiguous() if tr else x).double() * 2.0 ** -k
     l = x.shape[1]
     scale = 2.0 ** float(np.round(0.5 * np.log2(np.float32(l))))
-    g = _f32(x @ x.t().contiguous()).half().double()
-    assert torch.equal(_f32(g @ g).double(), g @ g)
-    q = _f32(B * g + C * (g @ g)).half().double()
-    new = _f32(A * x + q @ x).double()
-    new = _f32(new * scale).half().double()
+    g = _f32(x @ x.t().contiguous()).double()
+    assert torch.equal(g.half().double(), g)        # (its diagonal is stored apart)
+    q = _f32(B * g + C * (g @ g)).double()
+    d = q.diagonal().clone()
+    q = q.half().double()
+    _f32(A + d)
+    q.diagonal().copy_(d)
+    new = _f32((A * x + q @ x) * scale)
+    hi = new.half()
+    low = ((new - hi.float()) * 2.0 ** 14).clamp(-448, 448).to(torch.float8_e4m3fn)
+    new = _f32(hi.double() + low.double() * 2.0 ** -14).double()
+    new = _f32(3 * new).half().double()
     res = _f32(new / scale * out_mul).to(TORCH[out])
     return res.t().contiguous() if tr else res
 
@@ -77,7 +87,7 @@ def test_every_tile_exactly(gq, n):
     gen = torch.Generator(device="cuda").manual_seed(n)
     # 64 out: the smallest entries stay normal in binary16
     mul = [64.0 * (1 + i % 2) for i in range(len(shapes))]
-    coef = [(1, 0, 0), (A, B, C), (1, 0, 0)]
+    coef = [(1, 0, 0), (A, B, C), (3, 0, 0), (1, 0, 0), (1, 0, 0)]
     for gap, dt, out, mom, nesterov in ((0, "f32", "bf16", True, True), (3, "f16", "f16", False, False),
                                         (8, "bf16", "f16", True, False), (4, "f32", "f16", False, True)):
         say("tiles", tiles, len(shapes), "matrices, gap", gap, dt, out, mom, nesterov)
@@ -90,7 +100,7 @@ def test_every_tile_exactly(gq, n):
         g = g.to(TORCH[dt])
         m = torch.full((total,), float("nan"), device="cuda") if mom else None
         res = torch.full((total,), 77.0, dtype=TORCH[out], device="cuda")
-        plan = gq.gq_ortho_create(shapes, off, steps=3, coef=coef, eps=0.0, out_mul=mul)
+        plan = gq.gq_ortho_create(shapes, off, steps=5, coef=coef, eps=0.0, out_mul=mul)
         assert gq.gq_ortho_tiles(plan) == tiles
         for again in range(2):          # the plan's workspace is used again
             if mom:
