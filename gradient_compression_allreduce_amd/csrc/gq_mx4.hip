@@ -79,7 +79,7 @@ __device__ __forceinline__ uint32_t group_max(uint32_t m) {
 // slots are counted up to whole blocks; those past its end read as zeros.
 // Rows may start at any element: a slot is one load of 16 bytes either way, and
 // the last, short one of a row is the 16 bytes that end with the row, shifted.
-// 8 ranks of 60.2M fp32: 345 us, 6.3 TB/s (fp16, 8 of 335M: 1.17 ms, 5.8 TB/s); rows
+// 8 ranks of 60.2M fp32: 352 us, 6.2 TB/s (fp16, 8 of 335M: 1.17 ms, 5.8 TB/s); rows
 // of 4100 bf16, 8191 of them: 16 us, 5.2 TB/s (an element per lane: 52 us).
 
 // The bytes of v from byte n on (0 < n < 16), zeros behind them.
@@ -282,8 +282,8 @@ __global__ __launch_bounds__(64 * MXT_BLOCKS) void k_mx4_quantize_cols(const MxQ
 // need the lane's own maximum only.  The sums leave through the wave's 8 KiB
 // of LDS, so that the wave's stores of 16 bytes per lane are contiguous.
 // FLAT: rows == 1 or whole blocks, so the sums are one 16-byte aligned array.
-// Bound by HBM: 8 ranks of 60.2M with sum and codes 80 us, 6.6 TB/s; one rank's
-// sum alone (decoding) 47 us, 5.8 TB/s; decoding 8191 rows of 4100 29 us, 5.2 TB/s
+// Bound by HBM: 8 ranks of 60.2M with sum and codes 78 us, 6.8 TB/s; one rank's
+// sum alone (decoding) 47 us, 5.7 TB/s; decoding 8191 rows of 4100 29 us, 5.2 TB/s
 // (with 4-byte stores, a division each, 52 us).
 template <bool SUM, bool CODES, bool FLAT>
 __global__ __launch_bounds__(MXR_BLOCK) void k_mx4_reduce(const MxRArgs a) {

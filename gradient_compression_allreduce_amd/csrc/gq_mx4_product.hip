@@ -5,11 +5,14 @@
 //   k_mx4_product  a tile of C; or, where C has too few tiles to fill the
 //                  device, the tile's share of K into a partial C of its own;
 //   k_mx4_join     adds the partial sums in the order of K.
-// Measured: 8192^3 297 - 315 us, 3.5 - 3.7 PFLOP/s; 4096 x 1024 x 16384 49 us in four
-// parts and 15 to join them, 2.2 PFLOP/s; 1024 x 1024 x 512 added to fp32 5.6 us; 7 x 30522 x 1024 9.1 us.  The large
-// ones are bound by the way of the codes from the L2 cache over LDS into the
-// registers: without its matrix instructions the loop of tiles of 256 takes 1.9
-// of 2.1 us a step, without the loads to LDS 1.7.
+// Measured, medians of 200 launches in a kernel trace: 8192^3 294 us, 3.7 PFLOP/s
+// (events over calls in a row 297 - 309, with inputs that are not in the cache 317;
+// the first launches after a pause up to 390); 4096 x 1024 x 16384 50 us in four
+// parts and 15 to join them, 2.1 PFLOP/s; 1024 x 1024 x 512 added to fp32 6.4 us;
+// 7 x 30522 x 1024 9.7 us.  8192 x 8192 with K = 1024 takes 85 us and each further
+// 256 of K 7.8, 4.4 PFLOP/s: the loop runs near the instructions' rate, and 54 us do
+// not depend on K, four rounds of filling the buffers and storing C with one work
+// group per compute unit.
 #include <hip/hip_fp16.h>
 
 #include "gq_mm.h"

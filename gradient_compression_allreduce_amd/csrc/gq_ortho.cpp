@@ -100,7 +100,7 @@ std::vector<OrTile> x_tiles(const std::vector<OrMat> &mats, int tile) {
 // where it is long and there are few tiles, for the joins of what was split,
 // and for Q.  Returns the number of partial sums.  K goes into parts of 1024
 // columns or more, as many as give two work groups per compute unit (128 x 30522,
-// fp32, momentum, five steps: 738 us with K whole, 188 in parts).
+// fp32, momentum, five steps: 738 us with K whole, 191 in parts).
 int64_t g_tiles(const std::vector<OrMat> &mats, int tile, std::vector<OrTile> &gram,
                 std::vector<OrTile> &join, std::vector<OrTile> &poly) {
     int64_t total = 0, parts = 0;
@@ -148,19 +148,22 @@ int64_t g_tiles(const std::vector<OrMat> &mats, int tile, std::vector<OrTile> &g
 // device enough tiles: one work group per compute unit with tiles of 256, nearly
 // two with tiles of 128 (64: any number).  Of the pairs that do, the one that
 // takes least time by what a tile costs a compute unit: its start (filling the
-// buffers, writing it out) and 64 of K a step, in us, fitted to times of the pairs
-// below.  Measured, us a call of five steps on fp32 gradients with momentum, g / x:
-//                            64/64  64/128 128/128 128/256 256/256
-//   one 2048 x 2048            419*            513             989
-//   4 of 1024 x 4096           699             652             996   (64/256: 584*)
-//   16 of 1024 x 1024          857             691     648*    696
-//   one 4096 x 4096           2565            2012    1832*   2047
-//   one 8192 x 8192          20962           13479           11760*
-//   24 of 768 x 768            579     547     489     453*
-//   36 of 256 x 2304           370     358*    414     429
-//   60 of 200 x 1000           274     263*    284     272
-//   300 of 64 x 512            168*                    690
-//   ResNet-152's 156          1247    1126*   1200    1228
+// buffers, writing it out) and 64 of K a step, in us, fitted to times of the pairs.
+// Measured, us a call of five steps on fp32 gradients with momentum, all pairs of a
+// row in turn, medians, g / x (* the choice; 24 of 768 x 768 on 128/256 have 216
+// tiles of X, too few by the rule, and 8 percent less time):
+//                       64/64  64/128  64/256 128/128 128/256 256/256
+//   one 2048 x 2048       422*    437     612     499     670    1027
+//   4 of 1024 x 4096      663     602     551*    668     615    1011
+//   16 of 1024 x 1024     826     755     706     717     670*    696
+//   one 4096 x 4096      2487    2205    2029    1989    1821*   1982
+//   one 8192 x 8192     21010   18972   17506   13623   12198   11710*
+//   24 of 768 x 768       576     552     513     502*    463     580
+//   36 of 256 x 2304      393     388*    400     462     476     681
+//   60 of 200 x 1000      292     281*    267     311     296     428
+//   300 of 64 x 512       186*    272     652     303     648     786
+//   ResNet-152's 156     1337    1220*   1250    1291    1319    1600
+//   BERT-Large's 145    13091   11308   10465    9760    8950    8769*
 struct Tiles {
     int g, x;
 };
@@ -199,7 +202,7 @@ Tiles choose_tiles(const int64_t *rows, const int64_t *cols, int64_t n) {
 }
 
 // Whether every matrix fits one work group.  64 x 147 (fp32, momentum, five
-// steps): 26 us in one launch, 64 us in 17 of tiles, which the host takes 53 us
+// steps): 23 us in one launch, 64 us in 17 of tiles, which the host takes 53 us
 // to issue.  (64 x 1024 would take 141 us in one work group's LDS: tiles.)
 bool fits_small(const int64_t *rows, const int64_t *cols, int64_t n) {
     for (int64_t i = 0; i < n; ++i)

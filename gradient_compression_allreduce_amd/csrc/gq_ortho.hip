@@ -369,11 +369,12 @@ struct AddX {
 //      OR_MM_LAST, OR_MM_LAST_BF16: the same into the caller's output
 //      OR_MM_JOIN: D and G0 from the partial sums that OR_MM_GRAM left of tiles
 //                  whose K it split, added in the order of K
-// 97 matrices of 1024 x 1024 and 48 of 1024 x 4096, tiles of 256, us a launch: G
-// 379 (0.81 PFLOP/s of the upper half), Q 258 (0.60), X 743 (0.83), the last X 751.
-// With K = 1024 a tile's loop is 16 steps, and filling the buffers and writing the
-// tile out are a third of its time (X without its loop 220, of that 150 the
-// stores); one work group per compute unit leaves nobody to cover them.
+// 97 matrices of 1024 x 1024 and 48 of 1024 x 4096, tiles of 256, us a launch
+// (medians of a kernel trace): G 389 (0.80 PFLOP/s of the upper half), Q 271 (0.57),
+// X 788 (0.79; the first two read and write y), the last X 748 (0.83).  With
+// K = 1024 a tile's loop is 16 steps, and filling the buffers and writing the tile
+// out are a third of its time (X without its loop 220, of that 150 the stores);
+// one work group per compute unit leaves nobody to cover them.
 template <typename S, int MODE>
 __global__ __launch_bounds__(S::THREADS) void k_ortho_mm(const OrArgs a) {
     MM_LDS(S);
