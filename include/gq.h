@@ -670,8 +670,8 @@ gq_status gq_mx4_product(const uint8_t *a, const uint8_t *a_scale, const uint8_t
  * in binary32.  For the default
  * coefficients the result is 4e-4 to 1e-3 (Frobenius norm) from the exact
  * iteration's, 2e-3 to 4e-3 where the gradient's directions beyond the first few
- * have 1/256 of its norm, and the output's rounding more.  A zero matrix gives 0;
- * inf or NaN makes its own matrix NaN and no other. */
+ * have 1/256 of its norm or all entries round alike, and the output's rounding
+ * more.  A zero matrix gives 0; inf or NaN makes its own matrix NaN and no other. */
 
 typedef struct gq_ortho gq_ortho;
 
