@@ -11,16 +11,20 @@ from tests.conftest import ROOT
 SIDES = ((1 << 15, 1 << 22), (1 << 22, 1 << 15), (1 << 15, 1 << 19))
 
 CHILD = """
-import ctypes, resource, sys
+import ctypes, sys
 import numpy as np
 from gradient_compression_allreduce_amd import gq
+
+def peak():     # KiB, of this program alone
+    return int(open("/proc/self/status").read().split("VmHWM:")[1].split()[0])
+
 rows, cols = int(sys.argv[1]), int(sys.argv[2])
 gq.gq_mx4_sizes(1, 1)
-before = resource.getrusage(resource.RUSAGE_SELF).ru_maxrss
+before = peak()
 a = [np.array([v], np.int64) for v in (0, rows, cols)]
 h = ctypes.c_void_p()
 st = gq.lib.gq_ortho_create(*(v.ctypes.data for v in a), 1, 5, None, 1e-7, None, ctypes.byref(h))
-after = resource.getrusage(resource.RUSAGE_SELF).ru_maxrss
+after = peak()
 print(st, after - before, gq.gq_last_error())
 """
 
