@@ -319,7 +319,8 @@ __device__ __forceinline__ mm_u32x4 mm_scale_shift(mm_u32x4 v, const MmScale &s,
 // Tiles of 256: the scales of four groups (2048 elements of K) at once.  16
 // bytes a row and group are an eighth of a line of the L2 cache each time, as
 // many requests as half the codes are.  At 8192 x 8192, us with K = 1024 / 8192 /
-// 32768: group by group 98 / 323 / 1130, four at once 84 / 297 / 1032.  A lane's
+// 32768: group by group 98 / 323 / 1130, four at once 84 / 297 / 1032 (another
+// device: 85 / 302 / 1093).  A lane's
 // 16 bytes of four rows are one group's, so a wave's loads are of 64 bytes a
 // row.  (They are not held twice: the waves meet once more before new ones are
 // written.)
