@@ -1,0 +1,118 @@
+// gq_embed.cpp -- the C-ABI entry points of the embedding's lookup and
+// gradient: argument checks, workspace and dispatch.  Contracts: include/gq.h.
+#include <algorithm>
+#include <cmath>
+
+#include "gq_args.h"
+#include "gq_embed.h"
+
+using namespace gq;
+
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t{1} << 30;
+constexpr int64_t kMaxRows = int64_t{1} << 30;
+constexpr int64_t kMaxCols = int64_t{1} << 24;
+
+gq_status check_sizes(const char *op, int64_t tokens, int64_t rows, int64_t cols) {
+    if (tokens < 0 || tokens > kMaxTokens || rows < 1 || rows > kMaxRows || cols < 1 ||
+        cols > kMaxCols)
+        return arg_fail(GQ_ERR_INVALID, op,
+                        "tokens = %lld outside [0, 2^30], rows = %lld outside [1, 2^30], or "
+                        "cols = %lld outside [1, 2^24]", static_cast<long long>(tokens),
+                        static_cast<long long>(rows), static_cast<long long>(cols));
+    return GQ_OK;
+}
+
+gq_status check_index(const char *op, const void *idx, int32_t idx_bytes, int64_t tokens) {
+    if (idx_bytes != 4 && idx_bytes != 8)
+        return arg_fail(GQ_ERR_INVALID, op, "idx_bytes = %d must be 4 or 8", idx_bytes);
+    return tokens ? arg_ptr(op, "idx", idx, static_cast<uintptr_t>(idx_bytes)) : GQ_OK;
+}
+
+// `rows` rows of cols elements, ld apart (ld counts from two rows on).
+gq_status check_rows(const char *op, const char *name, const void *p, gq_dtype dt, int64_t rows,
+                     int64_t cols, int64_t &ld) {
+    if (rows <= 1) ld = cols;
+    if (ld < cols || (rows && ld > kMaxElems / rows))
+        return arg_fail(GQ_ERR_INVALID, op,
+                        "%s: row stride %lld below cols, or rows * stride above 2^40", name,
+                        static_cast<long long>(ld));
+    return rows ? arg_ptr(op, name, p, elem_bytes(dt)) : GQ_OK;
+}
+
+gq_status check_mul(const char *op, float mul) {
+    if (!std::isfinite(mul))
+        return arg_fail(GQ_ERR_INVALID, op, "mul = %g must be finite", static_cast<double>(mul));
+    return GQ_OK;
+}
+
+int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// start[rows + 1], order[tokens].
+int64_t grad_workspace(int64_t tokens, int64_t rows) {
+    return round16(4 * (rows + 1)) + round16(4 * tokens);
+}
+
+}  // namespace
+
+extern "C" {
+
+gq_status gq_embed(const void *idx, int32_t idx_bytes, int64_t tokens, const void *table,
+                   gq_dtype dt, int64_t rows, int64_t cols, int64_t ld, float mul,
+                   gq_dtype out_dt, void *out, int64_t ldo, gq_stream stream) {
+    const char *op = "gq_embed";
+    GQ_ARG(check_sizes(op, tokens, rows, cols));
+    GQ_ARG(arg_dtype(op, "dtype", dt));
+    GQ_ARG(arg_dtype(op, "out's dtype", out_dt));
+    GQ_ARG(check_mul(op, mul));
+    GQ_ARG(check_index(op, idx, idx_bytes, tokens));
+    GQ_ARG(check_rows(op, "table", table, dt, rows, cols, ld));
+    GQ_ARG(check_rows(op, "out", out, out_dt, tokens, cols, ldo));
+    if (!tokens) return arg_ok();
+    const EmArgs a = {idx, table, out, tokens, rows, cols, ld, ldo, mul, idx_bytes == 8};
+    return arg_launch(op, launch_embed(a, dt, out_dt, static_cast<hipStream_t>(stream)));
+}
+
+gq_status gq_embed_grad_workspace(int64_t tokens, int64_t rows, int64_t cols, int64_t *bytes) {
+    const char *op = "gq_embed_grad_workspace";
+    if (!bytes) return arg_fail(GQ_ERR_INVALID, op, "bytes is NULL");
+    GQ_ARG(check_sizes(op, tokens, rows, cols));
+    *bytes = grad_workspace(tokens, rows);
+    return arg_ok();
+}
+
+gq_status gq_embed_grad(const void *idx, int32_t idx_bytes, int64_t tokens, const void *dy,
+                        gq_dtype dt, int64_t ldy, float mul, int64_t skip, int64_t rows,
+                        int64_t cols, gq_dtype out_dt, int32_t accumulate, void *grad,
+                        int64_t ldg, void *workspace, int64_t workspace_bytes,
+                        gq_stream stream) {
+    const char *op = "gq_embed_grad";
+    GQ_ARG(check_sizes(op, tokens, rows, cols));
+    GQ_ARG(arg_dtype(op, "dtype", dt));
+    GQ_ARG(arg_dtype(op, "grad's dtype", out_dt));
+    if (accumulate && out_dt != GQ_F32)
+        return arg_fail(GQ_ERR_INVALID, op, "accumulate needs a GQ_F32 gradient");
+    GQ_ARG(check_mul(op, mul));
+    GQ_ARG(check_index(op, idx, idx_bytes, tokens));
+    GQ_ARG(check_rows(op, "dy", dy, dt, tokens, cols, ldy));
+    GQ_ARG(check_rows(op, "grad", grad, out_dt, rows, cols, ldg));
+    GQ_ARG(arg_ptr(op, "workspace", workspace, 16));
+    const int64_t need = grad_workspace(tokens, rows);
+    if (workspace_bytes < need)
+        return arg_fail(GQ_ERR_CAPACITY, op, "workspace of %lld bytes, needs %lld",
+                        static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+    if (!tokens && accumulate) return arg_ok();
+    char *ws = static_cast<char *>(workspace);
+    int32_t *start = reinterpret_cast<int32_t *>(ws);
+    int32_t *order = reinterpret_cast<int32_t *>(ws + round16(4 * (rows + 1)));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const int32_t per = static_cast<int32_t>(std::min<int64_t>(EG_SORT_ROWS, (rows + 255) / 256));
+    const EgSortArgs sa = {idx, tokens, rows, skip, start, order, per, idx_bytes == 8};
+    hipError_t e = launch_embed_sort(sa, st);
+    const EgSumArgs ga = {dy, grad, start, order, rows, cols, ldy, ldg, mul, accumulate != 0};
+    if (e == hipSuccess) e = launch_embed_sum(ga, dt, out_dt, st);
+    return arg_launch(op, e);
+}
+
+}  // extern "C"

@@ -1,0 +1,49 @@
+// gq_embed.h -- argument blocks and launchers of the embedding's kernels.
+// Not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gq.h"
+
+namespace gq {
+
+struct EmArgs {
+    const void *idx;            // [T], int32 or int64
+    const void *table;          // [rows][ld]
+    void *out;                  // [T][ldo]
+    int64_t T, rows, cols, ld, ldo;
+    float mul;
+    bool wide;                  // idx is int64
+};
+
+constexpr int EG_SORT_BLOCK = 1024;
+constexpr int EG_SORT_ROWS = 1024;      // most rows of the table per work group
+
+// The order of tokens that a gradient is summed in: the tokens of row 0, those
+// of row 1, ..., each row's in the order in which they come; row r's are
+// order[start[r]] .. order[start[r + 1] - 1].
+struct EgSortArgs {
+    const void *idx;
+    int64_t T, rows, skip;
+    int32_t *start;             // [rows + 1]
+    int32_t *order;             // [T]
+    int32_t rows_per;           // rows of a work group
+    bool wide;
+};
+
+struct EgSumArgs {
+    const void *dy;             // [T][ldy]
+    void *grad;                 // [rows][ldg]
+    const int32_t *start, *order;
+    int64_t rows, cols, ldy, ldg;
+    float mul;
+    bool add;
+};
+
+hipError_t launch_embed(const EmArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s);
+hipError_t launch_embed_sort(const EgSortArgs &a, hipStream_t s);
+hipError_t launch_embed_sum(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s);
+
+}  // namespace gq

@@ -39,7 +39,9 @@ EXPORTS = ("gq_last_error", "gq_version", "gq_plan_chunks", "gq_units_create",
            "gq_chunker_destroy", "gq_chunker_update", "gq_chunker_predict", "gq_chunker_plan",
            "gq_mx4_sizes", "gq_mx4_quantize", "gq_mx4_reduce_dequant", "gq_mx4_reduce_requantize",
            "gq_mx4_product_workspace", "gq_mx4_product", "gq_ortho_create", "gq_ortho_destroy",
-           "gq_ortho_info", "gq_ortho_tiles", "gq_ortho_step")
+           "gq_ortho_info", "gq_ortho_tiles", "gq_ortho_step", "gq_tensors_create",
+           "gq_tensors_destroy", "gq_tensors_info", "gq_tensors_norm", "gq_tensors_clip",
+           "gq_embed", "gq_embed_grad_workspace", "gq_embed_grad")
 GQ_STATS = 10
 STATS = ("max_abs_err", "max_abs_ref", "max_rel_err", "sum_abs_err", "sum_abs_ref",
          "mean_rel_err", "sum_dd", "sum_rr", "sum_dr", "cos")
@@ -150,6 +152,23 @@ def _load():
     L.gq_ortho_tiles.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(i32)]
     L.gq_ortho_step.restype = st
     L.gq_ortho_step.argtypes = [vp, vp, i32, f32, vp, f32, i32, i32, vp, vp]
+    L.gq_tensors_create.restype = st
+    L.gq_tensors_create.argtypes = [vp, vp, vp, i64, ctypes.POINTER(vp)]
+    L.gq_tensors_destroy.restype = st
+    L.gq_tensors_destroy.argtypes = [vp]
+    L.gq_tensors_info.restype = st
+    L.gq_tensors_info.argtypes = [vp, ctypes.POINTER(i64), ctypes.POINTER(i64), ctypes.POINTER(i64)]
+    L.gq_tensors_norm.restype = st
+    L.gq_tensors_norm.argtypes = [vp, f32, vp, vp, vp]
+    L.gq_tensors_clip.restype = st
+    L.gq_tensors_clip.argtypes = [vp, vp, f32, f32, f32, vp, vp]
+    L.gq_embed.restype = st
+    L.gq_embed.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, f32, i32, vp, i64, vp]
+    L.gq_embed_grad_workspace.restype = st
+    L.gq_embed_grad_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    L.gq_embed_grad.restype = st
+    L.gq_embed_grad.argtypes = [vp, i32, i64, vp, i32, i64, f32, i64, i64, i64, i32, i32, vp, i64,
+                                vp, i64, vp]
     return L
 
 
@@ -306,6 +325,7 @@ def _dt():
             "f64": (torch.float64,),
             "u8": (torch.uint8,),
             "half": (torch.float16, torch.bfloat16),
+            "index": {torch.int32: 4, torch.int64: 8},
             "code": {torch.float32: GQ_F32, torch.float16: GQ_F16, torch.bfloat16: GQ_BF16},
         })
     return _TORCH
@@ -966,3 +986,152 @@ def gq_ortho_step(plan, g, out, in_mul=1.0, momentum=None, mu=0.95, nesterov=Tru
     _check(lib.gq_ortho_step(plan.handle, g.data_ptr(), T["code"][g.dtype], in_mul, mp, mu,
                              1 if nesterov else 0, T["code"][out.dtype], out.data_ptr(),
                              _stream(stream)))
+
+
+class Tensors:
+    """Owner of a gq_tensors list (destroyed with the object); it keeps its
+    tensors' memory alive."""
+
+    def __init__(self, xs):
+        if not isinstance(xs, (list, tuple)) or not xs:
+            raise TypeError("xs must be a list of one or more tensors")
+        dev = _current_device()
+        code = _dt()["code"]
+        for i, x in enumerate(xs):
+            if not (getattr(x, "is_cuda", False) and x.dtype in code and x.is_contiguous()
+                    and x.get_device() == dev):
+                raise _why("xs[%d]" % i, x, 0, code, dev) or ValueError("xs[%d]" % i)
+        px, k1 = _ptrs(xs)
+        n = np.array([x.numel() for x in xs], dtype=np.int64)
+        dt = np.array([code[x.dtype] for x in xs], dtype=np.int32)
+        h = ctypes.c_void_p()
+        _check(lib.gq_tensors_create(px, n.ctypes.data, dt.ctypes.data, len(xs), ctypes.byref(h)))
+        self.handle = h
+        self.tensors = tuple(xs)
+        self.n = int(n.sum())
+        self.count = len(xs)
+        _live.add(self)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            _check(lib.gq_tensors_destroy(self.handle))
+            self.handle = ctypes.c_void_p()
+            self.tensors = ()
+
+    def __del__(self):
+        # (at interpreter shutdown this module's globals may already be
+        # None; the exit hook has freed the handle by then)
+        try:
+            if not _finalizing():
+                self.close()
+        except Exception:
+            pass
+
+
+def gq_tensors_create(xs):
+    """List of the contiguous tensors xs (float32, float16, bfloat16, mixed),
+    which stay where they are: once per model, for gradients that keep their
+    buffers."""
+    return Tensors(xs)
+
+
+def gq_tensors_destroy(tensors):
+    tensors.close()
+
+
+def gq_tensors_info(tensors):
+    """{"n", "count", "bytes"} of a list."""
+    v = [ctypes.c_int64(0) for _ in range(3)]
+    _check(lib.gq_tensors_info(tensors.handle, *(ctypes.byref(x) for x in v)))
+    return {"n": v[0].value, "count": v[1].value, "bytes": v[2].value}
+
+
+def _list(name, t):
+    if not isinstance(t, Tensors) or not getattr(t, "handle", None):
+        raise ValueError("%s must be a live list of tensors (gq_tensors_create)" % name)
+    return t
+
+
+def gq_tensors_norm(tensors, norm, norms=None, in_mul=1.0, stream=None):
+    """norm (fp32, one element) = in_mul * the 2-norm of all tensors of the
+    list together; norms (fp32, one per tensor): also that of each."""
+    _list("tensors", tensors)
+    dev = _current_device()
+    f32 = _dt()["f32"]
+    _need("norm", norm, 1, f32, dev)
+    np_ = None
+    if norms is not None:
+        _need("norms", norms, tensors.count, f32, dev)
+        np_ = norms.data_ptr()
+    _check(lib.gq_tensors_norm(tensors.handle, in_mul, norm.data_ptr(), np_, _stream(stream)))
+
+
+def gq_tensors_clip(tensors, norm, max_norm, eps=1e-6, in_mul=1.0, out=None, stream=None):
+    """Every tensor times in_mul * min(1, max_norm / (norm + eps)), norm being
+    the fp32 norm of in_mul times the list: in place, or into the list out of
+    tensors of the same lengths and any types."""
+    _list("tensors", tensors)
+    _need("norm", norm, 1, _dt()["f32"], _current_device())
+    op = _list("out", out).handle if out is not None else None
+    _check(lib.gq_tensors_clip(tensors.handle, norm.data_ptr(), max_norm, eps, in_mul, op,
+                               _stream(stream)))
+
+
+def _tokens(idx, dev):
+    """(tokens, bytes of an index) of a contiguous index tensor of any shape."""
+    size = _dt()["index"]
+    _need("idx", idx, 0, size, dev)
+    return idx.numel(), size[idx.dtype]
+
+
+def _token_rows(name, t, tokens, dtypes, dev):
+    """(cols, row stride) of a matrix of one row per token."""
+    if not tokens and getattr(t, "is_cuda", False) and len(t.shape) == 2 and not t.shape[0]:
+        _need(name, t, 0, dtypes, dev)
+        return t.shape[1], t.shape[1]
+    rows, cols, ld = _matrix(name, t, dtypes, dev)
+    if rows != tokens:
+        raise ValueError("%s has %d rows for %d tokens" % (name, rows, tokens))
+    return cols, ld
+
+
+def gq_embed(idx, table, out, mul=1.0, stream=None):
+    """out[t] = mul * table[idx[t]] for the indexes (int32 or int64, any shape)
+    of all tokens; zeros for an index outside the table.  table and out:
+    float32, float16 or bfloat16 matrices, out of one row per token."""
+    dev = _current_device()
+    code = _dt()["code"]
+    tokens, size = _tokens(idx, dev)
+    rows, cols, ld = _matrix("table", table, code, dev)
+    ocols, ldo = _token_rows("out", out, tokens, code, dev)
+    if ocols != cols:
+        raise ValueError("out has %d columns, the table %d" % (ocols, cols))
+    _check(lib.gq_embed(idx.data_ptr(), size, tokens, table.data_ptr(), code[table.dtype], rows,
+                        cols, ld, mul, code[out.dtype], out.data_ptr(), ldo, _stream(stream)))
+
+
+def gq_embed_grad_workspace(tokens, rows, cols):
+    """Bytes of workspace that gq_embed_grad needs."""
+    v = ctypes.c_int64(0)
+    _check(lib.gq_embed_grad_workspace(tokens, rows, cols, ctypes.byref(v)))
+    return v.value
+
+
+def gq_embed_grad(idx, dy, grad, workspace, mul=1.0, skip=None, accumulate=False, stream=None):
+    """grad[v] = mul * the sum of dy[t] over the tokens with idx[t] = v, rows
+    without a token 0; accumulate (float32): grad += it.  Tokens of the index
+    skip, and of one outside grad's rows, add nothing.  workspace: a uint8
+    tensor of gq_embed_grad_workspace bytes."""
+    dev = _current_device()
+    T = _dt()
+    code = T["code"]
+    tokens, size = _tokens(idx, dev)
+    rows, cols, ldg = _matrix("grad", grad, code, dev)
+    dcols, ldy = _token_rows("dy", dy, tokens, code, dev)
+    if dcols != cols:
+        raise ValueError("dy has %d columns, grad %d" % (dcols, cols))
+    _need("workspace", workspace, 0, T["u8"], dev)
+    _check(lib.gq_embed_grad(idx.data_ptr(), size, tokens, dy.data_ptr(), code[dy.dtype], ldy, mul,
+                             -1 if skip is None else int(skip), rows, cols, code[grad.dtype],
+                             1 if accumulate else 0, grad.data_ptr(), ldg, workspace.data_ptr(),
+                             workspace.numel(), _stream(stream)))

@@ -80,7 +80,7 @@ typedef enum {
 typedef enum {
     GQ_F32 = 0, /* IEEE binary32 gradient elements */
     GQ_F16 = 1, /* IEEE binary16 gradient elements (loss-scaled, see in_mul) */
-    GQ_BF16 = 2 /* bfloat16 elements: gq_mx4_* and gq_ortho_* only */
+    GQ_BF16 = 2 /* bfloat16 elements: gq_mx4_*, gq_ortho_*, gq_tensors_*, gq_embed* only */
 } gq_dtype;
 
 /* Largest number of simulated ranks a call accepts. */
@@ -729,6 +729,116 @@ gq_status gq_ortho_tiles(const gq_ortho *p, int32_t *tile_g, int32_t *tile_x);
  */
 gq_status gq_ortho_step(gq_ortho *p, const void *g, gq_dtype dt, float in_mul, float *momentum,
                         float mu, int32_t nesterov, gq_dtype out_dt, void *out, gq_stream stream);
+
+/* ---- Gradient norm and clipping over many tensors --------------------------
+ * Between the reduce and the update: the 2-norm of all gradients of a model
+ * together, and their scaling down to a largest norm.  The norm stays on the
+ * device, so a job whose gradients are sharded can combine the shards' norms
+ * (the root of the sum of their squares) before it clips. */
+
+/* A list of tensors on one device: where they lie, their lengths and types. */
+typedef struct gq_tensors gq_tensors;
+
+/*
+ * gq_tensors_create -- a list of tensors on the current device.
+ * x, numel, dt  host arrays of count (1 .. 2^20): tensor i is numel[i] >= 0
+ *         contiguous elements of dt[i] (GQ_F32, GQ_F16, GQ_BF16; types may
+ *         differ) from x[i] on, aligned to its element (NULL where numel[i] is
+ *         0).  At most 2^36 elements together.  Tensors may not overlap.
+ * The list keeps the addresses: the memory has to stay where it is, with any
+ * contents, for as long as the list is used, as gradients in flat buffers do.
+ * Tensors that have moved need a new list.
+ * Allocates device memory (about 24 bytes per 4096 elements and tensor) and
+ * synchronizes.  Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_HIP.
+ */
+gq_status gq_tensors_create(void *const *x, const int64_t *numel, const gq_dtype *dt,
+                            int64_t count, gq_tensors **out);
+
+/* Free a list (its work must have completed; NULL is accepted).  The tensors
+ * are not touched. */
+gq_status gq_tensors_destroy(gq_tensors *t);
+
+/* Elements, tensors, and bytes of the list's own device memory
+ * (informational); any pointer may be NULL. */
+gq_status gq_tensors_info(const gq_tensors *t, int64_t *n, int64_t *count, int64_t *bytes);
+
+/*
+ * gq_tensors_norm -- norm = in_mul * sqrt(sum of x^2 over all elements of the
+ * list), and where norms is given that of each tensor.  Squares and sums are
+ * binary64, each result is rounded to binary32 once.  inf and NaN give inf and
+ * NaN; a list without elements, and a tensor without, gives 0.
+ * in_mul  as for gq_quantize, e.g. 2^-16 for loss-scaled gradients.
+ * norm    device pointer, 1 fp32.  norms: NULL, or a device array of count
+ *         fp32.  Neither may lie in a tensor of the list.
+ * The list holds the call's scratch memory: norms of one list must be ordered,
+ * captured ones included.  Equal calls give equal bits.
+ * Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_DEVICE, GQ_ERR_HIP.
+ */
+gq_status gq_tensors_norm(gq_tensors *t, float in_mul, float *norm, float *norms,
+                          gq_stream stream);
+
+/*
+ * gq_tensors_clip -- y = x * f for every element, with
+ *   c = 1 where norm + eps <= max_norm, else max_norm / (norm + eps)
+ *   f = in_mul * c       (binary64, rounded to binary32 once)
+ * and the product rounded to binary32, then to y's type.  A NaN norm gives NaN
+ * everywhere; an infinite one 0, and NaN for elements that are infinite.
+ * norm      device pointer, 1 fp32: of in_mul * x, as gq_tensors_norm writes it.
+ * max_norm  >= 0 (inf: c is 1 unless the norm is NaN).  eps: finite, >= 0.
+ * out       NULL: in place, and where f is 1 nothing is written.  Otherwise a
+ *           list of tensors of the same lengths, of any types, that share no
+ *           memory with t's; they receive y.
+ * Uses no scratch memory.  Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_DEVICE,
+ * GQ_ERR_HIP.
+ */
+gq_status gq_tensors_clip(const gq_tensors *t, const float *norm, float max_norm, float eps,
+                          float in_mul, const gq_tensors *out, gq_stream stream);
+
+/* ---- Embedding --------------------------------------------------------------
+ * The layer whose weight gradient is no product (gq_mx4_product makes the
+ * others'): rows of a table looked up by token, and the table's gradient, which
+ * is the largest single tensor of many models' gradients.  An index outside
+ * [0, rows) names no row: its token's output is 0, and it adds to no gradient
+ * (so a padded batch may hold -1).  idx: device array of `tokens` indexes of
+ * idx_bytes (4: int32, 8: int64) each.  tokens: 0 .. 2^30, rows: 1 .. 2^30,
+ * cols: 1 .. 2^24.  Matrices are row-major, with a row stride in elements (>= cols;
+ * ignored for one row), aligned to their element.  Outputs may not overlap
+ * inputs, and columns behind cols are not touched. */
+
+/*
+ * gq_embed -- out[t] = mul * table[idx[t]]: one product rounded to binary32,
+ * then to out's type (mul = 1 and one type: the row as it is).
+ * table: rows x cols of dt, row stride ld; out: tokens x cols of out_dt, ldo.
+ * mul: finite.  Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_HIP.
+ */
+gq_status gq_embed(const void *idx, int32_t idx_bytes, int64_t tokens, const void *table,
+                   gq_dtype dt, int64_t rows, int64_t cols, int64_t ld, float mul,
+                   gq_dtype out_dt, void *out, int64_t ldo, gq_stream stream);
+
+/* gq_embed_grad_workspace -- bytes of workspace that gq_embed_grad needs.  Host
+ * only.  Errors: GQ_ERR_INVALID. */
+gq_status gq_embed_grad_workspace(int64_t tokens, int64_t rows, int64_t cols, int64_t *bytes);
+
+/*
+ * gq_embed_grad -- grad[v] = mul * the sum of dy[t] over the tokens t with
+ * idx[t] = v, in binary32, rounded to grad's type once.
+ * dy          tokens x cols of dt, row stride ldy.  mul: finite.
+ * skip        tokens of this index add nothing (a padding token); -1: none.
+ * accumulate  0: every row of grad is written, rows without a token with 0.
+ *             Otherwise (GQ_F32 only) grad += it, with one rounded sum per
+ *             element, and rows without a token are not touched.
+ * grad        rows x cols of out_dt, row stride ldg; it may lie anywhere in a
+ *             flat gradient buffer.
+ * workspace   device memory of at least the bytes gq_embed_grad_workspace
+ *             gives, 16-byte aligned, contents of no matter; calls that share
+ *             it must be ordered, captured ones included.
+ * The order of each sum depends on idx and the sizes alone: equal calls give
+ * equal bits.  Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_CAPACITY, GQ_ERR_HIP.
+ */
+gq_status gq_embed_grad(const void *idx, int32_t idx_bytes, int64_t tokens, const void *dy,
+                        gq_dtype dt, int64_t ldy, float mul, int64_t skip, int64_t rows,
+                        int64_t cols, gq_dtype out_dt, int32_t accumulate, void *grad,
+                        int64_t ldg, void *workspace, int64_t workspace_bytes, gq_stream stream);
 
 #ifdef __cplusplus
 }
