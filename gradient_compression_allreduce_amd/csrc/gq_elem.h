@@ -93,6 +93,30 @@ __device__ __forceinline__ void store_v(T *p, const Raw<T, V> &r) {
     }
 }
 
+// One element.
+template <typename T>
+__device__ __forceinline__ float load_1(const T *p) {
+    if constexpr (sizeof(T) == 4) {
+        return *(const __attribute__((address_space(1))) float *)p;
+    } else {
+        const uint16_t b = *(const __attribute__((address_space(1))) uint16_t *)p;
+        T t;
+        __builtin_memcpy(&t, &b, 2);
+        return to_f32(t);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_1(T *p, T v) {
+    if constexpr (sizeof(T) == 4) {
+        *(__attribute__((address_space(1))) float *)p = v;
+    } else {
+        uint16_t b;
+        __builtin_memcpy(&b, &v, 2);
+        *(__attribute__((address_space(1))) uint16_t *)p = b;
+    }
+}
+
 // Element k of a vector.
 template <typename T, int V>
 __device__ __forceinline__ float elem(const Raw<T, V> &r, int k) {

@@ -49,9 +49,21 @@ gq_status check_mul(const char *op, float mul) {
 
 int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// start[rows + 1], order[tokens].
-int64_t grad_workspace(int64_t tokens, int64_t rows) {
-    return round16(4 * (rows + 1)) + round16(4 * tokens);
+// The parts of a gradient's workspace, and its bytes.
+struct Workspace {
+    int64_t order, piece_row, part, bytes;
+    int64_t pieces;
+};
+
+Workspace grad_workspace(int64_t tokens, int64_t rows, int64_t cols) {
+    Workspace w;
+    // (no row can have more tokens than a piece where there are no more)
+    w.pieces = tokens > EG_PIECE ? (tokens + EG_PIECE - 1) / EG_PIECE : 0;
+    w.order = round16(4 * (rows + 1));
+    w.piece_row = w.order + round16(4 * tokens);
+    w.part = w.piece_row + round16(4 * ((tokens + EG_PIECE - 1) / EG_PIECE));
+    w.bytes = w.part + w.pieces * 2 * 4 * ((cols + 511) / 512 * 512);
+    return w;
 }
 
 }  // namespace
@@ -78,7 +90,7 @@ gq_status gq_embed_grad_workspace(int64_t tokens, int64_t rows, int64_t cols, in
     const char *op = "gq_embed_grad_workspace";
     if (!bytes) return arg_fail(GQ_ERR_INVALID, op, "bytes is NULL");
     GQ_ARG(check_sizes(op, tokens, rows, cols));
-    *bytes = grad_workspace(tokens, rows);
+    *bytes = grad_workspace(tokens, rows, cols).bytes;
     return arg_ok();
 }
 
@@ -98,20 +110,24 @@ gq_status gq_embed_grad(const void *idx, int32_t idx_bytes, int64_t tokens, cons
     GQ_ARG(check_rows(op, "dy", dy, dt, tokens, cols, ldy));
     GQ_ARG(check_rows(op, "grad", grad, out_dt, rows, cols, ldg));
     GQ_ARG(arg_ptr(op, "workspace", workspace, 16));
-    const int64_t need = grad_workspace(tokens, rows);
-    if (workspace_bytes < need)
+    const Workspace w = grad_workspace(tokens, rows, cols);
+    if (workspace_bytes < w.bytes)
         return arg_fail(GQ_ERR_CAPACITY, op, "workspace of %lld bytes, needs %lld",
-                        static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+                        static_cast<long long>(workspace_bytes), static_cast<long long>(w.bytes));
     if (!tokens && accumulate) return arg_ok();
     char *ws = static_cast<char *>(workspace);
     int32_t *start = reinterpret_cast<int32_t *>(ws);
-    int32_t *order = reinterpret_cast<int32_t *>(ws + round16(4 * (rows + 1)));
+    int32_t *order = reinterpret_cast<int32_t *>(ws + w.order);
+    int32_t *piece_row = reinterpret_cast<int32_t *>(ws + w.piece_row);
+    float *part = reinterpret_cast<float *>(ws + w.part);
     hipStream_t st = static_cast<hipStream_t>(stream);
     const int32_t per = static_cast<int32_t>(std::min<int64_t>(EG_SORT_ROWS, (rows + 255) / 256));
-    const EgSortArgs sa = {idx, tokens, rows, skip, start, order, per, idx_bytes == 8};
+    const EgSortArgs sa = {idx, tokens, rows, skip, start, order, piece_row, per, idx_bytes == 8};
     hipError_t e = launch_embed_sort(sa, st);
-    const EgSumArgs ga = {dy, grad, start, order, rows, cols, ldy, ldg, mul, accumulate != 0};
+    const EgSumArgs ga = {dy,   grad, start, order, piece_row, part,
+                          rows, cols, ldy,   ldg,   w.pieces,  mul, accumulate != 0};
     if (e == hipSuccess) e = launch_embed_sum(ga, dt, out_dt, st);
+    if (e == hipSuccess && w.pieces) e = launch_embed_join(ga, dt, out_dt, st);
     return arg_launch(op, e);
 }
 

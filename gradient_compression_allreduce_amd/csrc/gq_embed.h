@@ -20,15 +20,19 @@ struct EmArgs {
 
 constexpr int EG_SORT_BLOCK = 1024;
 constexpr int EG_SORT_ROWS = 1024;      // most rows of the table per work group
+constexpr int EG_PIECE = 64;            // tokens that one wave sums
 
 // The order of tokens that a gradient is summed in: the tokens of row 0, those
 // of row 1, ..., each row's in the order in which they come; row r's are
-// order[start[r]] .. order[start[r + 1] - 1].
+// order[start[r]] .. order[start[r + 1] - 1].  The order is cut into pieces of
+// EG_PIECE tokens; the token that piece p starts with is one of row
+// piece_row[p].
 struct EgSortArgs {
     const void *idx;
     int64_t T, rows, skip;
     int32_t *start;             // [rows + 1]
     int32_t *order;             // [T]
+    int32_t *piece_row;         // [ceil(T / EG_PIECE)]
     int32_t rows_per;           // rows of a work group
     bool wide;
 };
@@ -36,8 +40,10 @@ struct EgSortArgs {
 struct EgSumArgs {
     const void *dy;             // [T][ldy]
     void *grad;                 // [rows][ldg]
-    const int32_t *start, *order;
+    const int32_t *start, *order, *piece_row;
+    float *part;                // [pieces][2][round512(cols)]
     int64_t rows, cols, ldy, ldg;
+    int64_t pieces;             // 0 where no row can be long
     float mul;
     bool add;
 };
@@ -45,5 +51,6 @@ struct EgSumArgs {
 hipError_t launch_embed(const EmArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s);
 hipError_t launch_embed_sort(const EgSortArgs &a, hipStream_t s);
 hipError_t launch_embed_sum(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s);
+hipError_t launch_embed_join(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s);
 
 }  // namespace gq

@@ -23,12 +23,12 @@ struct Span {
 
 struct gq_tensors {
     int device = -1;
-    int64_t n = 0, count = 0, n_tiles = 0, bytes = 0;
+    int64_t n = 0, count = 0, n_tiles = 0, n_longs = 0, bytes = 0;
     std::vector<int64_t> numel;
     std::vector<Span> spans;            // of the tensors that are not empty, in order
     char *d_mem = nullptr;              // one allocation, parted as below
     TnTile *d_tiles = nullptr;
-    int64_t *d_first = nullptr;
+    TnLong *d_longs = nullptr;
     double *d_parts = nullptr, *d_sums = nullptr;
     uint32_t *d_ticket = nullptr;
 };
@@ -58,7 +58,7 @@ gq_status tensors_create(const char *op, void *const *x, const int64_t *numel, c
                          int64_t count, gq_tensors **out) {
     std::vector<Span> spans;
     std::vector<TnTile> tiles;
-    std::vector<int64_t> first;
+    std::vector<TnLong> longs;
     int64_t total = 0;
     for (int64_t i = 0; i < count; ++i) {
         GQ_ARG(arg_dtype(op, "dtype", dt[i]));
@@ -78,15 +78,17 @@ gq_status tensors_create(const char *op, void *const *x, const int64_t *numel, c
         if (spans[i].begin < spans[i - 1].end)
             return arg_fail(GQ_ERR_INVALID, op, "two tensors of the list share memory at %p",
                             reinterpret_cast<void *>(spans[i].begin));
-    first.reserve(count + 1);
     for (int64_t i = 0; i < count; ++i) {
-        first.push_back(static_cast<int64_t>(tiles.size()));
+        const int64_t at = static_cast<int64_t>(tiles.size());
+        const bool one = numel[i] <= TN_TILE;
         for (int64_t e = 0; e < numel[i]; e += TN_TILE)
             tiles.push_back({static_cast<char *>(x[i]) + e * elem_bytes(dt[i]),
-                             static_cast<uint32_t>(std::min<int64_t>(TN_TILE, numel[i] - e)),
-                             static_cast<uint32_t>(dt[i])});
+                             static_cast<uint32_t>(std::min<int64_t>(TN_TILE, numel[i] - e)) |
+                                 static_cast<uint32_t>(dt[i]) << 16,
+                             one ? static_cast<int32_t>(i) : -1});
+        // (an empty tensor's norm is the sum over no tiles)
+        if (!one || !numel[i]) longs.push_back({at, static_cast<int64_t>(tiles.size()), i});
     }
-    first.push_back(static_cast<int64_t>(tiles.size()));
 
     std::unique_ptr<gq_tensors> T(new gq_tensors);
     T->n = total;
@@ -95,23 +97,24 @@ gq_status tensors_create(const char *op, void *const *x, const int64_t *numel, c
     T->numel.assign(numel, numel + count);
     T->spans = std::move(spans);
     hipError_t e = hipGetDevice(&T->device);
-    const size_t at_first = tiles.size() * sizeof(TnTile);
-    const size_t at_sums = at_first + first.size() * sizeof(int64_t);
+    T->n_longs = static_cast<int64_t>(longs.size());
+    const size_t at_longs = tiles.size() * sizeof(TnTile);
+    const size_t at_sums = at_longs + longs.size() * sizeof(TnLong);
     const size_t at_parts = at_sums + tiles.size() * sizeof(double);
     const size_t at_ticket = at_parts + TN_MAX_GRID * sizeof(double);
     T->bytes = static_cast<int64_t>(at_ticket + sizeof(uint64_t));
     if (e == hipSuccess) e = hipMalloc(reinterpret_cast<void **>(&T->d_mem), T->bytes);
     if (e == hipSuccess) {
         T->d_tiles = reinterpret_cast<TnTile *>(T->d_mem);
-        T->d_first = reinterpret_cast<int64_t *>(T->d_mem + at_first);
+        T->d_longs = reinterpret_cast<TnLong *>(T->d_mem + at_longs);
         T->d_sums = reinterpret_cast<double *>(T->d_mem + at_sums);
         T->d_parts = reinterpret_cast<double *>(T->d_mem + at_parts);
         T->d_ticket = reinterpret_cast<uint32_t *>(T->d_mem + at_ticket);
         if (!tiles.empty())
-            e = hipMemcpy(T->d_tiles, tiles.data(), at_first, hipMemcpyHostToDevice);
+            e = hipMemcpy(T->d_tiles, tiles.data(), at_longs, hipMemcpyHostToDevice);
     }
-    if (e == hipSuccess)
-        e = hipMemcpy(T->d_first, first.data(), first.size() * sizeof(int64_t),
+    if (e == hipSuccess && !longs.empty())
+        e = hipMemcpy(T->d_longs, longs.data(), longs.size() * sizeof(TnLong),
                       hipMemcpyHostToDevice);
     const uint64_t zero = 0;
     if (e == hipSuccess) e = hipMemcpy(T->d_ticket, &zero, sizeof zero, hipMemcpyHostToDevice);
@@ -179,11 +182,11 @@ gq_status gq_tensors_norm(gq_tensors *t, float in_mul, float *norm, float *norms
     if (norms) GQ_ARG(arg_ptr(op, "norms", norms, 4));
     GQ_ARG(check_list(op, "the list", t));
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const TnNormArgs a = {t->d_tiles, t->n_tiles, t->d_parts, norms ? t->d_sums : nullptr,
-                          t->d_ticket, norm, in_mul};
+    const TnNormArgs a = {t->d_tiles, t->n_tiles, t->d_parts, t->d_sums, t->d_ticket, norm, norms,
+                          in_mul};
     hipError_t e = launch_tensors_norm(a, st);
-    if (e == hipSuccess && norms)
-        e = launch_tensors_each({t->d_first, t->d_sums, norms, t->count, in_mul}, st);
+    if (e == hipSuccess && norms && t->n_longs)
+        e = launch_tensors_each({t->d_longs, t->d_sums, norms, t->n_longs, in_mul}, st);
     return arg_launch(op, e);
 }
 

@@ -1,7 +1,8 @@
 // gq_tensors.hip -- gfx950 kernels over a list of tensors:
-//   k_tensors_norm  the 2-norm of all of them together, and each tile's sum of
-//                   squares where each tensor's norm is asked for;
-//   k_tensors_each  each tensor's norm from its tiles' sums;
+//   k_tensors_norm  the 2-norm of all of them together and, where each tensor's
+//                   norm is asked for, those of tensors of one tile and the
+//                   others' tiles' sums of squares;
+//   k_tensors_each  the norms of tensors of several tiles from their sums;
 //   k_tensors_clip  x * in_mul * min(1, max_norm / (norm + eps)).
 // All of it is bound by HBM: one operation or two per element.
 // Squares and their sums are binary64 (the square of a binary32 value is exact
@@ -14,6 +15,8 @@ namespace gq {
 namespace {
 
 constexpr int TN_WAVES = TN_BLOCK / 64;
+constexpr int TN_NWAVES = TN_NORM_BLOCK / 64;
+constexpr int TN_GROUP = 8;         // vectors of a lane in flight
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -28,24 +31,25 @@ __device__ __forceinline__ TnTile tile_at(const TnTile *tiles, int64_t t) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p));
     const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(p >> 32));
     v.p = reinterpret_cast<char *>(static_cast<uint64_t>(hi) << 32 | lo);
-    v.n = __builtin_amdgcn_readfirstlane(v.n);
-    v.dt = __builtin_amdgcn_readfirstlane(v.dt);
+    v.n_dt = __builtin_amdgcn_readfirstlane(v.n_dt);
+    v.only = __builtin_amdgcn_readfirstlane(v.only);
     return v;
 }
 
 // This lane's part of the sum of squares of n elements.  Whole tiles are
-// loaded whole before the first square; of a short one the lanes take a vector
-// each as long as there are whole ones, and the rest one by one.
+// loaded whole before the first square, shorter ones in groups of TN_GROUP
+// vectors a lane (those past the end are the last one again, and are not
+// added); what is left is less than a vector, an element a lane.
 template <typename T>
 __device__ __forceinline__ double squares(const T *p, int n) {
     constexpr int V = 16 / sizeof(T);
     constexpr int S = TN_TILE / V / 64;
     const int lane = threadIdx.x & 63;
     double s0 = 0.0, s1 = 0.0;
-    auto add = [&](const Raw<T, V> &r) {
+    auto add = [&](const Raw<T, V> &r, bool in) {
 #pragma unroll
         for (int k = 0; k < V; k += 2) {
-            const double a = elem<T, V>(r, k), b = elem<T, V>(r, k + 1);
+            const double a = in ? elem<T, V>(r, k) : 0.0f, b = in ? elem<T, V>(r, k + 1) : 0.0f;
             s0 = __builtin_fma(a, a, s0);
             s1 = __builtin_fma(b, b, s1);
         }
@@ -55,15 +59,22 @@ __device__ __forceinline__ double squares(const T *p, int n) {
 #pragma unroll
         for (int s = 0; s < S; ++s) r[s] = load_v<true, T, V>(p + (s * 64 + lane) * V);
 #pragma unroll
-        for (int s = 0; s < S; ++s) add(r[s]);
+        for (int s = 0; s < S; ++s) add(r[s], true);
     } else {
-        const int full = n / V;
-        for (int s = lane; s < full; s += 64) add(load_v<true, T, V>(p + s * V));
-        const int at = full * V + lane;
-        if (at < n) {
-            const double a = to_f32(p[at]);
-            s0 = __builtin_fma(a, a, s0);
+        const int full = n / V, rest = full * V + lane;
+        const float last = rest < n ? load_1(p + rest) : 0.0f;
+        for (int at = 0; at < full; at += TN_GROUP * 64) {
+            Raw<T, V> r[TN_GROUP];
+#pragma unroll
+            for (int g = 0; g < TN_GROUP; ++g) {
+                const int s = at + g * 64 + lane;
+                r[g] = load_v<true, T, V>(p + (s < full ? s : full - 1) * V);
+            }
+#pragma unroll
+            for (int g = 0; g < TN_GROUP; ++g) add(r[g], at + g * 64 + lane < full);
         }
+        const double a = last;
+        s0 = __builtin_fma(a, a, s0);
     }
     return s0 + s1;
 }
@@ -76,22 +87,25 @@ __device__ __forceinline__ float norm_of(double sum, float in_mul) {
 // sum; the last one to finish adds them in their order, so that equal calls
 // give equal bits.
 template <bool EACH>
-__global__ __launch_bounds__(TN_BLOCK) void k_tensors_norm(const TnNormArgs a) {
-    __shared__ double sh[TN_WAVES];
+__global__ __launch_bounds__(TN_NORM_BLOCK) void k_tensors_norm(const TnNormArgs a) {
+    __shared__ double sh[TN_NWAVES];
     __shared__ uint32_t done;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     double sum = 0.0;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * TN_WAVES + wave; t < a.n_tiles;
-         t += static_cast<int64_t>(gridDim.x) * TN_WAVES) {
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * TN_NWAVES + wave; t < a.n_tiles;
+         t += static_cast<int64_t>(gridDim.x) * TN_NWAVES) {
         const TnTile v = tile_at(a.tiles, t);
-        const int n = static_cast<int>(v.n);
+        const int n = v.n_dt & 0xffff, dt = v.n_dt >> 16;
         double s;
-        if (v.dt == GQ_F32) s = squares(reinterpret_cast<const float *>(v.p), n);
-        else if (v.dt == GQ_F16) s = squares(reinterpret_cast<const __half *>(v.p), n);
+        if (dt == GQ_F32) s = squares(reinterpret_cast<const float *>(v.p), n);
+        else if (dt == GQ_F16) s = squares(reinterpret_cast<const __half *>(v.p), n);
         else s = squares(reinterpret_cast<const bf16_t *>(v.p), n);
         if (EACH) {
             s = wave_sum(s);
-            if (lane == 0) a.tile_sums[t] = s;
+            if (lane == 0) {
+                if (v.only >= 0) a.norms[v.only] = norm_of(s, a.in_mul);
+                else a.tile_sums[t] = s;
+            }
         }
         sum += s;
     }
@@ -101,15 +115,19 @@ __global__ __launch_bounds__(TN_BLOCK) void k_tensors_norm(const TnNormArgs a) {
     if (threadIdx.x == 0) {
         double s = sh[0];
 #pragma unroll
-        for (int w = 1; w < TN_WAVES; ++w) s += sh[w];
+        for (int w = 1; w < TN_NWAVES; ++w) s += sh[w];
+        // The sum is on its way past this XCD's L2 cache (agent scope); once it
+        // has arrived the ticket may say so.  (An acquire-release ticket would
+        // write back and invalidate that cache in every work group: 112 us
+        // instead of 38 for 10000 tensors, 82 MB.)
         __hip_atomic_store(&a.parts[blockIdx.x], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        done = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        done = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     if (done != gridDim.x - 1) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     sum = 0.0;
-    for (uint32_t i = threadIdx.x; i < gridDim.x; i += TN_BLOCK)
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += TN_NORM_BLOCK)
         sum += __hip_atomic_load(&a.parts[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     sum = wave_sum(sum);
     if (lane == 0) sh[wave] = sum;      // read by thread 0 before the barrier above
@@ -117,56 +135,55 @@ __global__ __launch_bounds__(TN_BLOCK) void k_tensors_norm(const TnNormArgs a) {
     if (threadIdx.x == 0) {
         double s = sh[0];
 #pragma unroll
-        for (int w = 1; w < TN_WAVES; ++w) s += sh[w];
+        for (int w = 1; w < TN_NWAVES; ++w) s += sh[w];
         a.norm[0] = norm_of(s, a.in_mul);
         __hip_atomic_store(a.ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
-// A wave per tensor.
+// A wave per tensor of several tiles.
 __global__ __launch_bounds__(TN_BLOCK) void k_tensors_each(const TnEachArgs a) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * TN_WAVES + (threadIdx.x >> 6);
     if (i >= a.count) return;
     const int lane = threadIdx.x & 63;
+    const TnLong v = a.longs[i];
     double s = 0.0;
-    for (int64_t t = a.first[i] + lane; t < a.first[i + 1]; t += 64) s += a.tile_sums[t];
+    for (int64_t t = v.first + lane; t < v.end; t += 64) s += a.tile_sums[t];
     s = wave_sum(s);
-    if (lane == 0) a.norms[i] = norm_of(s, a.in_mul);
+    if (lane == 0) a.norms[v.tensor] = norm_of(s, a.in_mul);
 }
 
 // y = x * f, x and y apart or the same memory of one type.
 template <typename T, typename U>
 __device__ __forceinline__ void scale_tile(const T *x, U *y, int n, float f) {
     constexpr int V = sizeof(T) == 4 || sizeof(U) == 4 ? 4 : 8;
-    constexpr int G = 8;                // vectors in flight
     const int lane = threadIdx.x & 63;
-    auto out = [&](int at, const Raw<T, V> &r) {
-        float g[V];
+    const int full = n / V, rest = full * V + lane;
+    const float last = rest < n ? load_1(x + rest) : 0.0f;
+    for (int at = 0; at < full; at += TN_GROUP * 64) {
+        Raw<T, V> r[TN_GROUP];
 #pragma unroll
-        for (int k = 0; k < V; ++k) g[k] = elem<T, V>(r, k) * f;
-        store_v<true, U, V>(y + at, pack<U, V>(g));
-    };
-    if (n == TN_TILE) {
-#pragma unroll 1
-        for (int s = 0; s < TN_TILE / V / 64; s += G) {
-            Raw<T, V> r[G];
-#pragma unroll
-            for (int g = 0; g < G; ++g) r[g] = load_v<true, T, V>(x + ((s + g) * 64 + lane) * V);
-#pragma unroll
-            for (int g = 0; g < G; ++g) out(((s + g) * 64 + lane) * V, r[g]);
+        for (int g = 0; g < TN_GROUP; ++g) {
+            const int s = at + g * 64 + lane;
+            r[g] = load_v<true, T, V>(x + (s < full ? s : full - 1) * V);
         }
-    } else {
-        const int full = n / V;
-        for (int s = lane; s < full; s += 64) out(s * V, load_v<true, T, V>(x + s * V));
-        const int at = full * V + lane;
-        if (at < n) y[at] = from_f32<U>(to_f32(x[at]) * f);
+#pragma unroll
+        for (int g = 0; g < TN_GROUP; ++g) {
+            const int s = at + g * 64 + lane;
+            float v[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = elem<T, V>(r[g], k) * f;
+            if (s < full) store_v<true, U, V>(y + s * V, pack<U, V>(v));
+        }
     }
+    if (rest < n) store_1(y + rest, from_f32<U>(last * f));
 }
 
 template <typename T>
 __device__ __forceinline__ void scale_into(const T *x, const TnTile &y, int n, float f) {
-    if (y.dt == GQ_F32) scale_tile(x, reinterpret_cast<float *>(y.p), n, f);
-    else if (y.dt == GQ_F16) scale_tile(x, reinterpret_cast<__half *>(y.p), n, f);
+    const int dt = y.n_dt >> 16;
+    if (dt == GQ_F32) scale_tile(x, reinterpret_cast<float *>(y.p), n, f);
+    else if (dt == GQ_F16) scale_tile(x, reinterpret_cast<__half *>(y.p), n, f);
     else scale_tile(x, reinterpret_cast<bf16_t *>(y.p), n, f);
 }
 
@@ -179,35 +196,35 @@ __global__ __launch_bounds__(TN_BLOCK) void k_tensors_clip(const TnClipArgs a) {
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * TN_WAVES + wave; t < a.n_tiles;
          t += static_cast<int64_t>(gridDim.x) * TN_WAVES) {
         const TnTile v = tile_at(a.x, t), y = tile_at(a.y, t);
-        const int n = static_cast<int>(v.n);
-        if (v.dt == GQ_F32) scale_into(reinterpret_cast<const float *>(v.p), y, n, f);
-        else if (v.dt == GQ_F16) scale_into(reinterpret_cast<const __half *>(v.p), y, n, f);
+        const int n = v.n_dt & 0xffff, dt = v.n_dt >> 16;
+        if (dt == GQ_F32) scale_into(reinterpret_cast<const float *>(v.p), y, n, f);
+        else if (dt == GQ_F16) scale_into(reinterpret_cast<const __half *>(v.p), y, n, f);
         else scale_into(reinterpret_cast<const bf16_t *>(v.p), y, n, f);
     }
 }
 
-int groups(int64_t waves, int64_t most) {
-    const int64_t g = (waves + TN_WAVES - 1) / TN_WAVES;
+int groups(int64_t waves, int per, int64_t most) {
+    const int64_t g = (waves + per - 1) / per;
     return static_cast<int>(g < 1 ? 1 : g < most ? g : most);
 }
 
 }  // namespace
 
 hipError_t launch_tensors_norm(const TnNormArgs &a, hipStream_t s) {
-    const int grid = groups(a.n_tiles, TN_MAX_GRID);
-    if (a.tile_sums) k_tensors_norm<true><<<grid, TN_BLOCK, 0, s>>>(a);
-    else k_tensors_norm<false><<<grid, TN_BLOCK, 0, s>>>(a);
+    const int grid = groups(a.n_tiles, TN_NWAVES, TN_MAX_GRID);
+    if (a.norms) k_tensors_norm<true><<<grid, TN_NORM_BLOCK, 0, s>>>(a);
+    else k_tensors_norm<false><<<grid, TN_NORM_BLOCK, 0, s>>>(a);
     return hipGetLastError();
 }
 
 hipError_t launch_tensors_each(const TnEachArgs &a, hipStream_t s) {
-    k_tensors_each<<<groups(a.count, 1 << 20), TN_BLOCK, 0, s>>>(a);
+    k_tensors_each<<<groups(a.count, TN_WAVES, 1 << 20), TN_BLOCK, 0, s>>>(a);
     return hipGetLastError();
 }
 
 hipError_t launch_tensors_clip(const TnClipArgs &a, hipStream_t s) {
     if (a.n_tiles == 0) return hipSuccess;
-    k_tensors_clip<<<groups(a.n_tiles, 1 << 20), TN_BLOCK, 0, s>>>(a);
+    k_tensors_clip<<<groups(a.n_tiles, TN_WAVES, 1 << 20), TN_BLOCK, 0, s>>>(a);
     return hipGetLastError();
 }
 

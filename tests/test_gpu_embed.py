@@ -324,3 +324,17 @@ def test_above_2_32_elements(gq):
     o[T - 1], o[T - 2], o[5] = 3.0, 5.0, 7.0
     _grad(gq, idx, o, grad)
     assert bool((grad[0] == 12).all()) and bool((grad[1] == 3).all())
+
+
+def test_most_rows(gq):
+    """The largest number of rows, with a token in the first, the last and two
+    between, and the most frequent one in three pieces."""
+    V = 1 << 30
+    grad = torch.full((V, 1), GUARD, dtype=torch.float16, device="cuda")
+    idx = torch.tensor([V - 1, 0, V // 3, V // 2 + 1, V, -1] + [V - 2] * 150, device="cuda")
+    dy = torch.ones(idx.numel(), 1, dtype=torch.float16, device="cuda")
+    dy[:6, 0] = torch.arange(1, 7)
+    _grad(gq, idx, dy, grad)
+    at = [V - 1, 0, V // 3, V // 2 + 1, V - 2]
+    assert [float(grad[i, 0]) for i in at] == [1, 2, 3, 4, 150]
+    assert int((grad != 0).sum()) == 5
