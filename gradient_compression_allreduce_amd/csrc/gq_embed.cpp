@@ -49,19 +49,22 @@ gq_status check_mul(const char *op, float mul) {
 
 int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
-// The parts of a gradient's workspace, and its bytes.
+// The parts of a gradient's workspace, and its bytes (at least 16).
 struct Workspace {
-    int64_t order, piece_row, part, bytes;
-    int64_t pieces;
+    int64_t order = 0, piece_row = 0, keys = 0, part = 0, bytes = 16;
+    int64_t pieces = 0;
 };
 
 Workspace grad_workspace(int64_t tokens, int64_t rows, int64_t cols) {
     Workspace w;
-    // (no row can have more tokens than a piece where there are no more)
-    w.pieces = tokens > EG_PIECE ? (tokens + EG_PIECE - 1) / EG_PIECE : 0;
+    if (tokens <= EG_SMALL) return w;
+    w.pieces = (tokens + EG_PIECE - 1) / EG_PIECE;
     w.order = round16(4 * (rows + 1));
     w.piece_row = w.order + round16(4 * tokens);
-    w.part = w.piece_row + round16(4 * ((tokens + EG_PIECE - 1) / EG_PIECE));
+    w.keys = w.piece_row + round16(4 * w.pieces);
+    w.part = w.keys;
+    if (tokens > EG_BLOCK * EG_HELD)
+        w.part += 4 * ((tokens + EG_KEYS - 1) / EG_KEYS * EG_KEYS);
     w.bytes = w.part + w.pieces * 2 * 4 * ((cols + 511) / 512 * 512);
     return w;
 }
@@ -115,19 +118,38 @@ gq_status gq_embed_grad(const void *idx, int32_t idx_bytes, int64_t tokens, cons
         return arg_fail(GQ_ERR_CAPACITY, op, "workspace of %lld bytes, needs %lld",
                         static_cast<long long>(workspace_bytes), static_cast<long long>(w.bytes));
     if (!tokens && accumulate) return arg_ok();
-    char *ws = static_cast<char *>(workspace);
-    int32_t *start = reinterpret_cast<int32_t *>(ws);
-    int32_t *order = reinterpret_cast<int32_t *>(ws + w.order);
-    int32_t *piece_row = reinterpret_cast<int32_t *>(ws + w.piece_row);
-    float *part = reinterpret_cast<float *>(ws + w.part);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const int32_t per = static_cast<int32_t>(std::min<int64_t>(EG_SORT_ROWS, (rows + 255) / 256));
-    const EgSortArgs sa = {idx, tokens, rows, skip, start, order, piece_row, per, idx_bytes == 8};
+    const bool wide = idx_bytes == 8, add = accumulate != 0;
+    if (tokens <= EG_SMALL) {
+        // two work groups per compute unit, of 16 rows or more
+        const int64_t per = std::min<int64_t>(EG_SMALL_ROWS,
+                                              std::max<int64_t>(16, (rows + 511) / 512));
+        const EgSmallArgs a = {idx, dy,  grad, tokens, rows, cols, ldy, ldg, skip,
+                               static_cast<int32_t>(per), mul, wide, add};
+        return arg_launch(op, launch_embed_grad_small(a, dt, out_dt, st));
+    }
+    char *ws = static_cast<char *>(workspace);
+    EgSortArgs sa = {};
+    sa.idx = idx;
+    sa.T = tokens;
+    sa.rows = rows;
+    sa.skip = skip;
+    sa.keys = w.part > w.keys ? reinterpret_cast<uint32_t *>(ws + w.keys) : nullptr;
+    sa.start = reinterpret_cast<int32_t *>(ws);
+    sa.order = reinterpret_cast<int32_t *>(ws + w.order);
+    sa.piece_row = reinterpret_cast<int32_t *>(ws + w.piece_row);
+    sa.grad = add ? nullptr : static_cast<char *>(grad);
+    sa.cols = cols;
+    sa.ldg = ldg;
+    sa.elem = static_cast<int32_t>(elem_bytes(out_dt));
+    sa.rows_per = static_cast<int32_t>(std::min<int64_t>(EG_SORT_ROWS, (rows + 255) / 256));
+    sa.wide = wide;
+    const EgSumArgs ga = {dy, grad, sa.start, sa.order, sa.piece_row,
+                          reinterpret_cast<float *>(ws + w.part),
+                          rows, cols, ldy, ldg, w.pieces, mul, add};
     hipError_t e = launch_embed_sort(sa, st);
-    const EgSumArgs ga = {dy,   grad, start, order, piece_row, part,
-                          rows, cols, ldy,   ldg,   w.pieces,  mul, accumulate != 0};
     if (e == hipSuccess) e = launch_embed_sum(ga, dt, out_dt, st);
-    if (e == hipSuccess && w.pieces) e = launch_embed_join(ga, dt, out_dt, st);
+    if (e == hipSuccess) e = launch_embed_join(ga, dt, out_dt, st);
     return arg_launch(op, e);
 }
 

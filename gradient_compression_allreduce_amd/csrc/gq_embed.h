@@ -18,21 +18,40 @@ struct EmArgs {
     bool wide;                  // idx is int64
 };
 
-constexpr int EG_SORT_BLOCK = 1024;
+constexpr int EG_BLOCK = 1024;          // threads of a work group that orders tokens
+constexpr int EG_WAVES = EG_BLOCK / 64;
 constexpr int EG_SORT_ROWS = 1024;      // most rows of the table per work group
 constexpr int EG_PIECE = 64;            // tokens that one wave sums
+constexpr int EG_SMALL = EG_BLOCK;      // most tokens of a gradient in one launch
+constexpr int EG_SMALL_ROWS = 128;      // most rows of the table per work group there
+constexpr int EG_HELD = 16;             // tokens of a lane that the sort keeps
+constexpr int EG_KEYS = 256;            // the sort's row numbers come in multiples
+
+// A gradient of up to EG_SMALL tokens.
+struct EgSmallArgs {
+    const void *idx;
+    const void *dy;             // [T][ldy]
+    void *grad;                 // [rows][ldg]
+    int64_t T, rows, cols, ldy, ldg, skip;
+    int32_t rows_per;           // rows of a work group
+    float mul;
+    bool wide, add;
+};
 
 // The order of tokens that a gradient is summed in: the tokens of row 0, those
-// of row 1, ..., each row's in the order in which they come; row r's are
-// order[start[r]] .. order[start[r + 1] - 1].  The order is cut into pieces of
-// EG_PIECE tokens; the token that piece p starts with is one of row
-// piece_row[p].
+// of row 1, ...; row r's are order[start[r]] .. order[start[r + 1] - 1].  The
+// order is cut into pieces of EG_PIECE tokens; the token that piece p starts
+// with is one of row piece_row[p].
 struct EgSortArgs {
     const void *idx;
     int64_t T, rows, skip;
+    uint32_t *keys;             // NULL, or [round256(T)]
     int32_t *start;             // [rows + 1]
     int32_t *order;             // [T]
     int32_t *piece_row;         // [ceil(T / EG_PIECE)]
+    char *grad;                 // NULL, or where rows without a token get 0
+    int64_t cols, ldg;
+    int32_t elem;               // bytes of grad's elements
     int32_t rows_per;           // rows of a work group
     bool wide;
 };
@@ -49,6 +68,8 @@ struct EgSumArgs {
 };
 
 hipError_t launch_embed(const EmArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s);
+hipError_t launch_embed_grad_small(const EgSmallArgs &a, gq_dtype dt, gq_dtype out_dt,
+                                   hipStream_t s);
 hipError_t launch_embed_sort(const EgSortArgs &a, hipStream_t s);
 hipError_t launch_embed_sum(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s);
 hipError_t launch_embed_join(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s);

@@ -3,7 +3,8 @@
 //   k_embed_sort  the tokens in the order of their rows;
 //   k_embed_sum   grad[v] (+)= mul * the sum of dy over row v's tokens, and the
 //                 sums of the pieces of long rows;
-//   k_embed_join  the long rows from their pieces' sums.
+//   k_embed_join  the long rows from their pieces' sums;
+//   k_embed_grad_small  the whole gradient of few tokens.
 #include "gq_elem.h"
 #include "gq_embed.h"
 
@@ -51,59 +52,102 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed(const EmArgs a) {
 // the order its own tokens start, so no work group needs another's counts.
 // Wave w looks at the w-th sixteenth of the tokens.  It counts each row's;
 // sums over the waves and rows before give where its own tokens of a row go;
-// and in a second pass it puts them there, in the order in which they come.
-constexpr int EG_LOADS = 16;        // indexes of a lane in flight
+// and in a second pass it puts them there.  Up to 16384 tokens stay in registers
+// between the passes; more are first turned into row numbers of 32 bits
+// (k_embed_keys), which take the fewest instructions to look through.
 
-// The rows of 64 * EG_LOADS tokens from t on, -1 for those that count for none.
-__device__ __forceinline__ void rows_of(const EgSortArgs &a, int64_t t, int64_t end, int lane,
-                                        int32_t (&row)[EG_LOADS]) {
-#pragma unroll
-    for (int k = 0; k < EG_LOADS; ++k) {
-        const int64_t i = t + 64 * k + lane;
-        int64_t v = -1;
-        if (i < end) v = index_at(a.idx, a.wide, i);
-        row[k] = v >= 0 && v < a.rows && v != a.skip ? static_cast<int32_t>(v) : -1;
+// The row of token i, or ~0 where it counts for none.
+__device__ __forceinline__ uint32_t row_of(const void *idx, bool wide, int64_t rows, int64_t skip,
+                                           int64_t i) {
+    const int64_t v = index_at(idx, wide, i);
+    return v >= 0 && v < rows && v != skip ? static_cast<uint32_t>(v) : ~0u;
+}
+
+__global__ __launch_bounds__(EM_BLOCK) void k_embed_keys(const EgSortArgs a) {
+    const int64_t n = (a.T + EG_KEYS - 1) / EG_KEYS * EG_KEYS;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * EM_BLOCK + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * EM_BLOCK)
+        a.keys[i] = i < a.T ? row_of(a.idx, a.wide, a.rows, a.skip, i) : ~0u;
+}
+
+// Zeros into n elements of `elem` bytes, by a wave.
+__device__ __forceinline__ void zero_row(char *p, int64_t n, int elem, int lane) {
+    const int64_t bytes = n * elem;
+    for (int64_t b = lane * 16; b + 16 <= bytes; b += 64 * 16)
+        store_v<true>(reinterpret_cast<uint32_t *>(p + b), Raw<uint32_t, 4>{});
+    const int64_t b = bytes / 16 * 16 + lane * elem;
+    if (b < bytes) {
+        if (elem == 4) store_1(reinterpret_cast<uint32_t *>(p + b), 0u);
+        else store_1(reinterpret_cast<uint16_t *>(p + b), uint16_t{0});
     }
 }
 
-__global__ __launch_bounds__(EG_SORT_BLOCK) void k_embed_sort(const EgSortArgs a) {
-    constexpr int NW = EG_SORT_BLOCK / 64;
-    extern __shared__ int32_t count[];          // [NW][rows_per]
+template <bool KEYS>
+__global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
+    constexpr int NW = EG_WAVES;
+    extern __shared__ int32_t count[];          // [NW + 1][rows_per]
     __shared__ int32_t before[NW];
     __shared__ int32_t scan[NW];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int R = a.rows_per;
-    const int32_t row0 = static_cast<int32_t>(blockIdx.x) * R;
-    const int n_rows = static_cast<int>(a.rows - row0 < R ? a.rows - row0 : R);
-    const int64_t per = (a.T + NW * 64 - 1) / (NW * 64) * 64;
-    const int64_t t0 = wave * per, t1 = t0 + per < a.T ? t0 + per : a.T;
-    for (int i = threadIdx.x; i < NW * R; i += EG_SORT_BLOCK) count[i] = 0;
+    const uint32_t row0 = blockIdx.x * static_cast<uint32_t>(R);
+    const uint32_t n_rows = static_cast<uint32_t>(a.rows - row0 < R ? a.rows - row0 : R);
+    const int64_t step = KEYS ? EG_KEYS : 64;
+    const int64_t n = (a.T + step - 1) / step * step;
+    const int64_t per = (n + NW * step - 1) / (NW * step) * step;
+    const int64_t t0 = wave * per, t1 = t0 + per < n ? t0 + per : n;
+    for (int i = threadIdx.x; i < NW * R; i += EG_BLOCK) count[i] = 0;
+
+    // 64 * EG_HELD tokens from t on
+    uint32_t row[EG_HELD];
+    auto load = [&](int64_t t) {
+#pragma unroll
+        for (int k = 0; k < EG_HELD; k += KEYS ? 4 : 1) {
+            if constexpr (KEYS) {
+                Raw<uint32_t, 4> v = {{~0u, ~0u, ~0u, ~0u}};
+                if (t + 64 * k < t1)
+                    v = load_v<false, uint32_t, 4>(a.keys + t + 64 * k + 4 * lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) row[k + j] = v.w[j];
+            } else {
+                const int64_t i = t + 64 * k + lane;
+                row[k] = ~0u;
+                if (t + 64 * k < t1 && i < a.T)
+                    row[k] = row_of(a.idx, a.wide, a.rows, a.skip, i);
+            }
+        }
+    };
+    auto token = [&](int64_t t, int k) {
+        return KEYS ? t + 64 * (k & ~3) + 4 * lane + (k & 3) : t + 64 * k + lane;
+    };
+    if (!KEYS) load(t0);
     __syncthreads();
+
     int32_t *mine = count + wave * R;
     int32_t less = 0;
-    int32_t row[EG_LOADS];
-    for (int64_t t = t0; t < t1; t += 64 * EG_LOADS) {
-        rows_of(a, t, t1, lane, row);
+    for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
+        if (KEYS) load(t);
 #pragma unroll
-        for (int k = 0; k < EG_LOADS; ++k) {
-            if (row[k] >= 0 && row[k] < row0) ++less;
-            const uint32_t key = static_cast<uint32_t>(row[k]) - static_cast<uint32_t>(row0);
-            if (key < static_cast<uint32_t>(n_rows)) atomicAdd(&mine[key], 1);
+        for (int k = 0; k < EG_HELD; ++k) {
+            less += __popcll(__ballot(row[k] < row0));
+            const uint32_t key = row[k] - row0;
+            if (key < n_rows) atomicAdd(&mine[key], 1);
         }
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) less += __shfl_xor(less, o, 64);
     if (lane == 0) before[wave] = less;
     __syncthreads();
     // thread r: row r's tokens in each wave's part, as starts
     int32_t total = 0;
-    const int r = threadIdx.x;
-    if (r < n_rows)
+    const uint32_t r = threadIdx.x;
+    if (r < n_rows) {
         for (int w = 0; w < NW; ++w) {
             const int32_t c = count[w * R + r];
             count[w * R + r] = total;
             total += c;
         }
+        count[NW * R + r] = total;
+    }
     int32_t upto = total;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -123,24 +167,41 @@ __global__ __launch_bounds__(EG_SORT_BLOCK) void k_embed_sort(const EgSortArgs a
         if (row0 + r == a.rows - 1) a.start[a.rows] = at + total;
     }
     __syncthreads();
-    for (int64_t t = t0; t < t1; t += 64 * EG_LOADS) {
-        rows_of(a, t, t1, lane, row);
+    // the rows that no token names, while the order's loads and stores run
+    if (a.grad)
+        for (uint32_t q = wave; q < n_rows; q += NW)
+            if (count[NW * R + q] == 0)
+                zero_row(a.grad + (row0 + q) * a.ldg * a.elem, a.cols, a.elem, lane);
+    for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
+        if (KEYS) load(t);
 #pragma unroll
-        for (int k = 0; k < EG_LOADS; ++k) {
-            const uint32_t key = static_cast<uint32_t>(row[k]) - static_cast<uint32_t>(row0);
-            const bool own = key < static_cast<uint32_t>(n_rows);
-            uint64_t same = __ballot(own);
-            if (!same) continue;
-            // the lanes whose token names the same row
-            for (int b = 1; b < R; b <<= 1) {
-                const uint64_t set = __ballot((key & b) != 0);
-                same &= (key & b) ? set : ~set;
+        for (int k = 0; k < EG_HELD; ++k) {
+            const uint32_t key = row[k] - row0;
+            const bool own = key < n_rows;
+            const uint64_t any = __ballot(own);
+            if (!any) continue;
+            // the lanes whose token names the same row: of a few tokens one row
+            // after another, of many by the bits of their rows
+            uint64_t same = any;
+            if (__popcll(any) <= 8) {
+                for (uint64_t left = any; left;) {
+                    const int first = __ffsll(static_cast<unsigned long long>(left)) - 1;
+                    const uint32_t k0 = __builtin_amdgcn_readlane(key, first);
+                    const uint64_t m = __ballot(own && key == k0);
+                    if (key == k0) same = m;
+                    left &= ~m;
+                }
+            } else {
+                for (int b = 1; b < R; b <<= 1) {
+                    const uint64_t set = __ballot((key & b) != 0);
+                    same &= (key & b) ? set : ~set;
+                }
             }
             if (own) {
                 const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
                 const int32_t from = mine[key], to = from + rank;
-                a.order[to] = static_cast<int32_t>(t + 64 * k + lane);
-                if (to % EG_PIECE == 0) a.piece_row[to / EG_PIECE] = row[k];
+                a.order[to] = static_cast<int32_t>(token(t, k));
+                if (to % EG_PIECE == 0) a.piece_row[to / EG_PIECE] = static_cast<int32_t>(row[k]);
                 if (rank == 0) mine[key] = from + __popcll(same);
             }
             __builtin_amdgcn_wave_barrier();
@@ -185,9 +246,8 @@ __device__ __forceinline__ Raw<T, V> load_cols(const T *row, const Cols &c) {
 }
 
 // grad's columns of a lane from their sums.
-template <typename U, int V>
-__device__ __forceinline__ void finish(const EgSumArgs &a, int64_t row, const Cols &c,
-                                       float (&s)[V]) {
+template <typename U, int V, typename Args>
+__device__ __forceinline__ void finish(const Args &a, int64_t row, const Cols &c, float (&s)[V]) {
     if (!c.any) return;
     U *g = static_cast<U *>(a.grad) + row * a.ldg;
     Raw<U, V> old;
@@ -293,7 +353,7 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     const int32_t starts = a.start[row0 + (l < rows ? l : rows)];
     for (int r = 0; r < rows; ++r) {
         const int32_t first = take<LPR>(starts, r), end = take<LPR>(starts, r + 1);
-        if (end - first > EG_PIECE || (a.add && first == end)) continue;
+        if (end - first > EG_PIECE || first == end) continue;
         float s[V] = {};
         sum(first, end, s);
         finish<U, V>(a, row0 + r, c, s);
@@ -373,6 +433,113 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_join(const EgSumArgs a) {
     }
 }
 
+// ---- a gradient of few tokens ----------------------------------------------------
+// One launch: a work group of a range of rows looks through all the tokens, a
+// thread at each, and keeps those of its rows in LDS in the order in which they
+// come.  A wave sums a row's slab of columns; of a row with more than EG_ALONE tokens
+// every wave sums those among 64 of the work group's tokens, and the waves'
+// sums are joined.
+constexpr int EG_ALONE = 32;
+
+template <typename T, typename U>
+__global__ __launch_bounds__(EG_BLOCK) void k_embed_grad_small(const EgSmallArgs a) {
+    constexpr int V = 16 / sizeof(T);
+    constexpr int FLY = 8;
+    __shared__ uint32_t keys[EG_SMALL];
+    __shared__ int32_t tokens[EG_SMALL];
+    __shared__ int32_t counts[EG_SMALL_ROWS];
+    __shared__ int32_t ends[EG_WAVES];
+    __shared__ float sh[EG_WAVES][V][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t row0 = block * a.rows_per;
+    if (row0 >= a.rows) return;
+    const uint32_t n_rows =
+        static_cast<uint32_t>(a.rows - row0 < a.rows_per ? a.rows - row0 : a.rows_per);
+    uint32_t key = ~0u;
+    if (threadIdx.x < a.T) {
+        const uint32_t row = row_of(a.idx, a.wide, a.rows, a.skip, threadIdx.x);
+        if (row != ~0u) key = row - static_cast<uint32_t>(row0);
+    }
+    const bool own = key < n_rows;
+    const uint64_t mask = __ballot(own);
+    if (lane == 0) ends[wave] = __popcll(mask);
+    if (threadIdx.x < EG_SMALL_ROWS) counts[threadIdx.x] = 0;
+    __syncthreads();
+    int at = __popcll(mask & ((uint64_t{1} << lane) - 1)), n = 0;
+#pragma unroll
+    for (int w = 0; w < EG_WAVES; ++w) {
+        const int e = ends[w];
+        if (w < wave) at += e;
+        n += e;
+    }
+    if (n == 0 && a.add) return;
+    if (own) {
+        keys[at] = key;
+        tokens[at] = threadIdx.x;
+        atomicAdd(&counts[key], 1);
+    }
+    __syncthreads();
+
+    const T *dy = static_cast<const T *>(a.dy);
+    const int64_t slabs = (a.cols + 64 * V - 1) / (64 * V);
+    // s += those of the 64 kept tokens from `from` on that name row r
+    auto sum = [&](uint32_t r, int from, const Cols &c, float (&s)[V]) {
+        const bool in = from + lane < n;
+        const int32_t mine = in ? tokens[from + lane] : 0;
+        uint64_t m = __ballot(in && keys[from + lane] == r);
+        while (m) {
+            Raw<T, V> v[FLY];
+            const int have = __popcll(m);
+#pragma unroll
+            for (int k = 0; k < FLY; ++k)
+                if (k < have) {
+                    const int64_t t = __builtin_amdgcn_readlane(
+                        mine, __ffsll(static_cast<unsigned long long>(m)) - 1);
+                    m &= m - 1;
+                    if (c.any) v[k] = load_cols<T, V>(dy + t * a.ldy, c);
+                }
+#pragma unroll
+            for (int k = 0; k < FLY; ++k)
+                if (k < have)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[e] += elem<T, V>(v[k], e);
+        }
+    };
+    U *grad = static_cast<U *>(a.grad);
+    for (uint32_t r = wave; r < n_rows; r += EG_WAVES)
+        if (!a.add && counts[r] == 0)
+            zero_row(reinterpret_cast<char *>(grad + (row0 + r) * a.ldg), a.cols, sizeof(U), lane);
+    for (int64_t i = wave; i < n_rows * slabs; i += EG_WAVES) {
+        const uint32_t r = static_cast<uint32_t>(i / slabs);
+        if (counts[r] == 0 || counts[r] > EG_ALONE) continue;
+        const Cols c = cols_of<V>((i % slabs * 64 + lane) * V, a.cols);
+        float s[V] = {};
+        for (int from = 0; from < n; from += 64) sum(r, from, c, s);
+        finish<U, V>(a, row0 + r, c, s);
+    }
+    if (n <= EG_ALONE) return;
+    for (uint32_t r = 0; r < n_rows; ++r) {
+        if (counts[r] <= EG_ALONE) continue;
+        for (int64_t slab = 0; slab < slabs; ++slab) {
+            const Cols c = cols_of<V>((slab * 64 + lane) * V, a.cols);
+            float s[V] = {};
+            sum(r, wave * 64, c, s);
+#pragma unroll
+            for (int e = 0; e < V; ++e) sh[wave][e][lane] = s[e];
+            __syncthreads();
+            if (wave == 0) {
+                for (int w = 1; w < EG_WAVES; ++w)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[e] += sh[w][e][lane];
+                finish<U, V>(a, row0 + r, c, s);
+            }
+            __syncthreads();
+        }
+    }
+}
+
 int groups(int64_t waves) {
     const int64_t g = (waves + EM_WAVES - 1) / EM_WAVES;
     return static_cast<int>(g < 1 << 20 ? g : 1 << 20);
@@ -429,6 +596,17 @@ hipError_t sum_any(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, bool join, 
     return sum_from<bf16_t>(a, out_dt, join, s);
 }
 
+template <typename T>
+hipError_t small_from(const EgSmallArgs &a, gq_dtype out_dt, hipStream_t s) {
+    const int64_t blocks = (a.rows + a.rows_per - 1) / a.rows_per;
+    const int64_t x = blocks < 1 << 20 ? blocks : 1 << 20;
+    const dim3 grid(static_cast<uint32_t>(x), static_cast<uint32_t>((blocks + x - 1) / x));
+    if (out_dt == GQ_F32) k_embed_grad_small<T, float><<<grid, EG_BLOCK, 0, s>>>(a);
+    else if (out_dt == GQ_F16) k_embed_grad_small<T, __half><<<grid, EG_BLOCK, 0, s>>>(a);
+    else k_embed_grad_small<T, bf16_t><<<grid, EG_BLOCK, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_embed(const EmArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s) {
@@ -437,10 +615,23 @@ hipError_t launch_embed(const EmArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream
     return embed_from<bf16_t>(a, out_dt, s);
 }
 
+hipError_t launch_embed_grad_small(const EgSmallArgs &a, gq_dtype dt, gq_dtype out_dt,
+                                   hipStream_t s) {
+    if (dt == GQ_F32) return small_from<float>(a, out_dt, s);
+    if (dt == GQ_F16) return small_from<__half>(a, out_dt, s);
+    return small_from<bf16_t>(a, out_dt, s);
+}
+
 hipError_t launch_embed_sort(const EgSortArgs &a, hipStream_t s) {
-    const int64_t grid = (a.rows + a.rows_per - 1) / a.rows_per;
-    const size_t lds = sizeof(int32_t) * (EG_SORT_BLOCK / 64) * a.rows_per;
-    k_embed_sort<<<static_cast<uint32_t>(grid), EG_SORT_BLOCK, lds, s>>>(a);
+    const uint32_t grid = static_cast<uint32_t>((a.rows + a.rows_per - 1) / a.rows_per);
+    const size_t lds = sizeof(int32_t) * (EG_WAVES + 1) * a.rows_per;
+    if (a.keys) {
+        const int64_t blocks = (a.T + EM_BLOCK - 1) / EM_BLOCK;
+        k_embed_keys<<<static_cast<uint32_t>(blocks < 2048 ? blocks : 2048), EM_BLOCK, 0, s>>>(a);
+        k_embed_sort<true><<<grid, EG_BLOCK, lds, s>>>(a);
+    } else {
+        k_embed_sort<false><<<grid, EG_BLOCK, lds, s>>>(a);
+    }
     return hipGetLastError();
 }
 
