@@ -50,10 +50,11 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed(const EmArgs a) {
 // A counting sort in which every work group has a range of rows and looks
 // through all the tokens: how many name a row before its range says where in
 // the order its own tokens start, so no work group needs another's counts.
-// Wave w looks at the w-th sixteenth of the tokens.  It counts each row's;
-// sums over the waves and rows before give where its own tokens of a row go;
-// and in a second pass it puts them there.  Up to 16384 tokens stay in registers
-// between the passes; more are first turned into row numbers of 32 bits
+// Wave w looks at the w-th sixteenth of the tokens, counts each row's and keeps
+// its own tokens in a list in LDS; sums over the waves and rows before give where
+// its tokens of a row go, and it puts them there.  (A wave whose list is full,
+// as where one token makes up much of a batch, looks through its tokens again
+// instead.)  More than 16384 tokens are first turned into row numbers of 32 bits
 // (k_embed_keys), which take the fewest instructions to look through.
 
 // The row of token i, or ~0 where it counts for none.
@@ -70,11 +71,14 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_keys(const EgSortArgs a) {
         a.keys[i] = i < a.T ? row_of(a.idx, a.wide, a.rows, a.skip, i) : ~0u;
 }
 
+#ifndef ZNT
+#define ZNT true
+#endif
 // Zeros into n elements of `elem` bytes, by a wave.
 __device__ __forceinline__ void zero_row(char *p, int64_t n, int elem, int lane) {
     const int64_t bytes = n * elem;
     for (int64_t b = lane * 16; b + 16 <= bytes; b += 64 * 16)
-        store_v<true>(reinterpret_cast<uint32_t *>(p + b), Raw<uint32_t, 4>{});
+        store_v<ZNT>(reinterpret_cast<uint32_t *>(p + b), Raw<uint32_t, 4>{});
     const int64_t b = bytes / 16 * 16 + lane * elem;
     if (b < bytes) {
         if (elem == 4) store_1(reinterpret_cast<uint32_t *>(p + b), 0u);
@@ -82,10 +86,83 @@ __device__ __forceinline__ void zero_row(char *p, int64_t n, int elem, int lane)
     }
 }
 
+// Where a wave's token of row `key` goes, and the place behind it for the wave's
+// next: lanes of the same row get places in their order.  Only lanes that
+// `own` a token get one.  next: the wave's own, by row.
+__device__ __forceinline__ int32_t claim(uint32_t key, bool own, int32_t *next, int rows, int lane) {
+    const uint64_t any = __ballot(own);
+    // the lanes whose token names the same row: of a few tokens one row after
+    // another, of many by the bits of their rows
+    uint64_t same = any;
+    if (__popcll(any) <= 8) {
+        for (uint64_t left = any; left;) {
+            const int first = __ffsll(static_cast<unsigned long long>(left)) - 1;
+            const uint32_t k0 = __builtin_amdgcn_readlane(key, first);
+            const uint64_t m = __ballot(own && key == k0);
+            if (key == k0) same = m;
+            left &= ~m;
+        }
+    } else {
+        for (int b = 1; b < rows; b <<= 1) {
+            const uint64_t set = __ballot((key & b) != 0);
+            same &= (key & b) ? set : ~set;
+        }
+    }
+    int32_t at = 0;
+    if (own) {
+        const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
+        const int32_t from = next[key];
+        at = from + rank;
+        if (rank == 0) next[key] = from + __popcll(same);
+    }
+    __builtin_amdgcn_wave_barrier();
+    return at;
+}
+
+// Thread r of a work group: from the waves' counts of row r's tokens
+// count[wave][r], the places of the waves' first ones, and in count[EG_WAVES][r]
+// how many they are; `base` tokens come before.  Returns row r's first place.
+__device__ __forceinline__ int32_t places(int32_t *count, int rows, int32_t n_rows, int32_t base,
+                                          int32_t *scan) {
+    const int r = threadIdx.x, lane = r & 63, wave = r >> 6;
+    int32_t total = 0, c[EG_WAVES];
+    if (r < n_rows) {
+#pragma unroll
+        for (int w = 0; w < EG_WAVES; ++w) c[w] = count[w * rows + r];
+#pragma unroll
+        for (int w = 0; w < EG_WAVES; ++w) total += c[w];
+        count[EG_WAVES * rows + r] = total;
+    }
+    int32_t upto = total;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int32_t u = __shfl_up(upto, o, 64);
+        if (lane >= o) upto += u;
+    }
+    if (lane == 63) scan[wave] = upto;
+    __syncthreads();
+    int32_t at = base + upto - total;
+#pragma unroll
+    for (int w = 0; w < EG_WAVES; ++w) at += w < wave ? scan[w] : 0;
+    if (r < n_rows) {
+        int32_t next = at;
+#pragma unroll
+        for (int w = 0; w < EG_WAVES; ++w) {
+            count[w * rows + r] = next;
+            next += c[w];
+        }
+    }
+    __syncthreads();
+    return at;
+}
+
+constexpr int EG_LIST = 1024;               // tokens that a wave's list holds
+constexpr int EG_LIST_BITS = 22;            // of a token's number in it, and 10 of its row
+
 template <bool KEYS>
 __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
     constexpr int NW = EG_WAVES;
-    extern __shared__ int32_t count[];          // [NW + 1][rows_per]
+    extern __shared__ int32_t count[];      // [NW + 1][rows_per], [NW][EG_LIST]
     __shared__ int32_t before[NW];
     __shared__ int32_t scan[NW];
     const int lane = threadIdx.x & 63;
@@ -98,6 +175,7 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
     const int64_t per = (n + NW * step - 1) / (NW * step) * step;
     const int64_t t0 = wave * per, t1 = t0 + per < n ? t0 + per : n;
     for (int i = threadIdx.x; i < NW * R; i += EG_BLOCK) count[i] = 0;
+    uint32_t *list = reinterpret_cast<uint32_t *>(count + (NW + 1) * R) + wave * EG_LIST;
 
     // 64 * EG_HELD tokens from t on
     uint32_t row[EG_HELD];
@@ -118,95 +196,71 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
             }
         }
     };
-    auto token = [&](int64_t t, int k) {
-        return KEYS ? t + 64 * (k & ~3) + 4 * lane + (k & 3) : t + 64 * k + lane;
+    // the number in the wave's part of that of row[k]
+    auto number = [&](int64_t t, int k) {
+        return t - t0 + (KEYS ? 64 * (k & ~3) + 4 * lane + (k & 3) : 64 * k + lane);
     };
     if (!KEYS) load(t0);
     __syncthreads();
 
     int32_t *mine = count + wave * R;
-    int32_t less = 0;
+    int32_t less = 0, kept = 0;
     for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
         if (KEYS) load(t);
 #pragma unroll
         for (int k = 0; k < EG_HELD; ++k) {
             less += __popcll(__ballot(row[k] < row0));
             const uint32_t key = row[k] - row0;
-            if (key < n_rows) atomicAdd(&mine[key], 1);
+            const uint64_t own = __ballot(key < n_rows);
+            if (!own) continue;
+            if (key < n_rows) {
+                atomicAdd(&mine[key], 1);
+                const int32_t at = kept + __popcll(own & ((uint64_t{1} << lane) - 1));
+                if (at < EG_LIST)
+                    list[at] = key << EG_LIST_BITS | static_cast<uint32_t>(number(t, k));
+            }
+            kept += __popcll(own);
         }
     }
     if (lane == 0) before[wave] = less;
     __syncthreads();
-    // thread r: row r's tokens in each wave's part, as starts
-    int32_t total = 0;
+    int32_t base = 0;
+    for (int w = 0; w < NW; ++w) base += before[w];
+    const int32_t at = places(count, R, static_cast<int32_t>(n_rows), base, scan);
     const uint32_t r = threadIdx.x;
     if (r < n_rows) {
-        for (int w = 0; w < NW; ++w) {
-            const int32_t c = count[w * R + r];
-            count[w * R + r] = total;
-            total += c;
-        }
-        count[NW * R + r] = total;
-    }
-    int32_t upto = total;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int32_t u = __shfl_up(upto, o, 64);
-        if (lane >= o) upto += u;
-    }
-    if (lane == 63) scan[wave] = upto;
-    __syncthreads();
-    int32_t at = upto - total;
-    for (int w = 0; w < NW; ++w) {
-        at += before[w];
-        if (w < wave) at += scan[w];
-    }
-    if (r < n_rows) {
-        for (int w = 0; w < NW; ++w) count[w * R + r] += at;
         a.start[row0 + r] = at;
-        if (row0 + r == a.rows - 1) a.start[a.rows] = at + total;
+        if (row0 + r == a.rows - 1) a.start[a.rows] = at + count[NW * R + r];
     }
-    __syncthreads();
-    // the rows that no token names, while the order's loads and stores run
+    auto put = [&](uint32_t key, bool own, int64_t token) {
+        const int32_t to = claim(key, own, mine, R, lane);
+        if (!own) return;
+        a.order[to] = static_cast<int32_t>(token);
+        if (to % EG_PIECE == 0) a.piece_row[to / EG_PIECE] = static_cast<int32_t>(row0 + key);
+    };
+    if (!KEYS || (kept <= EG_LIST && per <= 1 << EG_LIST_BITS)) {
+        for (int32_t i = 0; i < kept; i += 64) {
+            const bool own = i + lane < kept;
+            const uint32_t e = own ? list[i + lane] : ~0u;
+            put(e >> EG_LIST_BITS, own, t0 + (e & ((1u << EG_LIST_BITS) - 1)));
+        }
+    } else {
+        for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
+            load(t);
+#pragma unroll 1
+            for (int k = 0; k < EG_HELD; ++k) {
+                uint32_t key = 0;
+#pragma unroll
+                for (int j = 0; j < EG_HELD; ++j) key = j == k ? row[j] - row0 : key;
+                if (__ballot(key < n_rows)) put(key, key < n_rows, t0 + number(t, k));
+            }
+        }
+    }
+    // the rows that no token names
     if (a.grad)
         for (uint32_t q = wave; q < n_rows; q += NW)
             if (count[NW * R + q] == 0)
                 zero_row(a.grad + (row0 + q) * a.ldg * a.elem, a.cols, a.elem, lane);
-    for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
-        if (KEYS) load(t);
-#pragma unroll
-        for (int k = 0; k < EG_HELD; ++k) {
-            const uint32_t key = row[k] - row0;
-            const bool own = key < n_rows;
-            const uint64_t any = __ballot(own);
-            if (!any) continue;
-            // the lanes whose token names the same row: of a few tokens one row
-            // after another, of many by the bits of their rows
-            uint64_t same = any;
-            if (__popcll(any) <= 8) {
-                for (uint64_t left = any; left;) {
-                    const int first = __ffsll(static_cast<unsigned long long>(left)) - 1;
-                    const uint32_t k0 = __builtin_amdgcn_readlane(key, first);
-                    const uint64_t m = __ballot(own && key == k0);
-                    if (key == k0) same = m;
-                    left &= ~m;
-                }
-            } else {
-                for (int b = 1; b < R; b <<= 1) {
-                    const uint64_t set = __ballot((key & b) != 0);
-                    same &= (key & b) ? set : ~set;
-                }
-            }
-            if (own) {
-                const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
-                const int32_t from = mine[key], to = from + rank;
-                a.order[to] = static_cast<int32_t>(token(t, k));
-                if (to % EG_PIECE == 0) a.piece_row[to / EG_PIECE] = static_cast<int32_t>(row[k]);
-                if (rank == 0) mine[key] = from + __popcll(same);
-            }
-            __builtin_amdgcn_wave_barrier();
-        }
-    }
 }
 
 // ---- the sums -------------------------------------------------------------------
@@ -245,13 +299,20 @@ __device__ __forceinline__ Raw<T, V> load_cols(const T *row, const Cols &c) {
     return pack<T, V>(v);
 }
 
+// What grad holds in a lane's columns, where it is added to.
+template <typename U, int V, typename Args>
+__device__ __forceinline__ Raw<U, V> old_of(const Args &a, int64_t row, const Cols &c) {
+    Raw<U, V> r = {};
+    if (a.add && c.any) r = load_cols<U, V>(static_cast<const U *>(a.grad) + row * a.ldg, c);
+    return r;
+}
+
 // grad's columns of a lane from their sums.
 template <typename U, int V, typename Args>
-__device__ __forceinline__ void finish(const Args &a, int64_t row, const Cols &c, float (&s)[V]) {
+__device__ __forceinline__ void finish(const Args &a, int64_t row, const Cols &c, float (&s)[V],
+                                       const Raw<U, V> &old) {
     if (!c.any) return;
     U *g = static_cast<U *>(a.grad) + row * a.ldg;
-    Raw<U, V> old;
-    if (a.add) old = load_cols<U, V>(g, c);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         s[k] *= a.mul;
@@ -354,21 +415,25 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     for (int r = 0; r < rows; ++r) {
         const int32_t first = take<LPR>(starts, r), end = take<LPR>(starts, r + 1);
         if (end - first > EG_PIECE || first == end) continue;
+        const Raw<U, V> old = old_of<U, V>(a, row0 + r, c);
         float s[V] = {};
         sum(first, end, s);
-        finish<U, V>(a, row0 + r, c, s);
+        finish<U, V>(a, row0 + r, c, s, old);
     }
 }
 
-// The sums of a long row's pieces, added in their order: a quarter of them by
-// each wave, then the quarters.  Work group b looks at the pieces b, b + grid,
+constexpr int EG_JOIN = 512;
+
+// The sums of a long row's pieces, added in their order: an eighth of them
+// by each wave, then the waves' sums.  Work group b looks at the pieces b, b + grid,
 // ..., a lane at each, for those in which a long row starts.
 template <typename T, typename U, int LPR>
-__global__ __launch_bounds__(EM_BLOCK) void k_embed_join(const EgSumArgs a) {
+__global__ __launch_bounds__(EG_JOIN) void k_embed_join(const EgSumArgs a) {
     using S = EgShape<T, LPR>;
     constexpr int V = S::V;
     constexpr int FLY = 4;
-    __shared__ float sh[EM_WAVES][V][64];
+    constexpr int NW = EG_JOIN / 64;
+    __shared__ float sh[NW][V][64];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t slabs = S::slabs(a.cols);
@@ -397,8 +462,10 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_join(const EgSumArgs a) {
             const int32_t s0 = __builtin_amdgcn_readfirstlane(a.start[r]);
             const int32_t s1 = __builtin_amdgcn_readfirstlane(a.start[r + 1]);
             const int32_t first = s0 / EG_PIECE, n = (s1 - 1) / EG_PIECE - first + 1;
-            const int32_t lo = static_cast<int32_t>(static_cast<int64_t>(n) * w / EM_WAVES);
-            const int32_t hi = static_cast<int32_t>(static_cast<int64_t>(n) * (w + 1) / EM_WAVES);
+            const int32_t lo = static_cast<int32_t>(static_cast<int64_t>(n) * w / NW);
+            const int32_t hi = static_cast<int32_t>(static_cast<int64_t>(n) * (w + 1) / NW);
+            Raw<U, V> old;
+            if (w == 0) old = old_of<U, V>(a, r, c);
             float s[V] = {};
             if (c.any)
                 for (int32_t j = lo; j < hi; j += FLY) {
@@ -422,11 +489,10 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_join(const EgSumArgs a) {
             for (int e = 0; e < V; ++e) sh[w][e][lane] = s[e];
             __syncthreads();
             if (w == 0) {
+                for (int q = 1; q < NW; ++q)
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-#pragma unroll
-                    for (int q = 1; q < EM_WAVES; ++q) s[e] += sh[q][e][lane];
-                finish<U, V>(a, r, c, s);
+                    for (int e = 0; e < V; ++e) s[e] += sh[q][e][lane];
+                finish<U, V>(a, r, c, s, old);
             }
             __syncthreads();
         }
@@ -434,22 +500,23 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_join(const EgSumArgs a) {
 }
 
 // ---- a gradient of few tokens ----------------------------------------------------
-// One launch: a work group of a range of rows looks through all the tokens, a
-// thread at each, and keeps those of its rows in LDS in the order in which they
-// come.  A wave sums a row's slab of columns; of a row with more than EG_ALONE tokens
-// every wave sums those among 64 of the work group's tokens, and the waves'
-// sums are joined.
-constexpr int EG_ALONE = 32;
+// One launch: a work group of a range of rows looks through all the tokens and
+// sorts those of its rows in LDS.  A wave sums a row's slab of columns; rows of more
+// than EG_ALONE tokens are summed by all waves, which share out a slab's tokens, or
+// several slabs', and join their sums.
+constexpr int EG_ALONE = 16;
 
 template <typename T, typename U>
 __global__ __launch_bounds__(EG_BLOCK) void k_embed_grad_small(const EgSmallArgs a) {
     constexpr int V = 16 / sizeof(T);
     constexpr int FLY = 8;
-    __shared__ uint32_t keys[EG_SMALL];
-    __shared__ int32_t tokens[EG_SMALL];
-    __shared__ int32_t counts[EG_SMALL_ROWS];
-    __shared__ int32_t ends[EG_WAVES];
-    __shared__ float sh[EG_WAVES][V][64];
+    constexpr int PER = EG_SMALL / EG_BLOCK;
+    constexpr int R = EG_SMALL_ROWS, NW = EG_WAVES;
+    __shared__ int32_t count[(NW + 1) * R];
+    __shared__ int32_t order[EG_SMALL];
+    __shared__ int32_t first[R];
+    __shared__ int32_t scan[NW];
+    __shared__ float sh[NW][V][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
@@ -457,87 +524,117 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_grad_small(const EgSmallArgs
     if (row0 >= a.rows) return;
     const uint32_t n_rows =
         static_cast<uint32_t>(a.rows - row0 < a.rows_per ? a.rows - row0 : a.rows_per);
-    uint32_t key = ~0u;
-    if (threadIdx.x < a.T) {
-        const uint32_t row = row_of(a.idx, a.wide, a.rows, a.skip, threadIdx.x);
-        if (row != ~0u) key = row - static_cast<uint32_t>(row0);
-    }
-    const bool own = key < n_rows;
-    const uint64_t mask = __ballot(own);
-    if (lane == 0) ends[wave] = __popcll(mask);
-    if (threadIdx.x < EG_SMALL_ROWS) counts[threadIdx.x] = 0;
-    __syncthreads();
-    int at = __popcll(mask & ((uint64_t{1} << lane) - 1)), n = 0;
+    uint32_t key[PER];
 #pragma unroll
-    for (int w = 0; w < EG_WAVES; ++w) {
-        const int e = ends[w];
-        if (w < wave) at += e;
-        n += e;
+    for (int k = 0; k < PER; ++k) {
+        const int i = k * EG_BLOCK + threadIdx.x;
+        key[k] = ~0u;
+        if (i < a.T) {
+            const uint32_t row = row_of(a.idx, a.wide, a.rows, a.skip, i);
+            if (row != ~0u) key[k] = row - static_cast<uint32_t>(row0);
+        }
     }
-    if (n == 0 && a.add) return;
-    if (own) {
-        keys[at] = key;
-        tokens[at] = threadIdx.x;
-        atomicAdd(&counts[key], 1);
+    for (int i = threadIdx.x; i < (NW + 1) * R; i += EG_BLOCK) count[i] = 0;
+    __syncthreads();
+    int32_t *mine = count + wave * R;
+    bool some = false;
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+        if (key[k] < n_rows) {
+            atomicAdd(&mine[key[k]], 1);
+            some = true;
+        }
+    if (!__syncthreads_or(some) && a.add) return;
+    const int32_t at = places(count, R, static_cast<int32_t>(n_rows), 0, scan);
+    if (threadIdx.x < R) first[threadIdx.x] = at;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const bool own = key[k] < n_rows;
+        if (!__ballot(own)) continue;
+        const int32_t to = claim(key[k], own, mine, R, lane);
+        if (own) order[to] = k * EG_BLOCK + threadIdx.x;
     }
     __syncthreads();
+    const int32_t *total = count + NW * R;
 
     const T *dy = static_cast<const T *>(a.dy);
+    U *grad = static_cast<U *>(a.grad);
     const int64_t slabs = (a.cols + 64 * V - 1) / (64 * V);
-    // s += those of the 64 kept tokens from `from` on that name row r
-    auto sum = [&](uint32_t r, int from, const Cols &c, float (&s)[V]) {
-        const bool in = from + lane < n;
-        const int32_t mine = in ? tokens[from + lane] : 0;
-        uint64_t m = __ballot(in && keys[from + lane] == r);
-        while (m) {
-            Raw<T, V> v[FLY];
-            const int have = __popcll(m);
+    // s += the tokens from .. end - 1 of the order
+    auto sum = [&](int32_t from, int32_t end, const Cols &c, float (&s)[V]) {
+        for (; from < end; from += 64) {
+            const int n = end - from < 64 ? end - from : 64;
+            const int32_t have = order[from + (lane < n ? lane : 0)];
+            for (int j = 0; j < n; j += FLY) {
+                Raw<T, V> v[FLY];
 #pragma unroll
-            for (int k = 0; k < FLY; ++k)
-                if (k < have) {
-                    const int64_t t = __builtin_amdgcn_readlane(
-                        mine, __ffsll(static_cast<unsigned long long>(m)) - 1);
-                    m &= m - 1;
-                    if (c.any) v[k] = load_cols<T, V>(dy + t * a.ldy, c);
-                }
+                for (int k = 0; k < FLY; ++k)
+                    if (j + k < n) {
+                        const int64_t t = __builtin_amdgcn_readlane(have, j + k);
+                        if (c.any) v[k] = load_cols<T, V>(dy + t * a.ldy, c);
+                    }
 #pragma unroll
-            for (int k = 0; k < FLY; ++k)
-                if (k < have)
+                for (int k = 0; k < FLY; ++k)
+                    if (j + k < n)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) s[e] += elem<T, V>(v[k], e);
+                        for (int e = 0; e < V; ++e) s[e] += elem<T, V>(v[k], e);
+            }
         }
     };
-    U *grad = static_cast<U *>(a.grad);
-    for (uint32_t r = wave; r < n_rows; r += EG_WAVES)
-        if (!a.add && counts[r] == 0)
-            zero_row(reinterpret_cast<char *>(grad + (row0 + r) * a.ldg), a.cols, sizeof(U), lane);
-    for (int64_t i = wave; i < n_rows * slabs; i += EG_WAVES) {
-        const uint32_t r = static_cast<uint32_t>(i / slabs);
-        if (counts[r] == 0 || counts[r] > EG_ALONE) continue;
-        const Cols c = cols_of<V>((i % slabs * 64 + lane) * V, a.cols);
-        float s[V] = {};
-        for (int from = 0; from < n; from += 64) sum(r, from, c, s);
-        finish<U, V>(a, row0 + r, c, s);
-    }
-    if (n <= EG_ALONE) return;
-    for (uint32_t r = 0; r < n_rows; ++r) {
-        if (counts[r] <= EG_ALONE) continue;
-        for (int64_t slab = 0; slab < slabs; ++slab) {
-            const Cols c = cols_of<V>((slab * 64 + lane) * V, a.cols);
-            float s[V] = {};
-            sum(r, wave * 64, c, s);
+    // this lane's rows' tokens, and the rows of few and of many as bits
+    static_assert(R == 128, "two rows a lane");
+    const int32_t n_of[2] = {total[lane], total[lane + 64]};
+    const int32_t first_of[2] = {first[lane], first[lane + 64]};
+    uint32_t items = 0;
 #pragma unroll
-            for (int e = 0; e < V; ++e) sh[wave][e][lane] = s[e];
-            __syncthreads();
-            if (wave == 0) {
-                for (int w = 1; w < EG_WAVES; ++w)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) s[e] += sh[w][e][lane];
-                finish<U, V>(a, row0 + r, c, s);
+    for (int h = 0; h < 2; ++h)
+        for (uint64_t m = __ballot(n_of[h] > 0 && n_of[h] <= EG_ALONE); m; m &= m - 1) {
+            const int bit = __ffsll(static_cast<unsigned long long>(m)) - 1;
+            const int32_t n = __builtin_amdgcn_readlane(n_of[h], bit);
+            const int32_t from = __builtin_amdgcn_readlane(first_of[h], bit);
+            for (int64_t slab = (wave - items) % NW; slab < slabs; slab += NW) {
+                const Cols c = cols_of<V>((slab * 64 + lane) * V, a.cols);
+                const Raw<U, V> old = old_of<U, V>(a, row0 + 64 * h + bit, c);
+                float s[V] = {};
+                sum(from, from + n, c, s);
+                finish<U, V>(a, row0 + 64 * h + bit, c, s, old);
             }
-            __syncthreads();
+            items += static_cast<uint32_t>(slabs);
         }
-    }
+    // `at_once` slabs at a time, each by `parts` waves
+    const int at_once = slabs < NW ? static_cast<int>(slabs) : NW, parts = NW / at_once;
+    const int my_slab = wave / parts, part = wave % parts;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        for (uint64_t m = __ballot(n_of[h] > EG_ALONE); m; m &= m - 1) {
+            const int bit = __ffsll(static_cast<unsigned long long>(m)) - 1;
+            const int64_t row = row0 + 64 * h + bit;
+            const int32_t n = __builtin_amdgcn_readlane(n_of[h], bit);
+            const int32_t from = __builtin_amdgcn_readlane(first_of[h], bit);
+            for (int64_t s0 = 0; s0 < slabs; s0 += at_once) {
+                const bool in = my_slab < at_once && s0 + my_slab < slabs;
+                const Cols c = cols_of<V>(((s0 + my_slab) * 64 + lane) * V, in ? a.cols : 0);
+                Raw<U, V> old;
+                if (part == 0) old = old_of<U, V>(a, row, c);
+                float s[V] = {};
+                if (in) sum(from + n * part / parts, from + n * (part + 1) / parts, c, s);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sh[wave][e][lane] = s[e];
+                __syncthreads();
+                if (part == 0 && in) {
+                    for (int w = 1; w < parts; ++w)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) s[e] += sh[wave + w][e][lane];
+                    finish<U, V>(a, row, c, s, old);
+                }
+                __syncthreads();
+            }
+        }
+    if (!a.add)
+        for (uint32_t r = wave; r < n_rows; r += NW)
+            if (total[r] == 0)
+                zero_row(reinterpret_cast<char *>(grad + (row0 + r) * a.ldg), a.cols, sizeof(U),
+                         lane);
 }
 
 int groups(int64_t waves) {
@@ -562,7 +659,7 @@ hipError_t sum_as(const EgSumArgs &a, bool join, hipStream_t s) {
     if (join) {
         const dim3 grid(static_cast<uint32_t>(a.pieces < 256 ? a.pieces : 256),
                         static_cast<uint32_t>(slabs));
-        k_embed_join<T, U, LPR><<<grid, EM_BLOCK, 0, s>>>(a);
+        k_embed_join<T, U, LPR><<<grid, EG_JOIN, 0, s>>>(a);
     } else {
         const int64_t units = a.pieces + (a.rows + S::GROUP - 1) / S::GROUP;
         constexpr int64_t per = S::SUB * EM_WAVES;
@@ -624,7 +721,7 @@ hipError_t launch_embed_grad_small(const EgSmallArgs &a, gq_dtype dt, gq_dtype o
 
 hipError_t launch_embed_sort(const EgSortArgs &a, hipStream_t s) {
     const uint32_t grid = static_cast<uint32_t>((a.rows + a.rows_per - 1) / a.rows_per);
-    const size_t lds = sizeof(int32_t) * (EG_WAVES + 1) * a.rows_per;
+    const size_t lds = sizeof(int32_t) * ((EG_WAVES + 1) * a.rows_per + EG_WAVES * EG_LIST);
     if (a.keys) {
         const int64_t blocks = (a.T + EM_BLOCK - 1) / EM_BLOCK;
         k_embed_keys<<<static_cast<uint32_t>(blocks < 2048 ? blocks : 2048), EM_BLOCK, 0, s>>>(a);
