@@ -21,7 +21,10 @@ struct EmArgs {
 constexpr int EG_BLOCK = 1024;          // threads of a work group that orders tokens
 constexpr int EG_WAVES = EG_BLOCK / 64;
 constexpr int EG_SORT_ROWS = 1024;      // most rows of the table per work group
-constexpr int EG_PIECE = 64;            // tokens that one wave sums
+#ifndef XPIECE
+#define XPIECE 64
+#endif
+constexpr int EG_PIECE = XPIECE;            // tokens that one wave sums
 constexpr int EG_SMALL = 4 * EG_BLOCK;  // most tokens of a gradient in one launch
 constexpr int EG_SMALL_ROWS = 128;      // most rows of the table per work group there
 constexpr int EG_HELD = 16;             // tokens of a lane in flight

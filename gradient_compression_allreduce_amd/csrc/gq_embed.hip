@@ -11,6 +11,18 @@
 namespace gq {
 namespace {
 
+#ifndef XGROUP
+#define XGROUP 4
+#endif
+#ifndef XFLY
+#define XFLY 16
+#endif
+#ifndef ENT
+#define ENT true
+#endif
+#ifndef EW
+#define EW 4
+#endif
 constexpr int EM_BLOCK = 256;
 constexpr int EM_WAVES = EM_BLOCK / 64;
 
@@ -18,30 +30,47 @@ __device__ __forceinline__ int64_t index_at(const void *idx, bool wide, int64_t 
     return wide ? static_cast<const int64_t *>(idx)[t] : static_cast<const int32_t *>(idx)[t];
 }
 
-// A wave takes 64 vectors of a row.
-template <typename T, typename U>
+// LPR lanes of a wave share a row (64, or fewer where a row has few columns), so
+// a wave takes 64 / LPR slabs of LPR vectors at once, W times, one after another
+// in the output, and has all of their loads in flight.
+template <typename T, typename U, int LPR, int W>
 __global__ __launch_bounds__(EM_BLOCK) void k_embed(const EmArgs a) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 16 / sizeof(T), SUB = 64 / LPR;
     const int lane = threadIdx.x & 63;
-    const int64_t slabs = (a.cols + 64 * V - 1) / (64 * V);
+    const int64_t slabs = (a.cols + LPR * V - 1) / (LPR * V), n = a.T * slabs;
+    const int64_t wave = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * EM_WAVES +
+                         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t i0 = wave * (SUB * W) + (SUB > 1 ? lane / LPR : 0);
     const T *table = static_cast<const T *>(a.table);
     U *out = static_cast<U *>(a.out);
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * EM_WAVES + (threadIdx.x >> 6);
-         i < a.T * slabs; i += static_cast<int64_t>(gridDim.x) * EM_WAVES) {
-        const int64_t t = i / slabs, col = (i % slabs * 64 + lane) * V;
-        const int64_t v = index_at(a.idx, a.wide, t);
-        const bool inside = v >= 0 && v < a.rows;
-        const T *x = table + (inside ? v : 0) * a.ld + col;
-        U *y = out + t * a.ldo + col;
-        if (col + V <= a.cols) {
-            float g[V];
-            const Raw<T, V> r = load_v<false, T, V>(x);
+    int64_t t[W], col[W], v[W];
+    Raw<T, V> r[W];
 #pragma unroll
-            for (int k = 0; k < V; ++k) g[k] = inside ? elem<T, V>(r, k) * a.mul : 0.0f;
-            store_v<true, U, V>(y, pack<U, V>(g));
+    for (int k = 0; k < W; ++k) {
+        const int64_t i = i0 + k * SUB < n ? i0 + k * SUB : n - 1;
+        t[k] = SUB > 1 ? i : i / slabs;
+        col[k] = ((SUB > 1 ? 0 : i % slabs * LPR) + lane % LPR) * V;
+        v[k] = index_at(a.idx, a.wide, t[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        if (v[k] < 0 || v[k] >= a.rows) v[k] = -1;
+        if (v[k] >= 0 && col[k] + V <= a.cols)
+            r[k] = load_v<false, T, V>(table + v[k] * a.ld + col[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        if (i0 + k * SUB >= n) break;
+        U *y = out + t[k] * a.ldo + col[k];
+        if (col[k] + V <= a.cols) {
+            float g[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[e] = v[k] >= 0 ? elem<T, V>(r[k], e) * a.mul : 0.0f;
+            store_v<ENT, U, V>(y, pack<U, V>(g));
         } else {
-            for (int k = 0; k < V && col + k < a.cols; ++k)
-                y[k] = from_f32<U>(inside ? to_f32(x[k]) * a.mul : 0.0f);
+            const T *x = table + (v[k] >= 0 ? v[k] : 0) * a.ld + col[k];
+            for (int e = 0; e < V && col[k] + e < a.cols; ++e)
+                y[e] = from_f32<U>(v[k] >= 0 ? to_f32(x[e]) * a.mul : 0.0f);
         }
     }
 }
@@ -72,7 +101,7 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_keys(const EgSortArgs a) {
 }
 
 #ifndef ZNT
-#define ZNT true
+#define ZNT false
 #endif
 // Zeros into n elements of `elem` bytes, by a wave.
 __device__ __forceinline__ void zero_row(char *p, int64_t n, int elem, int lane) {
@@ -196,31 +225,36 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
             }
         }
     };
-    // the number in the wave's part of that of row[k]
-    auto number = [&](int64_t t, int k) {
-        return t - t0 + (KEYS ? 64 * (k & ~3) + 4 * lane + (k & 3) : 64 * k + lane);
+    // the number of row[k]'s token, where row[]'s first one has number `first`
+    auto number = [&](int64_t first, int k) {
+        return first + (KEYS ? 64 * (k & ~3) + 4 * lane + (k & 3) : 64 * k + lane);
     };
     if (!KEYS) load(t0);
     __syncthreads();
 
     int32_t *mine = count + wave * R;
     int32_t less = 0, kept = 0;
-    for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
-        if (KEYS) load(t);
+    // this wave's own tokens of row[] to the list's end, as far as it holds them;
+    // row[]'s first token has number `first`
+    auto keep = [&](int64_t first, bool tally) {
 #pragma unroll
         for (int k = 0; k < EG_HELD; ++k) {
-            less += __popcll(__ballot(row[k] < row0));
+            if (tally) less += __popcll(__ballot(row[k] < row0));
             const uint32_t key = row[k] - row0;
             const uint64_t own = __ballot(key < n_rows);
             if (!own) continue;
             if (key < n_rows) {
-                atomicAdd(&mine[key], 1);
+                if (tally) atomicAdd(&mine[key], 1);
                 const int32_t at = kept + __popcll(own & ((uint64_t{1} << lane) - 1));
                 if (at < EG_LIST)
-                    list[at] = key << EG_LIST_BITS | static_cast<uint32_t>(number(t, k));
+                    list[at] = key << EG_LIST_BITS | static_cast<uint32_t>(number(first, k));
             }
             kept += __popcll(own);
         }
+    };
+    for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
+        if (KEYS) load(t);
+        keep(t - t0, true);
     }
     if (lane == 0) before[wave] = less;
     __syncthreads();
@@ -232,28 +266,27 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
         a.start[row0 + r] = at;
         if (row0 + r == a.rows - 1) a.start[a.rows] = at + count[NW * R + r];
     }
-    auto put = [&](uint32_t key, bool own, int64_t token) {
-        const int32_t to = claim(key, own, mine, R, lane);
-        if (!own) return;
-        a.order[to] = static_cast<int32_t>(token);
-        if (to % EG_PIECE == 0) a.piece_row[to / EG_PIECE] = static_cast<int32_t>(row0 + key);
-    };
-    if (!KEYS || (kept <= EG_LIST && per <= 1 << EG_LIST_BITS)) {
+    // the list's tokens to their places; their numbers count from `from`
+    auto put = [&](int64_t from) {
         for (int32_t i = 0; i < kept; i += 64) {
             const bool own = i + lane < kept;
-            const uint32_t e = own ? list[i + lane] : ~0u;
-            put(e >> EG_LIST_BITS, own, t0 + (e & ((1u << EG_LIST_BITS) - 1)));
+            const uint32_t e = own ? list[i + lane] : 0, key = e >> EG_LIST_BITS;
+            const int32_t to = claim(key, own, mine, R, lane);
+            if (!own) continue;
+            a.order[to] = static_cast<int32_t>(from + (e & ((1u << EG_LIST_BITS) - 1)));
+            if (to % EG_PIECE == 0) a.piece_row[to / EG_PIECE] = static_cast<int32_t>(row0 + key);
         }
+    };
+    if (!KEYS || (kept <= EG_LIST && per <= 1 << EG_LIST_BITS)) {
+        put(t0);
     } else {
+        // (a load of tokens always fits an empty list)
+        static_assert(64 * EG_HELD <= EG_LIST, "");
         for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
             load(t);
-#pragma unroll 1
-            for (int k = 0; k < EG_HELD; ++k) {
-                uint32_t key = 0;
-#pragma unroll
-                for (int j = 0; j < EG_HELD; ++j) key = j == k ? row[j] - row0 : key;
-                if (__ballot(key < n_rows)) put(key, key < n_rows, t0 + number(t, k));
-            }
+            kept = 0;
+            keep(0, false);
+            put(t);
         }
     }
     // the rows that no token names
@@ -315,8 +348,8 @@ __device__ __forceinline__ void finish(const Args &a, int64_t row, const Cols &c
     U *g = static_cast<U *>(a.grad) + row * a.ldg;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        s[k] *= a.mul;
-        if (a.add) s[k] += elem<U, V>(old, k);
+        // (0 is added so that no sum of nothing becomes -0)
+        s[k] = s[k] * a.mul + (a.add ? elem<U, V>(old, k) : 0.0f);
     }
     if (!c.n && !c.skip) {
         store_v<true, U, V>(g + c.col, pack<U, V>(s));
@@ -331,8 +364,8 @@ template <typename T, int LPR>
 struct EgShape {
     static constexpr int V = 16 / sizeof(T);
     static constexpr int SUB = 64 / LPR;                // rows of a wave at once
-    static constexpr int GROUP = LPR > 8 ? 8 : LPR - 1; // rows of LPR lanes, one after another
-    static constexpr int FLY = LPR > 8 ? 8 : LPR;       // tokens in flight
+    static constexpr int GROUP = LPR > 8 ? XGROUP : LPR - 1; // rows of LPR lanes, one after another
+    static constexpr int FLY = LPR > 8 ? XFLY : LPR;       // tokens in flight
     static __host__ __device__ int64_t slabs(int64_t cols) {
         return (cols + LPR * V - 1) / (LPR * V);
     }
@@ -358,17 +391,25 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     const Cols c = cols_of<V>((slab * LPR + l) * V, a.cols);
     const T *dy = static_cast<const T *>(a.dy);
 
+    // the tokens of the order from `held` on, LPR or up to held_end, a lane at each
+    int32_t held = 0, held_end = 0, have = 0;
+    auto hold = [&](int32_t at, int32_t end) {
+        held = at;
+        held_end = end - at < LPR ? end : at + LPR;
+        have = 0;
+        if (at + l < end) have = a.order[at + l];
+    };
     // s += the tokens first .. end - 1 of the order
     auto sum = [&](int32_t first, int32_t end, float (&s)[V]) {
         for (int32_t at = first; at < end; at += LPR) {
-            int32_t have = 0;
-            if (at + l < end) have = a.order[at + l];
             const int n = end - at < LPR ? end - at : LPR;
+            if (at < held || at + n > held_end) hold(at, end);
+            const int skip = at - held;
             for (int j = 0; j < n; j += FLY) {
                 Raw<T, V> v[FLY];
 #pragma unroll
                 for (int k = 0; k < FLY; ++k) {
-                    const int64_t t = take<LPR>(have, j + k < LPR ? j + k : 0);
+                    const int64_t t = take<LPR>(have, j + k < n ? skip + j + k : 0);
                     if (j + k < n && c.any) v[k] = load_cols<T, V>(dy + t * a.ldy, c);
                 }
 #pragma unroll
@@ -384,27 +425,29 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     };
 
     if (unit < a.pieces) {
+        // (what lies behind the last token's piece is of no meaning)
         const int32_t total = uniform(a.start[a.rows]);
+        int32_t head = a.piece_row[unit];
+        int32_t tail = a.piece_row[unit + 1 < a.pieces ? unit + 1 : unit];
         const int64_t from = unit * EG_PIECE;
         if (from >= total) return;
         const int32_t begin = static_cast<int32_t>(from);
         const int32_t stop = total - begin < EG_PIECE ? total : begin + EG_PIECE;
-        const int32_t head = uniform(a.piece_row[unit]);
+        head = uniform(head);
+        tail = uniform(stop < total ? tail : head);
         const int32_t h0 = uniform(a.start[head]), h1 = uniform(a.start[head + 1]);
+        const int32_t t0 = uniform(a.start[tail]), t1 = uniform(a.start[tail + 1]);
+        hold(begin, stop);
         const int64_t place = (unit * 2 * slabs + slab) * (LPR * V) + l * V;
         if (h1 - h0 > EG_PIECE) {
             float s[V] = {};
             sum(begin, h1 < stop ? h1 : stop, s);
             store_v<false, float, V>(a.part + place, pack<float, V>(s));
         }
-        if (stop < total) {
-            const int32_t tail = uniform(a.piece_row[unit + 1]);
-            const int32_t t0 = uniform(a.start[tail]), t1 = uniform(a.start[tail + 1]);
-            if (tail != head && t0 < stop && t1 - t0 > EG_PIECE) {
-                float s[V] = {};
-                sum(t0, stop, s);
-                store_v<false, float, V>(a.part + place + slabs * (LPR * V), pack<float, V>(s));
-            }
+        if (tail != head && t0 < stop && t1 - t0 > EG_PIECE) {
+            float s[V] = {};
+            sum(t0, stop, s);
+            store_v<false, float, V>(a.part + place + slabs * (LPR * V), pack<float, V>(s));
         }
         return;
     }
@@ -412,6 +455,7 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     if (row0 >= a.rows) return;
     const int rows = static_cast<int>(a.rows - row0 < S::GROUP ? a.rows - row0 : S::GROUP);
     const int32_t starts = a.start[row0 + (l < rows ? l : rows)];
+    hold(take<LPR>(starts, 0), take<LPR>(starts, rows));
     for (int r = 0; r < rows; ++r) {
         const int32_t first = take<LPR>(starts, r), end = take<LPR>(starts, r + 1);
         if (end - first > EG_PIECE || first == end) continue;
@@ -438,29 +482,35 @@ __global__ __launch_bounds__(EG_JOIN) void k_embed_join(const EgSumArgs a) {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t slabs = S::slabs(a.cols);
     const int64_t slab = blockIdx.y;
-    const int32_t total = a.start[a.rows];
-    const int64_t pieces = (static_cast<int64_t>(total) + EG_PIECE - 1) / EG_PIECE;
     const Cols c = cols_of<V>((slab * LPR + lane) * V, lane < LPR ? a.cols : 0);
-    for (int64_t p0 = blockIdx.x; p0 < pieces; p0 += static_cast<int64_t>(gridDim.x) * 64) {
-        // the long row that starts in this lane's piece: its first piece's
+    for (int64_t p0 = blockIdx.x; p0 < a.pieces; p0 += static_cast<int64_t>(gridDim.x) * 64) {
+        // the long row that starts in this lane's piece, if any: that of its
         // first token, or the one that the next piece starts with
         const int64_t p = p0 + static_cast<int64_t>(gridDim.x) * lane;
-        int32_t row = -1;
-        if (p < pieces) {
-            int32_t r = a.piece_row[p];
-            if (a.start[r] < p * EG_PIECE) r = p + 1 < pieces ? a.piece_row[p + 1] : -1;
-            else if (a.start[r + 1] - a.start[r] <= EG_PIECE && p + 1 < pieces) r = a.piece_row[p + 1];
-            if (r >= 0 && a.start[r] >= p * EG_PIECE && a.start[r] < (p + 1) * EG_PIECE &&
-                a.start[r + 1] - a.start[r] > EG_PIECE)
-                row = r;
+        const int64_t total = a.start[a.rows];
+        int32_t row = -1, begin = 0, stop = 0;
+        if (p * EG_PIECE < total) {
+            const bool last = (p + 1) * EG_PIECE >= total;
+            const int32_t r0 = a.piece_row[p], r1 = last ? r0 : a.piece_row[p + 1];
+            const int32_t b0 = a.start[r0], e0 = a.start[r0 + 1];
+            const int32_t b1 = a.start[r1], e1 = a.start[r1 + 1];
+            if (b0 == p * EG_PIECE && e0 - b0 > EG_PIECE) {
+                row = r0;
+                begin = b0;
+                stop = e0;
+            } else if (b1 > p * EG_PIECE && b1 < (p + 1) * EG_PIECE && e1 - b1 > EG_PIECE) {
+                row = r1;
+                begin = b1;
+                stop = e1;
+            }
         }
         uint64_t found = __ballot(row >= 0);
         while (found) {
             const int from = __ffsll(static_cast<unsigned long long>(found)) - 1;
             found &= found - 1;
             const int32_t r = __builtin_amdgcn_readlane(row, from);
-            const int32_t s0 = __builtin_amdgcn_readfirstlane(a.start[r]);
-            const int32_t s1 = __builtin_amdgcn_readfirstlane(a.start[r + 1]);
+            const int32_t s0 = __builtin_amdgcn_readlane(begin, from);
+            const int32_t s1 = __builtin_amdgcn_readlane(stop, from);
             const int32_t first = s0 / EG_PIECE, n = (s1 - 1) / EG_PIECE - first + 1;
             const int32_t lo = static_cast<int32_t>(static_cast<int64_t>(n) * w / NW);
             const int32_t hi = static_cast<int32_t>(static_cast<int64_t>(n) * (w + 1) / NW);
@@ -637,19 +687,37 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_grad_small(const EgSmallArgs
                          lane);
 }
 
-int groups(int64_t waves) {
-    const int64_t g = (waves + EM_WAVES - 1) / EM_WAVES;
-    return static_cast<int>(g < 1 << 20 ? g : 1 << 20);
+// A grid of that many work groups, whose sides have less than 2^32 work-items;
+// those that are too many find nothing to do.
+dim3 grid_of(int64_t blocks) {
+    const int64_t x = blocks < 1 << 20 ? blocks : 1 << 20;
+    return dim3(static_cast<uint32_t>(x), static_cast<uint32_t>((blocks + x - 1) / x));
+}
+
+template <typename T, typename U, int LPR>
+hipError_t embed_as(const EmArgs &a, hipStream_t s) {
+    constexpr int64_t slab = LPR * 16 / sizeof(T), per = 64 / LPR * EM_WAVES;
+    const int64_t n = a.T * ((a.cols + slab - 1) / slab);
+    if (n >= EW * 2048 * per)
+        k_embed<T, U, LPR, EW><<<grid_of((n + EW * per - 1) / (EW * per)), EM_BLOCK, 0, s>>>(a);
+    else
+        k_embed<T, U, LPR, 1><<<grid_of((n + per - 1) / per), EM_BLOCK, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, typename U>
+hipError_t embed_into(const EmArgs &a, hipStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (a.cols <= 4 * V) return embed_as<T, U, 4>(a, s);
+    if (a.cols <= 16 * V) return embed_as<T, U, 16>(a, s);
+    return embed_as<T, U, 64>(a, s);
 }
 
 template <typename T>
 hipError_t embed_from(const EmArgs &a, gq_dtype out_dt, hipStream_t s) {
-    constexpr int64_t slab = 64 * 16 / sizeof(T);
-    const int grid = groups(a.T * ((a.cols + slab - 1) / slab));
-    if (out_dt == GQ_F32) k_embed<T, float><<<grid, EM_BLOCK, 0, s>>>(a);
-    else if (out_dt == GQ_F16) k_embed<T, __half><<<grid, EM_BLOCK, 0, s>>>(a);
-    else k_embed<T, bf16_t><<<grid, EM_BLOCK, 0, s>>>(a);
-    return hipGetLastError();
+    if (out_dt == GQ_F32) return embed_into<T, float>(a, s);
+    if (out_dt == GQ_F16) return embed_into<T, __half>(a, s);
+    return embed_into<T, bf16_t>(a, s);
 }
 
 template <typename T, typename U, int LPR>
@@ -664,10 +732,7 @@ hipError_t sum_as(const EgSumArgs &a, bool join, hipStream_t s) {
         const int64_t units = a.pieces + (a.rows + S::GROUP - 1) / S::GROUP;
         constexpr int64_t per = S::SUB * EM_WAVES;
         const int64_t blocks = (units * slabs + per - 1) / per;
-        // (a grid's side has less than 2^32 work-items)
-        const int64_t x = blocks < 1 << 20 ? blocks : 1 << 20;
-        const dim3 grid(static_cast<uint32_t>(x), static_cast<uint32_t>((blocks + x - 1) / x));
-        k_embed_sum<T, U, LPR><<<grid, EM_BLOCK, 0, s>>>(a);
+        k_embed_sum<T, U, LPR><<<grid_of(blocks), EM_BLOCK, 0, s>>>(a);
     }
     return hipGetLastError();
 }
@@ -696,8 +761,7 @@ hipError_t sum_any(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, bool join, 
 template <typename T>
 hipError_t small_from(const EgSmallArgs &a, gq_dtype out_dt, hipStream_t s) {
     const int64_t blocks = (a.rows + a.rows_per - 1) / a.rows_per;
-    const int64_t x = blocks < 1 << 20 ? blocks : 1 << 20;
-    const dim3 grid(static_cast<uint32_t>(x), static_cast<uint32_t>((blocks + x - 1) / x));
+    const dim3 grid = grid_of(blocks);
     if (out_dt == GQ_F32) k_embed_grad_small<T, float><<<grid, EG_BLOCK, 0, s>>>(a);
     else if (out_dt == GQ_F16) k_embed_grad_small<T, __half><<<grid, EG_BLOCK, 0, s>>>(a);
     else k_embed_grad_small<T, bf16_t><<<grid, EG_BLOCK, 0, s>>>(a);
