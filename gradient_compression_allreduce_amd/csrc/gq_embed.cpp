@@ -121,9 +121,8 @@ gq_status gq_embed_grad(const void *idx, int32_t idx_bytes, int64_t tokens, cons
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool wide = idx_bytes == 8, add = accumulate != 0;
     if (tokens <= EG_SMALL) {
-        // two work groups per compute unit, of 16 rows or more
-        const int64_t per = std::min<int64_t>(EG_SMALL_ROWS,
-                                              std::max<int64_t>(16, (rows + 511) / 512));
+        // two work groups per compute unit
+        const int64_t per = std::min<int64_t>(EG_SMALL_ROWS, (rows + 511) / 512);
         const EgSmallArgs a = {idx, dy,  grad, tokens, rows, cols, ldy, ldg, skip,
                                static_cast<int32_t>(per), mul, wide, add};
         return arg_launch(op, launch_embed_grad_small(a, dt, out_dt, st));

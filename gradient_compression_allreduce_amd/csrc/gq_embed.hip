@@ -11,20 +11,9 @@
 namespace gq {
 namespace {
 
-#ifndef XGROUP
-#define XGROUP 4
-#endif
-#ifndef XFLY
-#define XFLY 16
-#endif
-#ifndef ENT
-#define ENT true
-#endif
-#ifndef EW
-#define EW 4
-#endif
 constexpr int EM_BLOCK = 256;
 constexpr int EM_WAVES = EM_BLOCK / 64;
+constexpr int EM_SLABS = 4;          // slabs of a wave in long lookups
 
 __device__ __forceinline__ int64_t index_at(const void *idx, bool wide, int64_t t) {
     return wide ? static_cast<const int64_t *>(idx)[t] : static_cast<const int32_t *>(idx)[t];
@@ -66,7 +55,7 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed(const EmArgs a) {
             float g[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) g[e] = v[k] >= 0 ? elem<T, V>(r[k], e) * a.mul : 0.0f;
-            store_v<ENT, U, V>(y, pack<U, V>(g));
+            store_v<true, U, V>(y, pack<U, V>(g));
         } else {
             const T *x = table + (v[k] >= 0 ? v[k] : 0) * a.ld + col[k];
             for (int e = 0; e < V && col[k] + e < a.cols; ++e)
@@ -100,19 +89,48 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_keys(const EgSortArgs a) {
         a.keys[i] = i < a.T ? row_of(a.idx, a.wide, a.rows, a.skip, i) : ~0u;
 }
 
-#ifndef ZNT
-#define ZNT false
-#endif
-// Zeros into n elements of `elem` bytes, by a wave.
-__device__ __forceinline__ void zero_row(char *p, int64_t n, int elem, int lane) {
-    const int64_t bytes = n * elem;
-    for (int64_t b = lane * 16; b + 16 <= bytes; b += 64 * 16)
-        store_v<ZNT>(reinterpret_cast<uint32_t *>(p + b), Raw<uint32_t, 4>{});
-    const int64_t b = bytes / 16 * 16 + lane * elem;
-    if (b < bytes) {
-        if (elem == 4) store_1(reinterpret_cast<uint32_t *>(p + b), 0u);
-        else store_1(reinterpret_cast<uint16_t *>(p + b), uint16_t{0});
+// Zeros into the rows of a work group's range that have no token: n_rows rows of
+// cols elements of `elem` bytes from `to` on, ld elements apart, whose
+// tokens are counted in `total`.  A wave takes a row, or 64 lanes as many
+// slots of 16 bytes of rows that have fewer.
+__device__ __forceinline__ void zero_rows(char *to, uint32_t n_rows, int64_t cols, int64_t ld,
+                                          int elem, const int32_t *total, int wave, int lane) {
+    const int64_t bytes = cols * elem;
+    auto zero = [&](char *p, int64_t b) {       // a slot
+        if (b + 16 <= bytes) {
+            store_v<false>(reinterpret_cast<uint32_t *>(p + b), Raw<uint32_t, 4>{});
+        } else {
+#pragma unroll 1
+            for (; b < bytes; b += elem) {
+                if (elem == 4) store_1(reinterpret_cast<uint32_t *>(p + b), 0u);
+                else store_1(reinterpret_cast<uint16_t *>(p + b), uint16_t{0});
+            }
+        }
+    };
+    if (bytes < 64 * 16) {
+        const uint32_t slots = static_cast<uint32_t>(bytes + 15) / 16;
+        for (uint32_t i = wave * 64 + lane; i < n_rows * slots; i += EG_BLOCK) {
+            const uint32_t r = i / slots;
+            if (total[r] == 0) zero(to + r * ld * elem, (i - r * slots) * 16);
+        }
+    } else {
+        for (uint32_t r = wave; r < n_rows; r += EG_WAVES)
+            if (total[r] == 0) {
+                char *p = to + r * ld * elem;
+                int64_t b = lane * 16;
+                for (; b + 16 <= bytes; b += 64 * 16)
+                    store_v<false>(reinterpret_cast<uint32_t *>(p + b), Raw<uint32_t, 4>{});
+                zero(p, b);
+            }
     }
+}
+
+// What lanes of a wave wrote to LDS is what its other lanes read from here on (LDS
+// serves a wave's accesses in order: this is for the compiler).
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Where a wave's token of row `key` goes, and the place behind it for the wave's
@@ -142,9 +160,10 @@ __device__ __forceinline__ int32_t claim(uint32_t key, bool own, int32_t *next, 
         const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
         const int32_t from = next[key];
         at = from + rank;
+        wave_fence();
         if (rank == 0) next[key] = from + __popcll(same);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_fence();
     return at;
 }
 
@@ -266,8 +285,13 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
         a.start[row0 + r] = at;
         if (row0 + r == a.rows - 1) a.start[a.rows] = at + count[NW * R + r];
     }
+    // the rows that no token names (the stores go on while the rest runs)
+    if (a.grad)
+        zero_rows(a.grad + row0 * a.ldg * a.elem, n_rows, a.cols, a.ldg, a.elem, count + NW * R,
+                  wave, lane);
     // the list's tokens to their places; their numbers count from `from`
     auto put = [&](int64_t from) {
+        wave_fence();
         for (int32_t i = 0; i < kept; i += 64) {
             const bool own = i + lane < kept;
             const uint32_t e = own ? list[i + lane] : 0, key = e >> EG_LIST_BITS;
@@ -285,15 +309,11 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
         for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
             load(t);
             kept = 0;
+            wave_fence();
             keep(0, false);
             put(t);
         }
     }
-    // the rows that no token names
-    if (a.grad)
-        for (uint32_t q = wave; q < n_rows; q += NW)
-            if (count[NW * R + q] == 0)
-                zero_row(a.grad + (row0 + q) * a.ldg * a.elem, a.cols, a.elem, lane);
 }
 
 // ---- the sums -------------------------------------------------------------------
@@ -364,8 +384,9 @@ template <typename T, int LPR>
 struct EgShape {
     static constexpr int V = 16 / sizeof(T);
     static constexpr int SUB = 64 / LPR;                // rows of a wave at once
-    static constexpr int GROUP = LPR > 8 ? XGROUP : LPR - 1; // rows of LPR lanes, one after another
-    static constexpr int FLY = LPR > 8 ? XFLY : LPR;       // tokens in flight
+    static constexpr int GROUP = LPR == 64 ? 4 : 1;      // rows of LPR lanes, one after another
+    static constexpr int FLY = 16;                      // tokens in flight
+    static constexpr int HOLD = LPR < 16 ? 16 / LPR : 1;  // tokens of the order a lane holds
     static __host__ __device__ int64_t slabs(int64_t cols) {
         return (cols + LPR * V - 1) / (LPR * V);
     }
@@ -378,39 +399,57 @@ __device__ __forceinline__ int32_t take(int32_t v, int from) {
     else return __shfl(v, from, LPR);
 }
 
+// The waves of the pieces come first (where few lanes share a row, they take a
+// piece's tokens in turns and add their sums), then those of the rows.
 template <typename T, typename U, int LPR>
 __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     using S = EgShape<T, LPR>;
-    constexpr int V = S::V, FLY = S::FLY;
-    const int lane = threadIdx.x & 63, l = lane % LPR;
+    constexpr int V = S::V, FLY = S::FLY, SUB = S::SUB, HOLD = S::HOLD, WINDOW = LPR * HOLD;
+    const int lane = threadIdx.x & 63, l = lane % LPR, sub = lane / LPR;
     const int64_t slabs = S::slabs(a.cols);
     const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
     const int64_t wave = block * EM_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t g = wave * S::SUB + (LPR == 64 ? 0 : lane / LPR);
-    const int64_t unit = g / slabs, slab = g % slabs;
+    const bool piece = wave < a.pieces * slabs;
+    const int64_t g = piece ? wave : (wave - a.pieces * slabs) * SUB + (SUB > 1 ? sub : 0);
+    const int64_t unit = SUB > 1 ? g : g / slabs, slab = SUB > 1 ? 0 : g % slabs;
     const Cols c = cols_of<V>((slab * LPR + l) * V, a.cols);
     const T *dy = static_cast<const T *>(a.dy);
 
-    // the tokens of the order from `held` on, LPR or up to held_end, a lane at each
-    int32_t held = 0, held_end = 0, have = 0;
-    auto hold = [&](int32_t at, int32_t end) {
+    // the tokens of the order from `held` on, WINDOW or up to held_end, some a lane
+    int32_t held = 0, held_end = 0, have[HOLD] = {};
+    auto hold = [&](int32_t at, int32_t end) __attribute__((always_inline)) {
         held = at;
-        held_end = end - at < LPR ? end : at + LPR;
-        have = 0;
-        if (at + l < end) have = a.order[at + l];
+        held_end = end - at < WINDOW ? end : at + WINDOW;
+#pragma unroll
+        for (int h = 0; h < HOLD; ++h) {
+            have[h] = 0;
+            if (at + h * LPR + l < end) have[h] = a.order[at + h * LPR + l];
+        }
+    };
+    auto token = [&](int at) __attribute__((always_inline)) {
+        int32_t v = have[0];
+#pragma unroll
+        for (int h = 1; h < HOLD; ++h) v = at / LPR == h ? have[h] : v;
+        return take<LPR>(v, at % LPR);
     };
     // s += the tokens first .. end - 1 of the order
-    auto sum = [&](int32_t first, int32_t end, float (&s)[V]) {
-        for (int32_t at = first; at < end; at += LPR) {
-            const int n = end - at < LPR ? end - at : LPR;
+    auto sum = [&](int32_t first, int32_t end, float (&s)[V]) __attribute__((always_inline)) {
+        for (int32_t at = first; at < end; at += WINDOW) {
+            const int n = end - at < WINDOW ? end - at : WINDOW;
             if (at < held || at + n > held_end) hold(at, end);
             const int skip = at - held;
             for (int j = 0; j < n; j += FLY) {
                 Raw<T, V> v[FLY];
+                // (tokens that come from another lane are all asked for first)
+                int32_t t[FLY];
+                if (SUB > 1)
+#pragma unroll
+                    for (int k = 0; k < FLY; ++k) t[k] = token(j + k < n ? skip + j + k : 0);
 #pragma unroll
                 for (int k = 0; k < FLY; ++k) {
-                    const int64_t t = take<LPR>(have, j + k < n ? skip + j + k : 0);
-                    if (j + k < n && c.any) v[k] = load_cols<T, V>(dy + t * a.ldy, c);
+                    if (SUB == 1) t[k] = token(j + k < n ? skip + j + k : 0);
+                    if (j + k < n && c.any)
+                        v[k] = load_cols<T, V>(dy + static_cast<int64_t>(t[k]) * a.ldy, c);
                 }
 #pragma unroll
                 for (int k = 0; k < FLY; ++k)
@@ -420,11 +459,9 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
             }
         }
     };
-    auto uniform = [](int32_t v) {
-        return LPR == 64 ? __builtin_amdgcn_readfirstlane(v) : v;
-    };
+    auto uniform = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
 
-    if (unit < a.pieces) {
+    if (piece) {
         // (what lies behind the last token's piece is of no meaning)
         const int32_t total = uniform(a.start[a.rows]);
         int32_t head = a.piece_row[unit];
@@ -437,21 +474,31 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
         tail = uniform(stop < total ? tail : head);
         const int32_t h0 = uniform(a.start[head]), h1 = uniform(a.start[head + 1]);
         const int32_t t0 = uniform(a.start[tail]), t1 = uniform(a.start[tail + 1]);
-        hold(begin, stop);
-        const int64_t place = (unit * 2 * slabs + slab) * (LPR * V) + l * V;
-        if (h1 - h0 > EG_PIECE) {
+        if (SUB == 1) hold(begin, stop);
+        float *place = a.part + (unit * 2 * slabs + slab) * (LPR * V) + l * V;
+#pragma unroll 1
+        for (int second = 0; second < 2; ++second) {
+            const int32_t r0 = second ? t0 : h0, r1 = second ? t1 : h1;
+            if (r1 - r0 <= EG_PIECE || (second && (tail == head || t0 >= stop))) continue;
+            const int32_t first = second ? t0 : begin, end = r1 < stop ? r1 : stop;
             float s[V] = {};
-            sum(begin, h1 < stop ? h1 : stop, s);
-            store_v<false, float, V>(a.part + place, pack<float, V>(s));
-        }
-        if (tail != head && t0 < stop && t1 - t0 > EG_PIECE) {
-            float s[V] = {};
-            sum(t0, stop, s);
-            store_v<false, float, V>(a.part + place + slabs * (LPR * V), pack<float, V>(s));
+            if constexpr (SUB == 1) {
+                sum(first, end, s);
+            } else {
+                const int32_t each = (end - first + SUB - 1) / SUB;
+                const int32_t mine = first + sub * each;
+                sum(mine, mine + each < end ? mine + each : end, s);
+#pragma unroll
+                for (int o = LPR; o < 64; o <<= 1)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[e] += __shfl_xor(s[e], o, 64);
+            }
+            if (sub == 0)
+                store_v<false, float, V>(place + second * slabs * (LPR * V), pack<float, V>(s));
         }
         return;
     }
-    const int64_t row0 = (unit - a.pieces) * S::GROUP;
+    const int64_t row0 = unit * S::GROUP;
     if (row0 >= a.rows) return;
     const int rows = static_cast<int>(a.rows - row0 < S::GROUP ? a.rows - row0 : S::GROUP);
     const int32_t starts = a.start[row0 + (l < rows ? l : rows)];
@@ -468,9 +515,14 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
 
 constexpr int EG_JOIN = 512;
 
+// Work groups of the join of each slab.
+__host__ __device__ inline int64_t join_groups(int64_t pieces) {
+    return pieces < 256 ? pieces : 256;
+}
+
 // The sums of a long row's pieces, added in their order: an eighth of them
-// by each wave, then the waves' sums.  Work group b looks at the pieces b, b + grid,
-// ..., a lane at each, for those in which a long row starts.
+// by each wave, then the waves' sums.  Work group b of a slab looks at the pieces
+// b, b + grid, ..., a lane at each, for those in which a long row starts.
 template <typename T, typename U, int LPR>
 __global__ __launch_bounds__(EG_JOIN) void k_embed_join(const EgSumArgs a) {
     using S = EgShape<T, LPR>;
@@ -481,12 +533,14 @@ __global__ __launch_bounds__(EG_JOIN) void k_embed_join(const EgSumArgs a) {
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t slabs = S::slabs(a.cols);
-    const int64_t slab = blockIdx.y;
+    const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int64_t grid = join_groups(a.pieces), slab = block % slabs;
+    if (block >= grid * slabs) return;
     const Cols c = cols_of<V>((slab * LPR + lane) * V, lane < LPR ? a.cols : 0);
-    for (int64_t p0 = blockIdx.x; p0 < a.pieces; p0 += static_cast<int64_t>(gridDim.x) * 64) {
+    for (int64_t p0 = block / slabs; p0 < a.pieces; p0 += grid * 64) {
         // the long row that starts in this lane's piece, if any: that of its
         // first token, or the one that the next piece starts with
-        const int64_t p = p0 + static_cast<int64_t>(gridDim.x) * lane;
+        const int64_t p = p0 + grid * lane;
         const int64_t total = a.start[a.rows];
         int32_t row = -1, begin = 0, stop = 0;
         if (p * EG_PIECE < total) {
@@ -610,8 +664,12 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_grad_small(const EgSmallArgs
     const T *dy = static_cast<const T *>(a.dy);
     U *grad = static_cast<U *>(a.grad);
     const int64_t slabs = (a.cols + 64 * V - 1) / (64 * V);
+    if (!a.add)
+        zero_rows(reinterpret_cast<char *>(grad + row0 * a.ldg), n_rows, a.cols, a.ldg, sizeof(U),
+                  total, wave, lane);
     // s += the tokens from .. end - 1 of the order
-    auto sum = [&](int32_t from, int32_t end, const Cols &c, float (&s)[V]) {
+    auto sum = [&](int32_t from, int32_t end, const Cols &c,
+                   float (&s)[V]) __attribute__((always_inline)) {
         for (; from < end; from += 64) {
             const int n = end - from < 64 ? end - from : 64;
             const int32_t have = order[from + (lane < n ? lane : 0)];
@@ -680,11 +738,6 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_grad_small(const EgSmallArgs
                 __syncthreads();
             }
         }
-    if (!a.add)
-        for (uint32_t r = wave; r < n_rows; r += NW)
-            if (total[r] == 0)
-                zero_row(reinterpret_cast<char *>(grad + (row0 + r) * a.ldg), a.cols, sizeof(U),
-                         lane);
 }
 
 // A grid of that many work groups, whose sides have less than 2^32 work-items;
@@ -698,8 +751,10 @@ template <typename T, typename U, int LPR>
 hipError_t embed_as(const EmArgs &a, hipStream_t s) {
     constexpr int64_t slab = LPR * 16 / sizeof(T), per = 64 / LPR * EM_WAVES;
     const int64_t n = a.T * ((a.cols + slab - 1) / slab);
-    if (n >= EW * 2048 * per)
-        k_embed<T, U, LPR, EW><<<grid_of((n + EW * per - 1) / (EW * per)), EM_BLOCK, 0, s>>>(a);
+    // (where that leaves a wave for every place on the chip)
+    if (n >= EM_SLABS * 2048 * per)
+        k_embed<T, U, LPR, EM_SLABS>
+            <<<grid_of((n + EM_SLABS * per - 1) / (EM_SLABS * per)), EM_BLOCK, 0, s>>>(a);
     else
         k_embed<T, U, LPR, 1><<<grid_of((n + per - 1) / per), EM_BLOCK, 0, s>>>(a);
     return hipGetLastError();
@@ -725,13 +780,12 @@ hipError_t sum_as(const EgSumArgs &a, bool join, hipStream_t s) {
     using S = EgShape<T, LPR>;
     const int64_t slabs = S::slabs(a.cols);
     if (join) {
-        const dim3 grid(static_cast<uint32_t>(a.pieces < 256 ? a.pieces : 256),
-                        static_cast<uint32_t>(slabs));
-        k_embed_join<T, U, LPR><<<grid, EG_JOIN, 0, s>>>(a);
+        k_embed_join<T, U, LPR>
+            <<<grid_of(join_groups(a.pieces) * slabs), EG_JOIN, 0, s>>>(a);
     } else {
-        const int64_t units = a.pieces + (a.rows + S::GROUP - 1) / S::GROUP;
-        constexpr int64_t per = S::SUB * EM_WAVES;
-        const int64_t blocks = (units * slabs + per - 1) / per;
+        const int64_t units = (a.rows + S::GROUP - 1) / S::GROUP * slabs;
+        const int64_t waves = a.pieces * slabs + (units + S::SUB - 1) / S::SUB;
+        const int64_t blocks = (waves + EM_WAVES - 1) / EM_WAVES;
         k_embed_sum<T, U, LPR><<<grid_of(blocks), EM_BLOCK, 0, s>>>(a);
     }
     return hipGetLastError();

@@ -821,7 +821,8 @@ gq_status gq_embed_grad_workspace(int64_t tokens, int64_t rows, int64_t cols, in
 
 /*
  * gq_embed_grad -- grad[v] = mul * the sum of dy[t] over the tokens t with
- * idx[t] = v, in binary32, rounded to grad's type once.
+ * idx[t] = v: binary32 sums, their product with mul rounded to binary32, then
+ * to grad's type.
  * dy          tokens x cols of dt, row stride ldy.  mul: finite.
  * skip        tokens of this index add nothing (a padding token); -1: none.
  * accumulate  0: every row of grad is written, rows without a token with 0.
