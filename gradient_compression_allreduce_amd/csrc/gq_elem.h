@@ -38,10 +38,10 @@ __device__ __forceinline__ bf16_t from_f32<bf16_t>(float v) {
     return r;
 }
 
-// V elements as they are in memory, in words.
+// V elements as they are in memory, in words (one of 16 bits in a word's lower half).
 template <typename T, int V>
 struct Raw {
-    static constexpr int W = V * static_cast<int>(sizeof(T)) / 4;
+    static constexpr int W = V * sizeof(T) < 4 ? 1 : V * static_cast<int>(sizeof(T)) / 4;
     uint32_t w[W];
 };
 
@@ -53,12 +53,19 @@ typedef unsigned int elem_u32x2 __attribute__((ext_vector_type(2)));
 typedef elem_u32x4 __attribute__((aligned(2), address_space(1))) elem_u32x4_any;
 typedef elem_u32x2 __attribute__((aligned(2), address_space(1))) elem_u32x2_any;
 
+typedef uint32_t __attribute__((address_space(1))) elem_u32;
+typedef uint16_t __attribute__((address_space(1))) elem_u16;
+
 // NT: with the non-temporal hint, for what is read or written once.
 template <bool NT, typename T, int V>
 __device__ __forceinline__ Raw<T, V> load_v(const T *p) {
     Raw<T, V> r;
-    static_assert(Raw<T, V>::W == 2 || Raw<T, V>::W % 4 == 0, "8 bytes, or a multiple of 16");
-    if constexpr (Raw<T, V>::W == 2) {
+    static_assert(V == 1 || Raw<T, V>::W == 2 || Raw<T, V>::W % 4 == 0, "1, 8 bytes, or 16 n");
+    if constexpr (V == 1 && sizeof(T) == 4) {
+        r.w[0] = *(const elem_u32 *)p;
+    } else if constexpr (V == 1) {
+        r.w[0] = *(const elem_u16 *)p;
+    } else if constexpr (Raw<T, V>::W == 2) {
         const elem_u32x2_any *q = (const elem_u32x2_any *)p;
         const elem_u32x2 v = NT ? __builtin_nontemporal_load(q) : *q;
         r.w[0] = v[0];
@@ -77,7 +84,11 @@ __device__ __forceinline__ Raw<T, V> load_v(const T *p) {
 
 template <bool NT, typename T, int V>
 __device__ __forceinline__ void store_v(T *p, const Raw<T, V> &r) {
-    if constexpr (Raw<T, V>::W == 2) {
+    if constexpr (V == 1 && sizeof(T) == 4) {
+        *(elem_u32 *)p = r.w[0];
+    } else if constexpr (V == 1) {
+        *(elem_u16 *)p = static_cast<uint16_t>(r.w[0]);
+    } else if constexpr (Raw<T, V>::W == 2) {
         elem_u32x2_any *q = (elem_u32x2_any *)p;
         const elem_u32x2 v = {r.w[0], r.w[1]};
         if (NT) __builtin_nontemporal_store(v, q);
@@ -90,30 +101,6 @@ __device__ __forceinline__ void store_v(T *p, const Raw<T, V> &r) {
             if (NT) __builtin_nontemporal_store(v, q);
             else *q = v;
         }
-    }
-}
-
-// One element.
-template <typename T>
-__device__ __forceinline__ float load_1(const T *p) {
-    if constexpr (sizeof(T) == 4) {
-        return *(const __attribute__((address_space(1))) float *)p;
-    } else {
-        const uint16_t b = *(const __attribute__((address_space(1))) uint16_t *)p;
-        T t;
-        __builtin_memcpy(&t, &b, 2);
-        return to_f32(t);
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_1(T *p, T v) {
-    if constexpr (sizeof(T) == 4) {
-        *(__attribute__((address_space(1))) float *)p = v;
-    } else {
-        uint16_t b;
-        __builtin_memcpy(&b, &v, 2);
-        *(__attribute__((address_space(1))) uint16_t *)p = b;
     }
 }
 
@@ -133,7 +120,12 @@ __device__ __forceinline__ float elem(const Raw<T, V> &r, int k) {
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> pack(const float (&f)[V]) {
     Raw<T, V> r;
-    if constexpr (sizeof(T) == 4) {
+    if constexpr (V == 1 && sizeof(T) == 2) {
+        const T a = from_f32<T>(f[0]);
+        uint16_t x;
+        __builtin_memcpy(&x, &a, 2);
+        r.w[0] = x;
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int k = 0; k < V; ++k) r.w[k] = __float_as_uint(f[k]);
     } else {
@@ -147,6 +139,18 @@ __device__ __forceinline__ Raw<T, V> pack(const float (&f)[V]) {
         }
     }
     return r;
+}
+
+// One element.
+template <typename T>
+__device__ __forceinline__ float load_1(const T *p) {
+    return elem<T, 1>(load_v<false, T, 1>(p), 0);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_1(T *p, float v) {
+    const float f[1] = {v};
+    store_v<false, T, 1>(p, pack<T, 1>(f));
 }
 
 }  // namespace

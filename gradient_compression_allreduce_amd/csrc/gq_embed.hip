@@ -19,48 +19,84 @@ __device__ __forceinline__ int64_t index_at(const void *idx, bool wide, int64_t 
     return wide ? static_cast<const int64_t *>(idx)[t] : static_cast<const int32_t *>(idx)[t];
 }
 
+// The columns of a lane: those from `lo` to `hi` of a vector of V from `col` on,
+// which lies inside the row (the others are another lane's, or none's).  A row has
+// V columns or more (V is 1 for short rows).
+struct Cols {
+    int64_t col;
+    int lo, hi;
+    bool any;
+};
+
+// Those of the vector from `at` on, which may start before or end behind the row.
+template <int V>
+__device__ __forceinline__ Cols cols_of(int64_t at, int64_t cols) {
+    Cols c;
+    c.any = at + V > 0 && at < cols;
+    c.col = at < 0 ? 0 : at + V <= cols ? at : cols - V;
+    c.lo = at < 0 ? 0 : static_cast<int>(at - c.col);
+    c.hi = at < 0 ? static_cast<int>(at + V) : V;
+    return c;
+}
+
+template <typename U, int V>
+__device__ __forceinline__ void store_cols(U *row, const Cols &c, const float (&f)[V]) {
+    if (!c.any) return;
+    if (V == 1 || (c.lo == 0 && c.hi == V)) {
+        store_v<true, U, V>(row + c.col, pack<U, V>(f));
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (k >= c.lo && k < c.hi) store_1(row + c.col + k, f[k]);
+    }
+}
+
+// Vectors of a row: 16 bytes of its wider type, or one element of few.
+template <typename T, typename U>
+constexpr int kWide = sizeof(T) == 4 || sizeof(U) == 4 ? 4 : 8;
+
 // LPR lanes of a wave share a row (64, or fewer where a row has few columns), so
 // a wave takes 64 / LPR slabs of LPR vectors at once, W times, one after another
 // in the output, and has all of their loads in flight.
-template <typename T, typename U, int LPR, int W>
+// SHIFT: the output's rows do not all start on a line of 128 bytes, and a row's
+// first slab is shortened so that the others do, as lines left to two waves cost
+// more (32527 tokens of 4100 bf16 from 60 rows into fp32: 142 us as it comes, 85
+// shifted, 80 for 4096 columns; of 4100 from 30522 rows into bf16 65 and 71).
+template <typename T, typename U, int V, int LPR, int W, bool SHIFT>
 __global__ __launch_bounds__(EM_BLOCK) void k_embed(const EmArgs a) {
-    constexpr int V = 16 / sizeof(T), SUB = 64 / LPR;
+    constexpr int SUB = 64 / LPR, LINE = 128 / sizeof(U);
     const int lane = threadIdx.x & 63;
-    const int64_t slabs = (a.cols + LPR * V - 1) / (LPR * V), n = a.T * slabs;
+    const int64_t slabs = (a.cols + (SHIFT ? LINE - 1 : 0) + LPR * V - 1) / (LPR * V);
+    const int64_t n = a.T * slabs;
     const int64_t wave = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * EM_WAVES +
                          __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t i0 = wave * (SUB * W) + (SUB > 1 ? lane / LPR : 0);
     const T *table = static_cast<const T *>(a.table);
     U *out = static_cast<U *>(a.out);
-    int64_t t[W], col[W], v[W];
+    int64_t t[W], v[W];
+    Cols c[W];
     Raw<T, V> r[W];
 #pragma unroll
     for (int k = 0; k < W; ++k) {
         const int64_t i = i0 + k * SUB < n ? i0 + k * SUB : n - 1;
         t[k] = SUB > 1 ? i : i / slabs;
-        col[k] = ((SUB > 1 ? 0 : i % slabs * LPR) + lane % LPR) * V;
+        int64_t at = ((SUB > 1 ? 0 : i % slabs * LPR) + lane % LPR) * V;
+        if (SHIFT)
+            at -= reinterpret_cast<uintptr_t>(out + t[k] * a.ldo) / sizeof(U) % LINE;
+        c[k] = cols_of<V>(at, a.cols);
         v[k] = index_at(a.idx, a.wide, t[k]);
+        if (v[k] < 0 || v[k] >= a.rows) v[k] = -1;
     }
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-        if (v[k] < 0 || v[k] >= a.rows) v[k] = -1;
-        if (v[k] >= 0 && col[k] + V <= a.cols)
-            r[k] = load_v<false, T, V>(table + v[k] * a.ld + col[k]);
-    }
+    for (int k = 0; k < W; ++k)
+        if (v[k] >= 0 && c[k].any) r[k] = load_v<false, T, V>(table + v[k] * a.ld + c[k].col);
 #pragma unroll
     for (int k = 0; k < W; ++k) {
         if (i0 + k * SUB >= n) break;
-        U *y = out + t[k] * a.ldo + col[k];
-        if (col[k] + V <= a.cols) {
-            float g[V];
+        float g[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) g[e] = v[k] >= 0 ? elem<T, V>(r[k], e) * a.mul : 0.0f;
-            store_v<true, U, V>(y, pack<U, V>(g));
-        } else {
-            const T *x = table + (v[k] >= 0 ? v[k] : 0) * a.ld + col[k];
-            for (int e = 0; e < V && col[k] + e < a.cols; ++e)
-                y[e] = from_f32<U>(v[k] >= 0 ? to_f32(x[e]) * a.mul : 0.0f);
-        }
+        for (int e = 0; e < V; ++e) g[e] = v[k] >= 0 ? elem<T, V>(r[k], e) * a.mul : 0.0f;
+        store_cols<U, V>(out + t[k] * a.ldo, c[k], g);
     }
 }
 
@@ -102,8 +138,8 @@ __device__ __forceinline__ void zero_rows(char *to, uint32_t n_rows, int64_t col
         } else {
 #pragma unroll 1
             for (; b < bytes; b += elem) {
-                if (elem == 4) store_1(reinterpret_cast<uint32_t *>(p + b), 0u);
-                else store_1(reinterpret_cast<uint16_t *>(p + b), uint16_t{0});
+                if (elem == 4) *(elem_u32 *)(p + b) = 0;
+                else *(elem_u16 *)(p + b) = 0;
             }
         }
     };
@@ -323,40 +359,11 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
 // and lies in it starts at or before the piece's first token, or else reaches
 // past its last, so a piece has at most two such rows, and two places for sums.
 
-// The columns of a lane: a vector of V from `col` on, of which the first `skip`
-// belong to the lane before (the last lane of a row whose columns are no
-// multiple of V); n > 0: a row of n < V columns.
-struct Cols {
-    int64_t col;
-    int skip, n;
-    bool any;
-};
-
-template <int V>
-__device__ __forceinline__ Cols cols_of(int64_t at, int64_t cols) {
-    Cols c;
-    c.any = at < cols;
-    c.n = cols < V ? static_cast<int>(cols) : 0;
-    c.col = c.n || at + V <= cols ? at : cols - V;
-    c.skip = static_cast<int>(at - c.col);
-    return c;
-}
-
-// (left as they are in memory, so that nothing waits for them before their use)
-template <typename T, int V>
-__device__ __forceinline__ Raw<T, V> load_cols(const T *row, const Cols &c) {
-    if (!c.n) return load_v<true, T, V>(row + c.col);
-    float v[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = k < c.n ? load_1(row + k) : 0.0f;
-    return pack<T, V>(v);
-}
-
 // What grad holds in a lane's columns, where it is added to.
 template <typename U, int V, typename Args>
 __device__ __forceinline__ Raw<U, V> old_of(const Args &a, int64_t row, const Cols &c) {
     Raw<U, V> r = {};
-    if (a.add && c.any) r = load_cols<U, V>(static_cast<const U *>(a.grad) + row * a.ldg, c);
+    if (a.add && c.any) r = load_v<true, U, V>(static_cast<const U *>(a.grad) + row * a.ldg + c.col);
     return r;
 }
 
@@ -364,25 +371,16 @@ __device__ __forceinline__ Raw<U, V> old_of(const Args &a, int64_t row, const Co
 template <typename U, int V, typename Args>
 __device__ __forceinline__ void finish(const Args &a, int64_t row, const Cols &c, float (&s)[V],
                                        const Raw<U, V> &old) {
-    if (!c.any) return;
-    U *g = static_cast<U *>(a.grad) + row * a.ldg;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         // (0 is added so that no sum of nothing becomes -0)
         s[k] = s[k] * a.mul + (a.add ? elem<U, V>(old, k) : 0.0f);
     }
-    if (!c.n && !c.skip) {
-        store_v<true, U, V>(g + c.col, pack<U, V>(s));
-    } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            if (c.n ? k < c.n : k >= c.skip) store_1(g + c.col + k, from_f32<U>(s[k]));
-    }
+    store_cols<U, V>(static_cast<U *>(a.grad) + row * a.ldg, c, s);
 }
 
-template <typename T, int LPR>
+template <int V, int LPR>
 struct EgShape {
-    static constexpr int V = 16 / sizeof(T);
     static constexpr int SUB = 64 / LPR;                // rows of a wave at once
     static constexpr int GROUP = LPR == 64 ? 4 : 1;      // rows of LPR lanes, one after another
     static constexpr int FLY = 16;                      // tokens in flight
@@ -401,10 +399,10 @@ __device__ __forceinline__ int32_t take(int32_t v, int from) {
 
 // The waves of the pieces come first (where few lanes share a row, they take a
 // piece's tokens in turns and add their sums), then those of the rows.
-template <typename T, typename U, int LPR>
+template <typename T, typename U, int V, int LPR>
 __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
-    using S = EgShape<T, LPR>;
-    constexpr int V = S::V, FLY = S::FLY, SUB = S::SUB, HOLD = S::HOLD, WINDOW = LPR * HOLD;
+    using S = EgShape<V, LPR>;
+    constexpr int FLY = S::FLY, SUB = S::SUB, HOLD = S::HOLD, WINDOW = LPR * HOLD;
     const int lane = threadIdx.x & 63, l = lane % LPR, sub = lane / LPR;
     const int64_t slabs = S::slabs(a.cols);
     const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
@@ -449,7 +447,7 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
                 for (int k = 0; k < FLY; ++k) {
                     if (SUB == 1) t[k] = token(j + k < n ? skip + j + k : 0);
                     if (j + k < n && c.any)
-                        v[k] = load_cols<T, V>(dy + static_cast<int64_t>(t[k]) * a.ldy, c);
+                        v[k] = load_v<true, T, V>(dy + static_cast<int64_t>(t[k]) * a.ldy + c.col);
                 }
 #pragma unroll
                 for (int k = 0; k < FLY; ++k)
@@ -523,12 +521,10 @@ __host__ __device__ inline int64_t join_groups(int64_t pieces) {
 // The sums of a long row's pieces, added in their order: an eighth of them
 // by each wave, then the waves' sums.  Work group b of a slab looks at the pieces
 // b, b + grid, ..., a lane at each, for those in which a long row starts.
-template <typename T, typename U, int LPR>
+template <typename U, int V, int LPR>
 __global__ __launch_bounds__(EG_JOIN) void k_embed_join(const EgSumArgs a) {
-    using S = EgShape<T, LPR>;
-    constexpr int V = S::V;
-    constexpr int FLY = 4;
-    constexpr int NW = EG_JOIN / 64;
+    using S = EgShape<V, LPR>;
+    constexpr int FLY = 4, NW = EG_JOIN / 64;
     __shared__ float sh[NW][V][64];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -610,9 +606,8 @@ __global__ __launch_bounds__(EG_JOIN) void k_embed_join(const EgSumArgs a) {
 // several slabs', and join their sums.
 constexpr int EG_ALONE = 16;
 
-template <typename T, typename U>
+template <typename T, typename U, int V>
 __global__ __launch_bounds__(EG_BLOCK) void k_embed_grad_small(const EgSmallArgs a) {
-    constexpr int V = 16 / sizeof(T);
     constexpr int FLY = 8;
     constexpr int PER = EG_SMALL / EG_BLOCK;
     constexpr int R = EG_SMALL_ROWS, NW = EG_WAVES;
@@ -679,7 +674,7 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_grad_small(const EgSmallArgs
                 for (int k = 0; k < FLY; ++k)
                     if (j + k < n) {
                         const int64_t t = __builtin_amdgcn_readlane(have, j + k);
-                        if (c.any) v[k] = load_cols<T, V>(dy + t * a.ldy, c);
+                        if (c.any) v[k] = load_v<true, T, V>(dy + t * a.ldy + c.col);
                     }
 #pragma unroll
                 for (int k = 0; k < FLY; ++k)
@@ -747,25 +742,35 @@ dim3 grid_of(int64_t blocks) {
     return dim3(static_cast<uint32_t>(x), static_cast<uint32_t>((blocks + x - 1) / x));
 }
 
-template <typename T, typename U, int LPR>
+template <typename T, typename U, int V, int LPR>
 hipError_t embed_as(const EmArgs &a, hipStream_t s) {
-    constexpr int64_t slab = LPR * 16 / sizeof(T), per = 64 / LPR * EM_WAVES;
+    constexpr int64_t slab = LPR * V, per = 64 / LPR * EM_WAVES, line = 128 / sizeof(U);
     const int64_t n = a.T * ((a.cols + slab - 1) / slab);
-    // (where that leaves a wave for every place on the chip)
-    if (n >= EM_SLABS * 2048 * per)
-        k_embed<T, U, LPR, EM_SLABS>
-            <<<grid_of((n + EM_SLABS * per - 1) / (EM_SLABS * per)), EM_BLOCK, 0, s>>>(a);
-    else
-        k_embed<T, U, LPR, 1><<<grid_of((n + per - 1) / per), EM_BLOCK, 0, s>>>(a);
+    // (slabs of several a wave where that leaves a wave for every place on the chip)
+    if (n < EM_SLABS * 2048 * per) {
+        k_embed<T, U, V, LPR, 1, false><<<grid_of((n + per - 1) / per), EM_BLOCK, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    constexpr int64_t all = EM_SLABS * per;
+    if constexpr (LPR == 64) {
+        if (reinterpret_cast<uintptr_t>(a.out) % 128 || a.ldo % line) {
+            const int64_t more = a.T * ((a.cols + line - 1 + slab - 1) / slab);
+            k_embed<T, U, V, LPR, EM_SLABS, true>
+                <<<grid_of((more + all - 1) / all), EM_BLOCK, 0, s>>>(a);
+            return hipGetLastError();
+        }
+    }
+    k_embed<T, U, V, LPR, EM_SLABS, false><<<grid_of((n + all - 1) / all), EM_BLOCK, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <typename T, typename U>
 hipError_t embed_into(const EmArgs &a, hipStream_t s) {
-    constexpr int V = 16 / sizeof(T);
-    if (a.cols <= 4 * V) return embed_as<T, U, 4>(a, s);
-    if (a.cols <= 16 * V) return embed_as<T, U, 16>(a, s);
-    return embed_as<T, U, 64>(a, s);
+    constexpr int V = kWide<T, U>;
+    if (a.cols < V) return embed_as<T, U, 1, 8>(a, s);
+    if (a.cols <= 4 * V) return embed_as<T, U, V, 4>(a, s);
+    if (a.cols <= 16 * V) return embed_as<T, U, V, 16>(a, s);
+    return embed_as<T, U, V, 64>(a, s);
 }
 
 template <typename T>
@@ -775,51 +780,55 @@ hipError_t embed_from(const EmArgs &a, gq_dtype out_dt, hipStream_t s) {
     return embed_into<T, bf16_t>(a, s);
 }
 
-template <typename T, typename U, int LPR>
-hipError_t sum_as(const EgSumArgs &a, bool join, hipStream_t s) {
-    using S = EgShape<T, LPR>;
+// Which launch of a gradient.
+enum EgPart { EG_SUM, EG_JOINED };
+
+template <typename T, typename U, int V, int LPR>
+hipError_t sum_as(const EgSumArgs &a, EgPart part, hipStream_t s) {
+    using S = EgShape<V, LPR>;
     const int64_t slabs = S::slabs(a.cols);
-    if (join) {
-        k_embed_join<T, U, LPR>
+    if (part == EG_JOINED) {
+        k_embed_join<U, V, LPR>
             <<<grid_of(join_groups(a.pieces) * slabs), EG_JOIN, 0, s>>>(a);
     } else {
         const int64_t units = (a.rows + S::GROUP - 1) / S::GROUP * slabs;
         const int64_t waves = a.pieces * slabs + (units + S::SUB - 1) / S::SUB;
         const int64_t blocks = (waves + EM_WAVES - 1) / EM_WAVES;
-        k_embed_sum<T, U, LPR><<<grid_of(blocks), EM_BLOCK, 0, s>>>(a);
+        k_embed_sum<T, U, V, LPR><<<grid_of(blocks), EM_BLOCK, 0, s>>>(a);
     }
     return hipGetLastError();
 }
 
 template <typename T, typename U>
-hipError_t sum_into(const EgSumArgs &a, bool join, hipStream_t s) {
+hipError_t grad_part(const EgSumArgs &a, EgPart part, hipStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    if (a.cols <= 4 * V) return sum_as<T, U, 4>(a, join, s);
-    if (a.cols <= 16 * V) return sum_as<T, U, 16>(a, join, s);
-    return sum_as<T, U, 64>(a, join, s);
+    if (a.cols <= 16) return sum_as<T, U, 1, 16>(a, part, s);
+    if (a.cols <= 64) return sum_as<T, U, 4, 16>(a, part, s);
+    if (a.cols <= 16 * V) return sum_as<T, U, V, 16>(a, part, s);
+    return sum_as<T, U, V, 64>(a, part, s);
 }
 
-template <typename T>
-hipError_t sum_from(const EgSumArgs &a, gq_dtype out_dt, bool join, hipStream_t s) {
-    if (out_dt == GQ_F32) return sum_into<T, float>(a, join, s);
-    if (out_dt == GQ_F16) return sum_into<T, __half>(a, join, s);
-    return sum_into<T, bf16_t>(a, join, s);
-}
-
-hipError_t sum_any(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, bool join, hipStream_t s) {
-    if (dt == GQ_F32) return sum_from<float>(a, out_dt, join, s);
-    if (dt == GQ_F16) return sum_from<__half>(a, out_dt, join, s);
-    return sum_from<bf16_t>(a, out_dt, join, s);
-}
-
-template <typename T>
-hipError_t small_from(const EgSmallArgs &a, gq_dtype out_dt, hipStream_t s) {
-    const int64_t blocks = (a.rows + a.rows_per - 1) / a.rows_per;
-    const dim3 grid = grid_of(blocks);
-    if (out_dt == GQ_F32) k_embed_grad_small<T, float><<<grid, EG_BLOCK, 0, s>>>(a);
-    else if (out_dt == GQ_F16) k_embed_grad_small<T, __half><<<grid, EG_BLOCK, 0, s>>>(a);
-    else k_embed_grad_small<T, bf16_t><<<grid, EG_BLOCK, 0, s>>>(a);
+template <typename T, typename U>
+hipError_t grad_part(const EgSmallArgs &a, EgPart, hipStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const dim3 grid = grid_of((a.rows + a.rows_per - 1) / a.rows_per);
+    if (a.cols < V) k_embed_grad_small<T, U, 1><<<grid, EG_BLOCK, 0, s>>>(a);
+    else k_embed_grad_small<T, U, V><<<grid, EG_BLOCK, 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <typename T, typename Args>
+hipError_t grad_from(const Args &a, gq_dtype out_dt, EgPart part, hipStream_t s) {
+    if (out_dt == GQ_F32) return grad_part<T, float>(a, part, s);
+    if (out_dt == GQ_F16) return grad_part<T, __half>(a, part, s);
+    return grad_part<T, bf16_t>(a, part, s);
+}
+
+template <typename Args>
+hipError_t grad_any(const Args &a, gq_dtype dt, gq_dtype out_dt, EgPart part, hipStream_t s) {
+    if (dt == GQ_F32) return grad_from<float>(a, out_dt, part, s);
+    if (dt == GQ_F16) return grad_from<__half>(a, out_dt, part, s);
+    return grad_from<bf16_t>(a, out_dt, part, s);
 }
 
 }  // namespace
@@ -832,9 +841,7 @@ hipError_t launch_embed(const EmArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream
 
 hipError_t launch_embed_grad_small(const EgSmallArgs &a, gq_dtype dt, gq_dtype out_dt,
                                    hipStream_t s) {
-    if (dt == GQ_F32) return small_from<float>(a, out_dt, s);
-    if (dt == GQ_F16) return small_from<__half>(a, out_dt, s);
-    return small_from<bf16_t>(a, out_dt, s);
+    return grad_any(a, dt, out_dt, EG_SUM, s);
 }
 
 hipError_t launch_embed_sort(const EgSortArgs &a, hipStream_t s) {
@@ -851,11 +858,11 @@ hipError_t launch_embed_sort(const EgSortArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_embed_sum(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s) {
-    return sum_any(a, dt, out_dt, false, s);
+    return grad_any(a, dt, out_dt, EG_SUM, s);
 }
 
 hipError_t launch_embed_join(const EgSumArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s) {
-    return sum_any(a, dt, out_dt, true, s);
+    return grad_any(a, dt, out_dt, EG_JOINED, s);
 }
 
 }  // namespace gq

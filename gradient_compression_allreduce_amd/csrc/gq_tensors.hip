@@ -176,7 +176,7 @@ __device__ __forceinline__ void scale_tile(const T *x, U *y, int n, float f) {
             if (s < full) store_v<true, U, V>(y + s * V, pack<U, V>(v));
         }
     }
-    if (rest < n) store_1(y + rest, from_f32<U>(last * f));
+    if (rest < n) store_1(y + rest, last * f);
 }
 
 template <typename T>

@@ -98,6 +98,26 @@ def test_lookup(gq, dt, out):
             _untouched(o, flat)
 
 
+@pytest.mark.parametrize("dt,out", [("f32", "f32"), ("f32", "bf16"), ("f16", "f16"),
+                                    ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("T,D", [(9001, 1024), (9001, 1029), (140_003, 40), (530_003, 5),
+                                 (5000, 4100), (40_000, 129)])
+def test_long_lookup(gq, dt, out, T, D):
+    """Lookups of several slabs a wave, with the output's rows on every offset
+    from a line of memory."""
+    rng = np.random.default_rng(T + D)
+    V = 97
+    table, _ = _wide(V, D, 0, dt)
+    table.copy_(torch.from_numpy(rng.standard_normal((V, D)).astype(np.float32)))
+    for gap, shift in ((0, 0), (0, 1), (3, 2), (64, 32)):
+        say("long lookup", dt, out, T, D, "gap", gap, "shift", shift)
+        idx = _idx(rng, T, V, "outside", torch.int32 if gap else torch.int64)
+        o, flat = _wide(T, D, gap, out, shift)
+        gq.gq_embed(idx, table, o, mul=0.37)
+        assert _bits(o, _lookup(idx, table, 0.37, TORCH[out])), (gap, shift)
+        _untouched(o, flat)
+
+
 def _sum64(idx, dy, V, mul, skip):
     """(the gradient, sum of magnitudes, tokens of each row) in 64 bits."""
     i = idx.long().view(-1).cpu()
@@ -136,12 +156,17 @@ def _grad(gq, idx, dy, grad, **kw):
     assert bool((ws[n:] == 0xA5).all()), "wrote past the workspace"
 
 
+# gradients of more tokens than one launch takes, of few and many columns
+LONG = [(3000, 1, 20), (20_000, 4, 9), (9000, 30_522, 24), (2049, 300, 16), (2500, 40, 17),
+        (3000, 90, 64), (3000, 90, 65), (5000, 20, 128), (5000, 2000, 129), (2100, 33, 1030)]
+
+
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("out", ["f32", "f16", "bf16", "add"])
 def test_gradient(gq, dt, out):
     rng = np.random.default_rng(2)
     add, out = out == "add", "f32" if out == "add" else out
-    for k, (T, V, D) in enumerate(SIZES + [(3000, 1, 20), (20_000, 4, 9), (9000, 30_522, 24)]):
+    for k, (T, V, D) in enumerate(SIZES + LONG):
         for j, kind in enumerate(("even", "skewed", "one", "outside")):
             it = (torch.int32, torch.int64)[(k + j) % 2]
             gap, shift, mul = (0, 1, 3)[(k + j) % 3], k % 4, (1.0, 0.37, -32.0)[k % 3]
@@ -178,7 +203,7 @@ def test_whole_numbers(gq, V):
             assert bool((grad.cpu().double() == want).all()), (V, T, kind)
 
 
-@pytest.mark.parametrize("D", [1, 31, 512, 1025])
+@pytest.mark.parametrize("D", [1, 16, 31, 64, 100, 512, 1025])
 def test_runs_of_every_length(gq, D):
     """Row r has r tokens, scattered over the batch; long and short runs
     meet at every offset."""
@@ -338,3 +363,17 @@ def test_most_rows(gq):
     at = [V - 1, 0, V // 3, V // 2 + 1, V - 2]
     assert [float(grad[i, 0]) for i in at] == [1, 2, 3, 4, 150]
     assert int((grad != 0).sum()) == 5
+
+
+def test_most_tokens(gq):
+    """More tokens than a wave's list can number: 2^26 and some, of whole
+    numbers."""
+    T, V = (1 << 26) + 5003, 70_001
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    idx = torch.randint(-1, V, (T,), dtype=torch.int32, device="cuda", generator=gen)
+    dy = torch.randint(-4, 5, (T, 1), device="cuda", generator=gen).to(torch.bfloat16)
+    grad = torch.full((V, 1), GUARD, device="cuda")
+    _grad(gq, idx, dy, grad, skip=5)
+    i = torch.where((idx >= 0) & (idx != 5), idx, torch.full_like(idx, V)).long()
+    want = torch.zeros(V + 1, dtype=torch.float64, device="cuda").index_add_(0, i, dy[:, 0].double())
+    assert bool((grad[:, 0].double() == want[:V]).all())

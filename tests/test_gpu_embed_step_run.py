@@ -1,0 +1,136 @@
+"""The calls of a training step in a row, as a program makes them: lookup,
+the table's gradient, the 4-bit exchange, the norm and the clip, and the
+orthogonalised update; eager, and captured in one graph."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+V, D, T, W = 300, 64, 2500, 2
+M = 96                      # a matrix of M x D behind the table in the flat gradient
+
+
+@pytest.fixture(scope="module")
+def gq():
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    from gradient_compression_allreduce_amd import gq as mod
+    return mod
+
+
+class Step:
+    def __init__(self, gq):
+        self.gq = gq
+        n = V * D + M * D
+        dev = dict(device="cuda")
+        self.idx = [torch.zeros(T, dtype=torch.int64, **dev) for _ in range(W)]
+        self.table = torch.zeros(V, D, **dev)
+        self.h = [torch.empty(T, D, dtype=torch.bfloat16, **dev) for _ in range(W)]
+        self.grad = [torch.zeros(n, **dev) for _ in range(W)]
+        self.ws = torch.empty(gq.gq_embed_grad_workspace(T, V, D), dtype=torch.uint8, **dev)
+        ns, nb = gq.gq_mx4_sizes(1, n)
+        self.s = [torch.empty(ns, dtype=torch.uint8, **dev) for _ in range(W)]
+        self.q = [torch.empty(nb, dtype=torch.uint8, **dev) for _ in range(W)]
+        self.total = torch.empty(n, **dev)
+        self.list = gq.gq_tensors_create([self.total[:V * D], self.total[V * D:]])
+        self.norm, self.each = torch.empty(1, **dev), torch.empty(2, **dev)
+        self.plan = gq.gq_ortho_create([(M, D)])
+        self.update = torch.empty(M * D, dtype=torch.bfloat16, **dev)
+
+    def __call__(self):
+        gq = self.gq
+        for w in range(W):
+            gq.gq_embed(self.idx[w], self.table, self.h[w], mul=8.0)
+            gq.gq_embed_grad(self.idx[w], self.h[w], self.grad[w][:V * D].view(V, D), self.ws,
+                             mul=0.5, skip=0)
+        gq.gq_mx4_quantize(self.grad, self.s, self.q)
+        gq.gq_mx4_reduce_dequant(self.q, self.s, 1, self.total.numel(), self.total)
+        gq.gq_tensors_norm(self.list, self.norm, norms=self.each, in_mul=1.0 / W)
+        gq.gq_tensors_clip(self.list, self.norm, 1.0, in_mul=1.0 / W)
+        gq.gq_ortho_step(self.plan, self.total[V * D:], self.update)
+
+    def inputs(self, k):
+        gen = torch.Generator(device="cuda").manual_seed(k)
+        for w in range(W):
+            self.idx[w].copy_(torch.randint(-2, V, (T,), device="cuda", generator=gen))
+            self.grad[w][V * D:].normal_(generator=gen)
+        self.table.normal_(generator=gen)
+
+    def check(self, gq):
+        """Each call's result from the ones before it."""
+        for w in range(W):
+            i = self.idx[w]
+            ok = i >= 0
+            x = torch.where(ok[:, None], self.table[i.clamp(min=0)] * 8.0, torch.zeros((), device="cuda"))
+            assert torch.equal(self.h[w], x.to(torch.bfloat16))
+            at = torch.where(ok & (i != 0), i, torch.full_like(i, V))
+            h = self.h[w].double()
+            g = torch.zeros(V + 1, D, dtype=torch.float64, device="cuda").index_add_(0, at, h)[:V]
+            m = torch.zeros(V + 1, D, dtype=torch.float64, device="cuda").index_add_(0, at, h.abs())[:V]
+            k = torch.bincount(at, minlength=V + 1)[:V, None].double()
+            # (a binary32 sum of k terms; halving is exact)
+            off = (self.grad[w][:V * D].view(V, D).double() - g * 0.5).abs()
+            assert bool((off <= k * 2.0 ** -24 * (1 + k * 2.0 ** -24) * m * 0.5).all())
+        values = torch.empty_like(self.total)
+        gq.gq_mx4_reduce_dequant(self.q, self.s, 1, values.numel(), values)
+        parts = (values[:V * D], values[V * D:])
+        want = [float(p.double().square().sum().sqrt()) / W for p in parts]
+        got = self.each.tolist() + [float(self.norm)]
+        for a, b in zip(got, want + [np.hypot(*want)]):
+            assert abs(a - b) <= b * (2.0 ** -24 + 2.0 ** -37)      # n 2^-52 of the sums
+        f = float(np.float32(min(1.0, 1.0 / (float(self.norm) + float(np.float32(1e-6)))) / W))
+        assert torch.equal(self.total, values * torch.tensor(f, device="cuda"))
+        again = torch.empty_like(self.update)
+        gq.gq_ortho_step(self.plan, (values * torch.tensor(f, device="cuda"))[V * D:].clone(), again)
+        assert torch.equal(self.update, again)
+
+
+def test_step(gq):
+    step = Step(gq)
+    for k in range(3):
+        step.inputs(k)
+        step()
+        torch.cuda.synchronize()
+        step.check(gq)
+
+
+def test_captured_step(gq):
+    step = Step(gq)
+    step.inputs(0)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for k in range(1, 5):
+        step.inputs(k)
+        g.replay()
+        torch.cuda.synchronize()
+        step.check(gq)          # (with eager calls of the same plan)
+
+
+def test_clip_of_int8_codes(gq):
+    """The reduced gradient's codes clipped by their scales alone: the list is
+    of the scales, the norm that of what the codes stand for."""
+    off = np.array([0, 1000, 5000, 70_000])
+    n, U = int(off[-1]), off.size - 1
+    units = gq.gq_units_create(off)
+    xs = [torch.randn(n, device="cuda") * 3 for _ in range(W)]
+    scales = [torch.empty(U, device="cuda") for _ in range(W)]
+    codes = [torch.empty(n, dtype=torch.int8, device="cuda") for _ in range(W)]
+    s_out, q_out = torch.empty(U, device="cuda"), torch.empty(n, dtype=torch.int8, device="cuda")
+    r, norm = torch.empty(n, device="cuda"), torch.empty(1, device="cuda")
+    gq.gq_quantize(xs, units, scales, codes)
+    gq.gq_reduce_requantize(codes, scales, units, s_out, q_out, r_out=r)
+    before = s_out.clone()
+    gq.gq_tensors_norm(gq.gq_tensors_create([r]), norm)
+    gq.gq_tensors_clip(gq.gq_tensors_create([s_out]), norm, 1.0)
+    torch.cuda.synchronize()
+    assert gq.gq_units_faults(units) == 0
+    f = float(np.float32(1.0 / (float(norm) + float(np.float32(1e-6)))))
+    assert f < 1 and torch.equal(s_out, before * torch.tensor(f, device="cuda"))
+    lengths = torch.from_numpy(np.diff(off)).cuda()
+    clipped = q_out.double() * torch.repeat_interleave(s_out.double(), lengths)
+    # the codes are off by at most half a scale each
+    half = 0.5 * float((before.double().square() * lengths).sum().sqrt()) * f
+    assert abs(float(clipped.norm()) - 1.0) <= half * 1.001 + 1e-5
