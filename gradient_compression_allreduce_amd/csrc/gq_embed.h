@@ -29,6 +29,7 @@ constexpr int EG_PIECE = 64;            // tokens that one wave sums
 constexpr int EG_SMALL = 2 * EG_BLOCK;
 constexpr int EG_SMALL_ROWS = 128;      // most rows of the table per work group there
 constexpr int EG_HELD = 16;             // tokens of a lane in flight
+constexpr int EG_ZERO = 8;              // rows that a wave clears
 constexpr int EG_KEYS = 256;            // the sort's row numbers come in multiples
 
 // A gradient of up to EG_SMALL tokens.
@@ -66,9 +67,11 @@ struct EgSumArgs {
     const int32_t *start, *order, *piece_row;
     float *part;                // [pieces][2][round512(cols)]
     int64_t rows, cols, ldy, ldg;
-    int64_t pieces;             // 0 where no row can be long
+    int64_t pieces;
+    int64_t zero_blocks, mixed_blocks;  // work groups that clear rows, and of all but pieces
     float mul;
     bool add;
+    bool zero;                  // rows without a token get 0
 };
 
 hipError_t launch_embed(const EmArgs &a, gq_dtype dt, gq_dtype out_dt, hipStream_t s);

@@ -125,6 +125,27 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_keys(const EgSortArgs a) {
         a.keys[i] = i < a.T ? row_of(a.idx, a.wide, a.rows, a.skip, i) : ~0u;
 }
 
+// Zeros into 16 bytes of a row of `bytes` from byte b on, or what is left of it.
+__device__ __forceinline__ void zero_slot(char *row, int64_t b, int64_t bytes, int elem) {
+    if (b + 16 <= bytes) {
+        store_v<false>(reinterpret_cast<uint32_t *>(row + b), Raw<uint32_t, 4>{});
+    } else {
+#pragma unroll 1
+        for (; b < bytes; b += elem) {
+            if (elem == 4) *(elem_u32 *)(row + b) = 0;
+            else *(elem_u16 *)(row + b) = 0;
+        }
+    }
+}
+
+// Zeros into a row, by a wave.
+__device__ __forceinline__ void zero_row(char *row, int64_t bytes, int elem, int lane) {
+    int64_t b = lane * 16;
+    for (; b + 16 <= bytes; b += 64 * 16)
+        store_v<false>(reinterpret_cast<uint32_t *>(row + b), Raw<uint32_t, 4>{});
+    zero_slot(row, b, bytes, elem);
+}
+
 // Zeros into the rows of a work group's range that have no token: n_rows rows of
 // cols elements of `elem` bytes from `to` on, ld elements apart, whose
 // tokens are counted in `total`.  A wave takes a row, or 64 lanes as many
@@ -132,32 +153,15 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_keys(const EgSortArgs a) {
 __device__ __forceinline__ void zero_rows(char *to, uint32_t n_rows, int64_t cols, int64_t ld,
                                           int elem, const int32_t *total, int wave, int lane) {
     const int64_t bytes = cols * elem;
-    auto zero = [&](char *p, int64_t b) {       // a slot
-        if (b + 16 <= bytes) {
-            store_v<false>(reinterpret_cast<uint32_t *>(p + b), Raw<uint32_t, 4>{});
-        } else {
-#pragma unroll 1
-            for (; b < bytes; b += elem) {
-                if (elem == 4) *(elem_u32 *)(p + b) = 0;
-                else *(elem_u16 *)(p + b) = 0;
-            }
-        }
-    };
     if (bytes < 64 * 16) {
         const uint32_t slots = static_cast<uint32_t>(bytes + 15) / 16;
         for (uint32_t i = wave * 64 + lane; i < n_rows * slots; i += EG_BLOCK) {
             const uint32_t r = i / slots;
-            if (total[r] == 0) zero(to + r * ld * elem, (i - r * slots) * 16);
+            if (total[r] == 0) zero_slot(to + r * ld * elem, (i - r * slots) * 16, bytes, elem);
         }
     } else {
         for (uint32_t r = wave; r < n_rows; r += EG_WAVES)
-            if (total[r] == 0) {
-                char *p = to + r * ld * elem;
-                int64_t b = lane * 16;
-                for (; b + 16 <= bytes; b += 64 * 16)
-                    store_v<false>(reinterpret_cast<uint32_t *>(p + b), Raw<uint32_t, 4>{});
-                zero(p, b);
-            }
+            if (total[r] == 0) zero_row(to + r * ld * elem, bytes, elem, lane);
     }
 }
 
@@ -405,10 +409,29 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     constexpr int FLY = S::FLY, SUB = S::SUB, HOLD = S::HOLD, WINDOW = LPR * HOLD;
     const int lane = threadIdx.x & 63, l = lane % LPR, sub = lane / LPR;
     const int64_t slabs = S::slabs(a.cols);
-    const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-    const int64_t wave = block * EM_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const bool piece = wave < a.pieces * slabs;
-    const int64_t g = piece ? wave : (wave - a.pieces * slabs) * SUB + (SUB > 1 ? sub : 0);
+    int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t first_block = (a.pieces * slabs + EM_WAVES - 1) / EM_WAVES;
+    const bool piece = block < first_block;
+    if (!piece) {
+        // every so many work groups one that clears rows
+        block -= first_block;
+        const int64_t n = a.zero_blocks * block / a.mixed_blocks;
+        if (a.zero_blocks && n != a.zero_blocks * (block + 1) / a.mixed_blocks) {
+            const int64_t row0 = (n * EM_WAVES + w) * EG_ZERO;
+            if (row0 >= a.rows) return;
+            const int rows = static_cast<int>(a.rows - row0 < EG_ZERO ? a.rows - row0 : EG_ZERO);
+            const int32_t starts = a.start[row0 + (lane < rows ? lane : rows)];
+            for (int r = 0; r < rows; ++r)
+                if (take<64>(starts, r) == take<64>(starts, r + 1))
+                    zero_row(reinterpret_cast<char *>(static_cast<U *>(a.grad) + (row0 + r) * a.ldg),
+                             a.cols * static_cast<int64_t>(sizeof(U)), sizeof(U), lane);
+            return;
+        }
+        block -= n;
+    }
+    const int64_t wave = block * EM_WAVES + w;
+    const int64_t g = piece ? wave : wave * SUB + (SUB > 1 ? sub : 0);
     const int64_t unit = SUB > 1 ? g : g / slabs, slab = SUB > 1 ? 0 : g % slabs;
     const Cols c = cols_of<V>((slab * LPR + l) * V, a.cols);
     const T *dy = static_cast<const T *>(a.dy);
@@ -460,6 +483,7 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     auto uniform = [](int32_t v) { return __builtin_amdgcn_readfirstlane(v); };
 
     if (piece) {
+        if (unit >= a.pieces) return;
         // (what lies behind the last token's piece is of no meaning)
         const int32_t total = uniform(a.start[a.rows]);
         int32_t head = a.piece_row[unit];
@@ -792,9 +816,12 @@ hipError_t sum_as(const EgSumArgs &a, EgPart part, hipStream_t s) {
             <<<grid_of(join_groups(a.pieces) * slabs), EG_JOIN, 0, s>>>(a);
     } else {
         const int64_t units = (a.rows + S::GROUP - 1) / S::GROUP * slabs;
-        const int64_t waves = a.pieces * slabs + (units + S::SUB - 1) / S::SUB;
-        const int64_t blocks = (waves + EM_WAVES - 1) / EM_WAVES;
-        k_embed_sum<T, U, V, LPR><<<grid_of(blocks), EM_BLOCK, 0, s>>>(a);
+        constexpr int64_t per = S::SUB * EM_WAVES;
+        EgSumArgs b = a;
+        b.zero_blocks = a.zero ? (a.rows + EM_WAVES * EG_ZERO - 1) / (EM_WAVES * EG_ZERO) : 0;
+        b.mixed_blocks = b.zero_blocks + (units + per - 1) / per;
+        const int64_t pieces = (a.pieces * slabs + EM_WAVES - 1) / EM_WAVES;
+        k_embed_sum<T, U, V, LPR><<<grid_of(pieces + b.mixed_blocks), EM_BLOCK, 0, s>>>(b);
     }
     return hipGetLastError();
 }

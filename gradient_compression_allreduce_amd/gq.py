@@ -1080,7 +1080,9 @@ def gq_tensors_clip(tensors, norm, max_norm, eps=1e-6, in_mul=1.0, out=None, str
 def _tokens(idx, dev):
     """(tokens, bytes of an index) of a contiguous index tensor of any shape."""
     size = _dt()["index"]
-    _need("idx", idx, 0, size, dev)
+    if not (getattr(idx, "is_cuda", False) and idx.dtype in size and idx.is_contiguous()
+            and idx.get_device() == dev):
+        raise _why("idx", idx, 0, size, dev) or ValueError("idx")
     return idx.numel(), size[idx.dtype]
 
 
