@@ -24,6 +24,7 @@ struct Span {
 struct gq_tensors {
     int device = -1;
     int64_t n = 0, count = 0, n_tiles = 0, n_longs = 0, bytes = 0;
+    int64_t data_bytes = 0;             // of the tensors
     std::vector<int64_t> numel;
     std::vector<Span> spans;            // of the tensors that are not empty, in order
     char *d_mem = nullptr;              // one allocation, parted as below
@@ -95,6 +96,7 @@ gq_status tensors_create(const char *op, void *const *x, const int64_t *numel, c
     T->count = count;
     T->n_tiles = static_cast<int64_t>(tiles.size());
     T->numel.assign(numel, numel + count);
+    for (const Span &s : spans) T->data_bytes += static_cast<int64_t>(s.end - s.begin);
     T->spans = std::move(spans);
     hipError_t e = hipGetDevice(&T->device);
     T->n_longs = static_cast<int64_t>(longs.size());
@@ -183,7 +185,7 @@ gq_status gq_tensors_norm(gq_tensors *t, float in_mul, float *norm, float *norms
     GQ_ARG(check_list(op, "the list", t));
     hipStream_t st = static_cast<hipStream_t>(stream);
     const TnNormArgs a = {t->d_tiles, t->n_tiles, t->d_parts, t->d_sums, t->d_ticket, norm, norms,
-                          in_mul};
+                          in_mul, t->data_bytes > TN_CACHED};
     hipError_t e = launch_tensors_norm(a, st);
     if (e == hipSuccess && norms && t->n_longs)
         e = launch_tensors_each({t->d_longs, t->d_sums, norms, t->n_longs, in_mul}, st);
@@ -210,8 +212,9 @@ gq_status gq_tensors_clip(const gq_tensors *t, const float *norm, float max_norm
         if (overlap(t->spans, out->spans))
             return arg_fail(GQ_ERR_INVALID, op, "out shares memory with the list");
     }
+    const int64_t bytes = t->data_bytes + (out ? out->data_bytes : 0);
     const TnClipArgs a = {t->d_tiles, out ? out->d_tiles : t->d_tiles, t->n_tiles, norm, max_norm,
-                          eps, in_mul};
+                          eps, in_mul, bytes > TN_CACHED};
     return arg_launch(op, launch_tensors_clip(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -21,6 +21,13 @@ constexpr int TN_BLOCK = 256;
 constexpr int TN_NORM_BLOCK = 512;
 constexpr int TN_MAX_GRID = 512;
 
+// Calls that touch more bytes than this go past the caches (non-temporal); those
+// below leave them in the 256 MB behind HBM for the call that follows.  Past the
+// caches / through them: clip of 64 MB of fp32 in place 24 / 21 us, norm and clip
+// of it 40 / 35; 240 MB 87 / 96 where other work came between, 129 / 108 right behind its
+// norm; norm and clip of 2 GB 1020 / 1120.
+constexpr int64_t TN_CACHED = int64_t{128} << 20;
+
 struct TnTile {
     char *p;                            // its first element
     uint32_t n_dt;                      // elements, 1 .. TN_TILE, and gq_dtype << 16
@@ -36,6 +43,7 @@ struct TnNormArgs {
     float *norm;
     float *norms;                       // NULL, or of each tensor
     float in_mul;
+    bool once;                          // past the caches
 };
 
 // A tensor of several tiles.
@@ -57,6 +65,7 @@ struct TnClipArgs {
     int64_t n_tiles;
     const float *norm;
     float max_norm, eps, in_mul;
+    bool once;                          // past the caches
 };
 
 hipError_t launch_tensors_norm(const TnNormArgs &a, hipStream_t s);

@@ -40,7 +40,7 @@ __device__ __forceinline__ TnTile tile_at(const TnTile *tiles, int64_t t) {
 // loaded whole before the first square, shorter ones in groups of TN_GROUP
 // vectors a lane (those past the end are the last one again, and are not
 // added); what is left is less than a vector, an element a lane.
-template <typename T>
+template <bool NT, typename T>
 __device__ __forceinline__ double squares(const T *p, int n) {
     constexpr int V = 16 / sizeof(T);
     constexpr int S = TN_TILE / V / 64;
@@ -57,7 +57,7 @@ __device__ __forceinline__ double squares(const T *p, int n) {
     if (n == TN_TILE) {
         Raw<T, V> r[S];
 #pragma unroll
-        for (int s = 0; s < S; ++s) r[s] = load_v<true, T, V>(p + (s * 64 + lane) * V);
+        for (int s = 0; s < S; ++s) r[s] = load_v<NT, T, V>(p + (s * 64 + lane) * V);
 #pragma unroll
         for (int s = 0; s < S; ++s) add(r[s], true);
     } else {
@@ -68,7 +68,7 @@ __device__ __forceinline__ double squares(const T *p, int n) {
 #pragma unroll
             for (int g = 0; g < TN_GROUP; ++g) {
                 const int s = at + g * 64 + lane;
-                r[g] = load_v<true, T, V>(p + (s < full ? s : full - 1) * V);
+                r[g] = load_v<NT, T, V>(p + (s < full ? s : full - 1) * V);
             }
 #pragma unroll
             for (int g = 0; g < TN_GROUP; ++g) add(r[g], at + g * 64 + lane < full);
@@ -86,7 +86,7 @@ __device__ __forceinline__ float norm_of(double sum, float in_mul) {
 // A wave takes every (waves of the grid)-th tile.  Each work group leaves one
 // sum; the last one to finish adds them in their order, so that equal calls
 // give equal bits.
-template <bool EACH>
+template <bool EACH, bool NT>
 __global__ __launch_bounds__(TN_NORM_BLOCK) void k_tensors_norm(const TnNormArgs a) {
     __shared__ double sh[TN_NWAVES];
     __shared__ uint32_t done;
@@ -97,9 +97,9 @@ __global__ __launch_bounds__(TN_NORM_BLOCK) void k_tensors_norm(const TnNormArgs
         const TnTile v = tile_at(a.tiles, t);
         const int n = v.n_dt & 0xffff, dt = v.n_dt >> 16;
         double s;
-        if (dt == GQ_F32) s = squares(reinterpret_cast<const float *>(v.p), n);
-        else if (dt == GQ_F16) s = squares(reinterpret_cast<const __half *>(v.p), n);
-        else s = squares(reinterpret_cast<const bf16_t *>(v.p), n);
+        if (dt == GQ_F32) s = squares<NT>(reinterpret_cast<const float *>(v.p), n);
+        else if (dt == GQ_F16) s = squares<NT>(reinterpret_cast<const __half *>(v.p), n);
+        else s = squares<NT>(reinterpret_cast<const bf16_t *>(v.p), n);
         if (EACH) {
             s = wave_sum(s);
             if (lane == 0) {
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(TN_BLOCK) void k_tensors_each(const TnEachArgs a) {
 }
 
 // y = x * f, x and y apart or the same memory of one type.
-template <typename T, typename U>
+template <bool NT, typename T, typename U>
 __device__ __forceinline__ void scale_tile(const T *x, U *y, int n, float f) {
     constexpr int V = sizeof(T) == 4 || sizeof(U) == 4 ? 4 : 8;
     const int lane = threadIdx.x & 63;
@@ -165,7 +165,7 @@ __device__ __forceinline__ void scale_tile(const T *x, U *y, int n, float f) {
 #pragma unroll
         for (int g = 0; g < TN_GROUP; ++g) {
             const int s = at + g * 64 + lane;
-            r[g] = load_v<true, T, V>(x + (s < full ? s : full - 1) * V);
+            r[g] = load_v<NT, T, V>(x + (s < full ? s : full - 1) * V);
         }
 #pragma unroll
         for (int g = 0; g < TN_GROUP; ++g) {
@@ -173,20 +173,21 @@ __device__ __forceinline__ void scale_tile(const T *x, U *y, int n, float f) {
             float v[V];
 #pragma unroll
             for (int k = 0; k < V; ++k) v[k] = elem<T, V>(r[g], k) * f;
-            if (s < full) store_v<true, U, V>(y + s * V, pack<U, V>(v));
+            if (s < full) store_v<NT, U, V>(y + s * V, pack<U, V>(v));
         }
     }
     if (rest < n) store_1(y + rest, last * f);
 }
 
-template <typename T>
+template <bool NT, typename T>
 __device__ __forceinline__ void scale_into(const T *x, const TnTile &y, int n, float f) {
     const int dt = y.n_dt >> 16;
-    if (dt == GQ_F32) scale_tile(x, reinterpret_cast<float *>(y.p), n, f);
-    else if (dt == GQ_F16) scale_tile(x, reinterpret_cast<__half *>(y.p), n, f);
-    else scale_tile(x, reinterpret_cast<bf16_t *>(y.p), n, f);
+    if (dt == GQ_F32) scale_tile<NT>(x, reinterpret_cast<float *>(y.p), n, f);
+    else if (dt == GQ_F16) scale_tile<NT>(x, reinterpret_cast<__half *>(y.p), n, f);
+    else scale_tile<NT>(x, reinterpret_cast<bf16_t *>(y.p), n, f);
 }
 
+template <bool NT>
 __global__ __launch_bounds__(TN_BLOCK) void k_tensors_clip(const TnClipArgs a) {
     const double top = static_cast<double>(a.norm[0]) + static_cast<double>(a.eps);
     const double c = top <= a.max_norm ? 1.0 : static_cast<double>(a.max_norm) / top;
@@ -197,9 +198,9 @@ __global__ __launch_bounds__(TN_BLOCK) void k_tensors_clip(const TnClipArgs a) {
          t += static_cast<int64_t>(gridDim.x) * TN_WAVES) {
         const TnTile v = tile_at(a.x, t), y = tile_at(a.y, t);
         const int n = v.n_dt & 0xffff, dt = v.n_dt >> 16;
-        if (dt == GQ_F32) scale_into(reinterpret_cast<const float *>(v.p), y, n, f);
-        else if (dt == GQ_F16) scale_into(reinterpret_cast<const __half *>(v.p), y, n, f);
-        else scale_into(reinterpret_cast<const bf16_t *>(v.p), y, n, f);
+        if (dt == GQ_F32) scale_into<NT>(reinterpret_cast<const float *>(v.p), y, n, f);
+        else if (dt == GQ_F16) scale_into<NT>(reinterpret_cast<const __half *>(v.p), y, n, f);
+        else scale_into<NT>(reinterpret_cast<const bf16_t *>(v.p), y, n, f);
     }
 }
 
@@ -212,8 +213,10 @@ int groups(int64_t waves, int per, int64_t most) {
 
 hipError_t launch_tensors_norm(const TnNormArgs &a, hipStream_t s) {
     const int grid = groups(a.n_tiles, TN_NWAVES, TN_MAX_GRID);
-    if (a.norms) k_tensors_norm<true><<<grid, TN_NORM_BLOCK, 0, s>>>(a);
-    else k_tensors_norm<false><<<grid, TN_NORM_BLOCK, 0, s>>>(a);
+    if (a.norms && a.once) k_tensors_norm<true, true><<<grid, TN_NORM_BLOCK, 0, s>>>(a);
+    else if (a.norms) k_tensors_norm<true, false><<<grid, TN_NORM_BLOCK, 0, s>>>(a);
+    else if (a.once) k_tensors_norm<false, true><<<grid, TN_NORM_BLOCK, 0, s>>>(a);
+    else k_tensors_norm<false, false><<<grid, TN_NORM_BLOCK, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -224,7 +227,9 @@ hipError_t launch_tensors_each(const TnEachArgs &a, hipStream_t s) {
 
 hipError_t launch_tensors_clip(const TnClipArgs &a, hipStream_t s) {
     if (a.n_tiles == 0) return hipSuccess;
-    k_tensors_clip<<<groups(a.n_tiles, TN_WAVES, 1 << 20), TN_BLOCK, 0, s>>>(a);
+    const int grid = groups(a.n_tiles, TN_WAVES, 1 << 20);
+    if (a.once) k_tensors_clip<true><<<grid, TN_BLOCK, 0, s>>>(a);
+    else k_tensors_clip<false><<<grid, TN_BLOCK, 0, s>>>(a);
     return hipGetLastError();
 }
 
