@@ -5,6 +5,11 @@
 //                 sums of the pieces of long rows;
 //   k_embed_join  the long rows from their pieces' sums;
 //   k_embed_grad_small  the whole gradient of few tokens.
+// Bound by HBM: a lookup reads each row that it meets and writes every token's,
+// a gradient reads dy and writes the table's gradient (131072 tokens of 2048 bf16 into
+// 100003 rows of fp32: 1.36 GB, 298 us, 4.6 TB/s, where a copy of 4 GiB runs at
+// 4.6).  Every sum has an order that idx alone gives; no two waves add to the same
+// place, and none waits for another.
 #include "gq_elem.h"
 #include "gq_embed.h"
 
@@ -57,7 +62,9 @@ constexpr int kWide = sizeof(T) == 4 || sizeof(U) == 4 ? 4 : 8;
 
 // LPR lanes of a wave share a row (64, or fewer where a row has few columns), so
 // a wave takes 64 / LPR slabs of LPR vectors at once, W times, one after another
-// in the output, and has all of their loads in flight.
+// in the output, and has all of their loads in flight.  65536 tokens of 4096 bf16:
+// 125 us, 512 MiB written past the caches, which keep the rows met again (one slab a
+// wave 179, two 133, eight 149, stored through the caches 145).
 // SHIFT: the output's rows do not all start on a line of 128 bytes, and a row's
 // first slab is shortened so that the others do, as lines left to two waves cost
 // more (32527 tokens of 4100 bf16 from 60 rows into fp32: 142 us as it comes, 85
@@ -110,6 +117,10 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed(const EmArgs a) {
 // as where one token makes up much of a batch, looks through its tokens again
 // instead.)  More than 16384 tokens are first turned into row numbers of 32 bits
 // (k_embed_keys), which take the fewest instructions to look through.
+// Bound by instructions: T tokens are looked at by 256 work groups, 30 us for
+// 131072 (with the tokens' places found in a second look 49), 10 for 16384; 7 to 15%
+// of a gradient of 1024 columns.  Clearing the rows without a token comes on
+// top at 5.5 to 6 TB/s.
 
 // The row of token i, or ~0 where it counts for none.
 __device__ __forceinline__ uint32_t row_of(const void *idx, bool wide, int64_t rows, int64_t skip,
@@ -311,9 +322,13 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
             kept += __popcll(own);
         }
     };
-    for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
-        if (KEYS) load(t);
-        keep(t - t0, true);
+    if constexpr (KEYS) {
+        for (int64_t t = t0; t < t1; t += 64 * EG_HELD) {
+            load(t);
+            keep(t - t0, true);
+        }
+    } else {
+        keep(0, true);
     }
     if (lane == 0) before[wave] = less;
     __syncthreads();
@@ -362,6 +377,10 @@ __global__ __launch_bounds__(EG_BLOCK) void k_embed_sort(const EgSortArgs a) {
 // piece and their sums joined by k_embed_join: a row that is longer than a piece
 // and lies in it starts at or before the piece's first token, or else reaches
 // past its last, so a piece has at most two such rows, and two places for sums.
+// 131072 tokens of 2048 bf16 into 100003 rows of fp32: 165 us, 788 MB, 4.8 TB/s (a
+// wave for each row whatever its length: 6.3 ms, for the row of the most frequent
+// token; pieces of 32 tokens 10 us more, of 128 9 more).  16384 of 1024 into 30522 rows,
+// added: 24 us, 100 MB, 4.2 TB/s, a chain of four loads.
 
 // What grad holds in a lane's columns, where it is added to.
 template <typename U, int V, typename Args>
@@ -544,7 +563,9 @@ __host__ __device__ inline int64_t join_groups(int64_t pieces) {
 
 // The sums of a long row's pieces, added in their order: an eighth of them
 // by each wave, then the waves' sums.  Work group b of a slab looks at the pieces
-// b, b + grid, ..., a lane at each, for those in which a long row starts.
+// b, b + grid, ..., a lane at each, for those in which a long row starts.  4.6 us where
+// little is to be joined (launch and a chain of three loads), 11 us for the pieces of
+// 131072 tokens of 2048.
 template <typename U, int V, int LPR>
 __global__ __launch_bounds__(EG_JOIN) void k_embed_join(const EgSumArgs a) {
     using S = EgShape<V, LPR>;
@@ -627,7 +648,8 @@ __global__ __launch_bounds__(EG_JOIN) void k_embed_join(const EgSumArgs a) {
 // One launch: a work group of a range of rows looks through all the tokens and
 // sorts those of its rows in LDS.  A wave sums a row's slab of columns; rows of more
 // than EG_ALONE tokens are summed by all waves, which share out a slab's tokens, or
-// several slabs', and join their sums.
+// several slabs', and join their sums.  512 tokens of 1024 bf16 added to 30522 rows of
+// fp32: 8.7 us of launch, indexes, sort, rows, one after another (three launches 18).
 constexpr int EG_ALONE = 16;
 
 template <typename T, typename U, int V>

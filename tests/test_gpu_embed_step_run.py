@@ -1,6 +1,9 @@
 """The calls of a training step in a row, as a program makes them: lookup,
 the table's gradient, the 4-bit exchange, the norm and the clip, and the
 orthogonalised update; eager, and captured in one graph."""
+import pathlib
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -134,3 +137,21 @@ def test_clip_of_int8_codes(gq):
     # the codes are off by at most half a scale each
     half = 0.5 * float((before.double().square() * lengths).sum().sqrt()) * f
     assert abs(float(clipped.norm()) - 1.0) <= half * 1.001 + 1e-5
+
+
+def test_readme_program(gq):
+    """The README's program of these calls: every token's row, and gradients of
+    norm 1."""
+    text = (pathlib.Path(__file__).resolve().parent.parent / "README.md").read_text()
+    programs = re.findall(r"```py\n(.*?)```", text, re.S)
+    assert len(programs) == 1
+    names = {}
+    exec(programs[0], names)
+    torch.cuda.synchronize()
+    mul = torch.tensor(names["D"] ** 0.5, device="cuda")
+    want = (names["table"][names["idx"].view(-1)] * mul).to(torch.bfloat16)
+    assert torch.equal(names["h"], want)
+    assert float(names["norm"]) > 1
+    # one rounding of each product, and 1e-6 / norm less
+    assert abs(float(names["flat"].double().norm()) - 1) <= 2.0 ** -22 + 1e-6
+    assert not bool(names["flat"][:names["D"]].any())
