@@ -351,18 +351,54 @@ def test_above_2_32_elements(gq):
     assert bool((grad[0] == 12).all()) and bool((grad[1] == 3).all())
 
 
-def test_most_rows(gq):
+@pytest.mark.parametrize("more", [150, 3000])
+def test_most_rows(gq, more):
     """The largest number of rows, with a token in the first, the last and two
-    between, and the most frequent one in three pieces."""
+    between, and `more` of one row."""
     V = 1 << 30
     grad = torch.full((V, 1), GUARD, dtype=torch.float16, device="cuda")
-    idx = torch.tensor([V - 1, 0, V // 3, V // 2 + 1, V, -1] + [V - 2] * 150, device="cuda")
+    idx = torch.tensor([V - 1, 0, V // 3, V // 2 + 1, V, -1] + [V - 2] * more, device="cuda")
     dy = torch.ones(idx.numel(), 1, dtype=torch.float16, device="cuda")
     dy[:6, 0] = torch.arange(1, 7)
+    dy[150:, 0] = 0                         # (sums up to 2048 are whole numbers of fp16)
     _grad(gq, idx, dy, grad)
     at = [V - 1, 0, V // 3, V // 2 + 1, V - 2]
-    assert [float(grad[i, 0]) for i in at] == [1, 2, 3, 4, 150]
+    assert [float(grad[i, 0]) for i in at] == [1, 2, 3, 4, 144]
     assert int((grad != 0).sum()) == 5
+
+
+@pytest.mark.parametrize("T", [3, 2049])
+def test_most_columns(gq, T):
+    """The largest number of columns: by one launch, and by pieces whose slabs
+    fill more than one side of a grid."""
+    D, V = 1 << 24, 2
+    idx = torch.zeros(T, dtype=torch.int32, device="cuda")
+    idx[1] = 1
+    dy = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    places = [0, 511, 512, D // 2 + 3, D - 1]
+    for p in places:
+        dy[:, p] = 1.0
+    grad = torch.full((V, D), GUARD, device="cuda")
+    _grad(gq, idx, dy, grad)
+    assert [float(grad[0, p]) for p in places] == [T - 1] * 5
+    assert [float(grad[1, p]) for p in places] == [1] * 5
+    assert float(grad.double().sum()) == 5 * T
+    out = torch.full((T, D), GUARD, dtype=torch.bfloat16, device="cuda") if T == 3 else dy
+    gq.gq_embed(idx, grad, out, mul=0.5)
+    assert [float(out[1, p]) for p in places] == [0.5] * 5 and float(out[1].double().sum()) == 2.5
+    assert [float(out[T - 1, p]) for p in places] == [0.5 * (T - 1)] * 5
+
+
+def test_single_vectors(gq):
+    """One token's output and gradient as vectors, the form of decoding."""
+    table = torch.randn(9, 70, device="cuda")
+    idx = torch.tensor([4], dtype=torch.int32, device="cuda")
+    o = torch.empty(70, device="cuda")
+    gq.gq_embed(idx, table, o)
+    assert torch.equal(o, table[4])
+    grad = torch.full((9, 70), GUARD, device="cuda")
+    _grad(gq, idx, o, grad)
+    assert torch.equal(grad[4], o) and int((grad != 0).any(1).sum()) == 1
 
 
 def test_most_tokens(gq):

@@ -270,3 +270,36 @@ def test_above_2_32_elements(gq):
     assert all(float(x[p]) == 1.5 for p in places)
     gq.gq_tensors_norm(t, norm)
     _near(norm[0], 1.5 * np.sqrt(len(places)), n, "norm after")
+
+
+def test_most_tensors(gq):
+    """2^20 tensors, every third one empty, through the C ABI."""
+    import ctypes
+    count = 1 << 20
+    rng = np.random.default_rng(8)
+    numel = rng.integers(1, 9, count).astype(np.int64)
+    numel[::3] = 0
+    numel[7] = 3 * TILE + 1
+    at = np.concatenate([[0], np.cumsum(numel)])
+    x = torch.randn(int(at[-1]), device="cuda")
+    ptr = (x.data_ptr() + 4 * at[:-1]).astype(np.uint64)
+    dt = np.zeros(count, np.int32)
+    h = ctypes.c_void_p()
+    assert gq.lib.gq_tensors_create(ptr.ctypes.data, numel.ctypes.data, dt.ctypes.data, count,
+                                    ctypes.byref(h)) == gq.GQ_OK, gq.gq_last_error()
+    norm, norms = torch.empty(1, device="cuda"), torch.full((count,), 7.0, device="cuda")
+    assert gq.lib.gq_tensors_norm(h, 1.0, norm.data_ptr(), norms.data_ptr(), None) == gq.GQ_OK
+    torch.cuda.synchronize()
+    _near(norm[0], _norm64([x]), x.numel(), "all")
+    sums = np.concatenate([[0.0], np.cumsum(x.double().cpu().numpy() ** 2)])
+    want = np.sqrt(np.diff(sums[at]))
+    # (the running sum's rounding, of up to its last value)
+    off = np.abs(norms.double().cpu().numpy() - want)
+    slack = sums[-1] * 2.0 ** -52 * x.numel() ** 0.5
+    assert np.all(off <= want * 2.0 ** -23 + slack / np.maximum(want, 1e-3))
+    assert bool((norms[::3] == 0).all())
+    before = x.clone()
+    assert gq.lib.gq_tensors_clip(h, norm.data_ptr(), 1.0, 0.0, 1.0, None, None) == gq.GQ_OK
+    torch.cuda.synchronize()
+    assert _bits(x, _want(before, _factor(float(norm), 1.0, 0.0, 1.0), torch.float32))
+    assert gq.lib.gq_tensors_destroy(h) == gq.GQ_OK
