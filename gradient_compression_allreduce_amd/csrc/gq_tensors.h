@@ -23,9 +23,9 @@ constexpr int TN_MAX_GRID = 512;
 
 // Calls that touch more bytes than this go past the caches (non-temporal); those
 // below leave them in the 256 MB behind HBM for the call that follows.  Past the
-// caches / through them: clip of 64 MB of fp32 in place 24 / 21 us, norm and clip
-// of it 40 / 35; 240 MB 87 / 96 where other work came between, 129 / 108 right behind its
-// norm; norm and clip of 2 GB 1020 / 1120.
+// caches / through them, fp32 in place: clip of 64 MB 22.6 / 20.5 us, of 240 MB 77 / 87
+// where other lists came between; norm and clip of one list in turn, 64 MB 37 / 36,
+// 240 MB 116 / 107, 500 MB 233 / 280, 2 GB 939 / 1060.
 constexpr int64_t TN_CACHED = int64_t{128} << 20;
 
 struct TnTile {

@@ -16,7 +16,8 @@ namespace {
 
 constexpr int TN_WAVES = TN_BLOCK / 64;
 constexpr int TN_NWAVES = TN_NORM_BLOCK / 64;
-constexpr int TN_GROUP = 8;         // vectors of a lane in flight
+constexpr int TN_GROUP = 8;         // vectors of a lane in flight in the norm
+constexpr int TN_PARTS = 4;         // parts of a tile that the clip takes one by one
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -155,25 +156,28 @@ __global__ __launch_bounds__(TN_BLOCK) void k_tensors_each(const TnEachArgs a) {
     if (lane == 0) a.norms[v.tensor] = norm_of(s, a.in_mul);
 }
 
-// y = x * f, x and y apart or the same memory of one type.  60.2M fp32 in place:
-// 87 us, 5.5 TB/s; 335M fp16 into fp32 352 us, 5.7 TB/s (mixed reads and writes, of
-// which a plain copy moves 4.6 to 5.4).
+// y = x * f, x and y apart or the same memory of one type.  A wave takes a quarter
+// of a tile, all of its loads in flight: with as many writes as reads HBM is fastest
+// with little of each at once.  60.2M fp32 in place: 77 us, 6.3 TB/s (whole tiles 87,
+// halves 79, eighths 75, but 10000 tensors of up to 4096 then 31 instead of 27);
+// 335M fp16 into fp32 343 us, 5.9 TB/s; 400M bf16 in place 255 (halves 266).
 template <bool NT, typename T, typename U>
-__device__ __forceinline__ void scale_tile(const T *x, U *y, int n, float f) {
+__device__ __forceinline__ void scale_part(const T *x, U *y, int n, float f) {
     constexpr int V = sizeof(T) == 4 || sizeof(U) == 4 ? 4 : 8;
+    constexpr int G = TN_TILE / TN_PARTS / V / 64;      // vectors of a lane in flight
     const int lane = threadIdx.x & 63;
     const int full = n / V, rest = full * V + lane;
     const float last = rest < n ? load_1(x + rest) : 0.0f;
-    for (int at = 0; at < full; at += TN_GROUP * 64) {
-        Raw<T, V> r[TN_GROUP];
+    if (full > 0) {
+        Raw<T, V> r[G];
 #pragma unroll
-        for (int g = 0; g < TN_GROUP; ++g) {
-            const int s = at + g * 64 + lane;
+        for (int g = 0; g < G; ++g) {       // (past the end the last one again)
+            const int s = g * 64 + lane;
             r[g] = load_v<NT, T, V>(x + (s < full ? s : full - 1) * V);
         }
 #pragma unroll
-        for (int g = 0; g < TN_GROUP; ++g) {
-            const int s = at + g * 64 + lane;
+        for (int g = 0; g < G; ++g) {
+            const int s = g * 64 + lane;
             float v[V];
 #pragma unroll
             for (int k = 0; k < V; ++k) v[k] = elem<T, V>(r[g], k) * f;
@@ -184,11 +188,11 @@ __device__ __forceinline__ void scale_tile(const T *x, U *y, int n, float f) {
 }
 
 template <bool NT, typename T>
-__device__ __forceinline__ void scale_into(const T *x, const TnTile &y, int n, float f) {
+__device__ __forceinline__ void scale_into(const T *x, const TnTile &y, int at, int n, float f) {
     const int dt = y.n_dt >> 16;
-    if (dt == GQ_F32) scale_tile<NT>(x, reinterpret_cast<float *>(y.p), n, f);
-    else if (dt == GQ_F16) scale_tile<NT>(x, reinterpret_cast<__half *>(y.p), n, f);
-    else scale_tile<NT>(x, reinterpret_cast<bf16_t *>(y.p), n, f);
+    if (dt == GQ_F32) scale_part<NT>(x, reinterpret_cast<float *>(y.p) + at, n, f);
+    else if (dt == GQ_F16) scale_part<NT>(x, reinterpret_cast<__half *>(y.p) + at, n, f);
+    else scale_part<NT>(x, reinterpret_cast<bf16_t *>(y.p) + at, n, f);
 }
 
 template <bool NT>
@@ -198,13 +202,16 @@ __global__ __launch_bounds__(TN_BLOCK) void k_tensors_clip(const TnClipArgs a) {
     const float f = static_cast<float>(c * static_cast<double>(a.in_mul));
     if (f == 1.0f && a.x == a.y) return;
     const int wave = threadIdx.x >> 6;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * TN_WAVES + wave; t < a.n_tiles;
+    constexpr int PART = TN_TILE / TN_PARTS;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * TN_WAVES + wave; t < a.n_tiles * TN_PARTS;
          t += static_cast<int64_t>(gridDim.x) * TN_WAVES) {
-        const TnTile v = tile_at(a.x, t), y = tile_at(a.y, t);
-        const int n = v.n_dt & 0xffff, dt = v.n_dt >> 16;
-        if (dt == GQ_F32) scale_into<NT>(reinterpret_cast<const float *>(v.p), y, n, f);
-        else if (dt == GQ_F16) scale_into<NT>(reinterpret_cast<const __half *>(v.p), y, n, f);
-        else scale_into<NT>(reinterpret_cast<const bf16_t *>(v.p), y, n, f);
+        const TnTile v = tile_at(a.x, t / TN_PARTS), y = tile_at(a.y, t / TN_PARTS);
+        const int at = static_cast<int>(t % TN_PARTS) * PART, dt = v.n_dt >> 16;
+        const int left = static_cast<int>(v.n_dt & 0xffff) - at, n = left < PART ? left : PART;
+        if (n <= 0) continue;
+        if (dt == GQ_F32) scale_into<NT>(reinterpret_cast<const float *>(v.p) + at, y, at, n, f);
+        else if (dt == GQ_F16) scale_into<NT>(reinterpret_cast<const __half *>(v.p) + at, y, at, n, f);
+        else scale_into<NT>(reinterpret_cast<const bf16_t *>(v.p) + at, y, at, n, f);
     }
 }
 
@@ -231,7 +238,7 @@ hipError_t launch_tensors_each(const TnEachArgs &a, hipStream_t s) {
 
 hipError_t launch_tensors_clip(const TnClipArgs &a, hipStream_t s) {
     if (a.n_tiles == 0) return hipSuccess;
-    const int grid = groups(a.n_tiles, TN_WAVES, 1 << 20);
+    const int grid = groups(a.n_tiles * TN_PARTS, TN_WAVES, 1 << 20);
     if (a.once) k_tensors_clip<true><<<grid, TN_BLOCK, 0, s>>>(a);
     else k_tensors_clip<false><<<grid, TN_BLOCK, 0, s>>>(a);
     return hipGetLastError();
