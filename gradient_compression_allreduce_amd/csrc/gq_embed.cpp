@@ -49,6 +49,16 @@ gq_status check_mul(const char *op, float mul) {
 
 int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
+// Whether one launch takes the gradient, in which the work group that has the most
+// frequent token's row sums that row alone: up to EG_SMALL tokens, and 2^21 elements of dy,
+// or 2^22 where the table is long and the tokens more evenly spread.  One launch / three,
+// bf16 added to fp32: 512 tokens of 8192 into 30522 rows 25 / 51 us, 2000 of 2048
+// 25 / 28, 1000 of 2048 into 200 20 / 23, 256 of 8192 into 100 24 / 19, 1697 of 2993 into
+// 173 58 / 27.
+bool is_small(int64_t tokens, int64_t rows, int64_t cols) {
+    return tokens <= EG_SMALL && tokens * cols <= (rows >= 8192 ? 1 << 22 : 1 << 21);
+}
+
 // The parts of a gradient's workspace, and its bytes (at least 16).
 struct Workspace {
     int64_t order = 0, piece_row = 0, keys = 0, part = 0, bytes = 16;
@@ -57,7 +67,7 @@ struct Workspace {
 
 Workspace grad_workspace(int64_t tokens, int64_t rows, int64_t cols) {
     Workspace w;
-    if (tokens <= EG_SMALL) return w;
+    if (is_small(tokens, rows, cols)) return w;
     w.pieces = (tokens + EG_PIECE - 1) / EG_PIECE;
     w.order = round16(4 * (rows + 1));
     w.piece_row = w.order + round16(4 * tokens);
@@ -120,7 +130,7 @@ gq_status gq_embed_grad(const void *idx, int32_t idx_bytes, int64_t tokens, cons
     if (!tokens && accumulate) return arg_ok();
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool wide = idx_bytes == 8, add = accumulate != 0;
-    if (tokens <= EG_SMALL) {
+    if (is_small(tokens, rows, cols)) {
         // two work groups per compute unit
         const int64_t per = std::min<int64_t>(EG_SMALL_ROWS, (rows + 511) / 512);
         const EgSmallArgs a = {idx, dy,  grad, tokens, rows, cols, ldy, ldg, skip,

@@ -158,7 +158,8 @@ def _grad(gq, idx, dy, grad, **kw):
 
 # gradients of more tokens than one launch takes, of few and many columns
 LONG = [(3000, 1, 20), (20_000, 4, 9), (9000, 30_522, 24), (2049, 300, 16), (2500, 40, 17),
-        (3000, 90, 64), (3000, 90, 65), (5000, 20, 128), (5000, 2000, 129), (2100, 33, 1030)]
+        (3000, 90, 64), (3000, 90, 65), (5000, 20, 128), (5000, 2000, 129), (2100, 33, 1030),
+        (1200, 90, 2000), (40, 12, 60_000)]
 
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
@@ -369,8 +370,8 @@ def test_most_rows(gq, more):
 
 @pytest.mark.parametrize("T", [3, 2049])
 def test_most_columns(gq, T):
-    """The largest number of columns: by one launch, and by pieces whose slabs
-    fill more than one side of a grid."""
+    """The largest number of columns, of few tokens and of pieces whose slabs fill
+    more than one side of a grid."""
     D, V = 1 << 24, 2
     idx = torch.zeros(T, dtype=torch.int32, device="cuda")
     idx[1] = 1
