@@ -124,6 +124,7 @@ gq_status tensors_create(const char *op, void *const *x, const int64_t *numel, c
     if (e != hipSuccess) {
         const long long size = T->bytes;
         if (T->d_mem) (void)hipFree(T->d_mem);
+        (void)hipGetLastError();        // (or the thread's next launch would report it)
         return arg_fail(GQ_ERR_HIP, op, "making a list of %lld bytes failed: %s", size,
                         hipGetErrorString(e));
     }

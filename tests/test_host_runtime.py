@@ -1,0 +1,72 @@
+"""The library's C-ABI files on a HIP runtime of the host
+(tests/host_runtime/runtime.cpp), in which a chosen call fails: what a failed
+allocation or copy leaves behind, and refusals that need a live handle."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+from gradient_compression_allreduce_amd.build import CSRC
+from tests.conftest import ROOT
+
+GQ_OK, GQ_ERR_INVALID, GQ_ERR_HIP = 0, 1, 4
+GOOD = 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("g++ is not available")
+    out = str(tmp_path_factory.mktemp("host") / "libhost.so")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    subprocess.run(
+        [cxx, "-std=c++17", "-O1", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-D__HIP_PLATFORM_AMD__",
+         "-I", os.path.join(rocm, "include"), "-o", out,
+         os.path.join(ROOT, "tests", "host_runtime", "runtime.cpp"),
+         os.path.join(CSRC, "gq_abi.cpp"), os.path.join(CSRC, "gq_tensors.cpp")],
+        check=True, capture_output=True, text=True, timeout=300)
+    # (launchers that no test reaches are looked for when they are called)
+    L = ctypes.CDLL(out, mode=os.RTLD_LAZY)
+    vp, f32, i64 = ctypes.c_void_p, ctypes.c_float, ctypes.c_int64
+    L.gq_last_error.restype = ctypes.c_char_p
+    L.gq_tensors_create.argtypes = [vp, vp, vp, i64, vp]
+    L.gq_tensors_destroy.argtypes = [vp]
+    L.gq_tensors_info.argtypes = [vp, vp, vp, vp]
+    L.gq_tensors_norm.argtypes = [vp, f32, vp, vp, vp]
+    L.gq_tensors_clip.argtypes = [vp, vp, f32, f32, f32, vp, vp]
+    return L
+
+
+def _list(lib, at, numel, dt=None):
+    """(status, handle) of a list of tensors at these addresses."""
+    x, n = np.array(at, np.uint64), np.array(numel, np.int64)
+    t = np.array(dt if dt is not None else [0] * len(at), np.int32)
+    h = ctypes.c_void_p()
+    st = lib.gq_tensors_create(x.ctypes.data, n.ctypes.data, t.ctypes.data, len(at), ctypes.byref(h))
+    return st, h
+
+
+def test_failed_list_leaves_no_error(lib):
+    """Whichever runtime call of gq_tensors_create fails: no memory stays
+    allocated, and no error is left for the thread's next call to report."""
+    at, numel = [GOOD, GOOD + (1 << 20)], [100, 5000]
+    st, good = _list(lib, at, numel)
+    assert st == GQ_OK
+    live, before = lib.host_live(), lib.host_calls()
+    st, h = _list(lib, at, numel)
+    n_calls = lib.host_calls() - before
+    assert st == GQ_OK and lib.gq_tensors_destroy(h) == GQ_OK and n_calls >= 6
+    for k in range(1, n_calls + 1):
+        lib.host_fail_in(k)
+        st, h = _list(lib, at, numel)
+        assert st == GQ_ERR_HIP and not h.value, k
+        assert b"out of memory" in lib.gq_last_error(), k
+        assert lib.host_live() == live, k
+        assert lib.hipPeekAtLastError() == 0, k
+        assert lib.gq_tensors_norm(good, 1.0, 1 << 30, None, None) == GQ_OK, k
+    lib.host_fail_in(0)
+    assert lib.gq_tensors_destroy(good) == GQ_OK
