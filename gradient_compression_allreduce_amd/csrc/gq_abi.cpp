@@ -28,6 +28,12 @@ gq_status fail(gq_status code, const char *op, const char *fmt, ...) {
     return code;
 }
 
+// A failed create: no error stays on the thread for its next launch to report.
+gq_status create_fail(const char *op, const char *what, hipError_t e) {
+    (void)hipGetLastError();
+    return fail(GQ_ERR_HIP, op, "%s failed: %s", what, hipGetErrorString(e));
+}
+
 gq_status ok() {
     g_last_error.clear();
     return GQ_OK;
@@ -357,14 +363,15 @@ gq_status gq_units_create(const int64_t *h_off, int64_t n_units, gq_units **out)
 
     gq_units *U = new (std::nothrow) gq_units;
     if (!U) return fail(GQ_ERR_INVALID, op, "out of host memory");
-    if (hipGetDevice(&U->device) != hipSuccess) {
+    hipError_t e = hipGetDevice(&U->device);
+    if (e != hipSuccess) {
         delete U;
-        return fail(GQ_ERR_HIP, op, "hipGetDevice failed");
+        return create_fail(op, "hipGetDevice", e);
     }
     U->n = n;
     U->n_units = n_units;
     std::vector<int64_t> off(h_off, h_off + n_units + 1);
-    hipError_t e = hipMalloc(reinterpret_cast<void **>(&U->d_faults), sizeof(uint32_t));
+    e = hipMalloc(reinterpret_cast<void **>(&U->d_faults), sizeof(uint32_t));
     if (e == hipSuccess) e = hipMemset(U->d_faults, 0, sizeof(uint32_t));
     for (int ti = 0; ti < gq::TAB_COUNT && e == hipSuccess; ++ti) {
         const int V = gq::kSlotElems[ti];
@@ -498,7 +505,7 @@ gq_status gq_units_create(const int64_t *h_off, int64_t n_units, gq_units **out)
     }
     if (e != hipSuccess) {
         (void)gq_units_destroy(U);
-        return fail(GQ_ERR_HIP, op, "device allocation failed: %s", hipGetErrorString(e));
+        return create_fail(op, "device allocation", e);
     }
     for (int ti = 0; ti < gq::TAB_COUNT; ++ti) {
         if (!gq::table_ready(U->tab[ti], n_units)) {
@@ -506,9 +513,10 @@ gq_status gq_units_create(const int64_t *h_off, int64_t n_units, gq_units **out)
             return fail(GQ_ERR_HIP, op, "internal error: work table %d incomplete", ti);
         }
     }
-    if (hipDeviceSynchronize() != hipSuccess) {
+    e = hipDeviceSynchronize();
+    if (e != hipSuccess) {
         (void)gq_units_destroy(U);
-        return fail(GQ_ERR_HIP, op, "synchronize failed");
+        return create_fail(op, "synchronize", e);
     }
     *out = U;
     return ok();
@@ -817,9 +825,10 @@ gq_status gq_pipe_create(const int64_t *h_off, int64_t n_units, const int64_t *b
                         (long long)b);
     gq_pipe *P = new (std::nothrow) gq_pipe;
     if (!P) return fail(GQ_ERR_INVALID, op, "out of host memory");
-    if (hipGetDevice(&P->device) != hipSuccess) {
+    hipError_t e = hipGetDevice(&P->device);
+    if (e != hipSuccess) {
         delete P;
-        return fail(GQ_ERR_HIP, op, "hipGetDevice failed");
+        return create_fail(op, "hipGetDevice", e);
     }
     P->n = h_off[n_units];
     P->n_units = n_units;
@@ -842,7 +851,7 @@ gq_status gq_pipe_create(const int64_t *h_off, int64_t n_units, const int64_t *b
         P->slot_elems = std::max(P->slot_elems, h_off[ub] - base);
         P->slot_units = std::max(P->slot_units, ub - ua);
     }
-    hipError_t e = hipStreamCreateWithFlags(&P->aux, hipStreamNonBlocking);
+    e = hipStreamCreateWithFlags(&P->aux, hipStreamNonBlocking);
     for (int k = 0; k < 2 && e == hipSuccess; ++k) {
         e = hipEventCreateWithFlags(&P->ev_q[k], hipEventDisableTiming);
         if (e == hipSuccess) e = hipEventCreateWithFlags(&P->ev_r[k], hipEventDisableTiming);
@@ -850,7 +859,7 @@ gq_status gq_pipe_create(const int64_t *h_off, int64_t n_units, const int64_t *b
     if (e == hipSuccess) e = hipEventCreateWithFlags(&P->ev_done, hipEventDisableTiming);
     if (e != hipSuccess) {
         (void)gq_pipe_destroy(P);
-        return fail(GQ_ERR_HIP, op, "stream or event creation failed: %s", hipGetErrorString(e));
+        return create_fail(op, "stream or event creation", e);
     }
     *out = P;
     return ok();

@@ -70,6 +70,14 @@ hipError_t hipMemset(void *p, int v, size_t n) {
     return e;
 }
 hipError_t hipDeviceSynchronize() { return call(); }
+hipError_t hipStreamCreateWithFlags(hipStream_t *s, unsigned) {
+    return hipMalloc(reinterpret_cast<void **>(s), 1);
+}
+hipError_t hipStreamDestroy(hipStream_t s) { return hipFree(s); }
+hipError_t hipEventCreateWithFlags(hipEvent_t *e, unsigned) {
+    return hipMalloc(reinterpret_cast<void **>(e), 1);
+}
+hipError_t hipEventDestroy(hipEvent_t e) { return hipFree(e); }
 
 }  // extern "C"
 

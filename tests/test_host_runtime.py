@@ -33,6 +33,10 @@ def lib(tmp_path_factory):
     L = ctypes.CDLL(out, mode=os.RTLD_LAZY)
     vp, f32, i64 = ctypes.c_void_p, ctypes.c_float, ctypes.c_int64
     L.gq_last_error.restype = ctypes.c_char_p
+    L.gq_units_create.argtypes = [vp, i64, vp]
+    L.gq_units_destroy.argtypes = [vp]
+    L.gq_pipe_create.argtypes = [vp, i64, vp, i64, ctypes.c_int32, vp]
+    L.gq_pipe_destroy.argtypes = [vp]
     L.gq_tensors_create.argtypes = [vp, vp, vp, i64, vp]
     L.gq_tensors_destroy.argtypes = [vp]
     L.gq_tensors_info.argtypes = [vp, vp, vp, vp]
@@ -70,3 +74,33 @@ def test_failed_list_leaves_no_error(lib):
         assert lib.gq_tensors_norm(good, 1.0, 1 << 30, None, None) == GQ_OK, k
     lib.host_fail_in(0)
     assert lib.gq_tensors_destroy(good) == GQ_OK
+
+
+def _units(lib):
+    off = np.array([0, 5, 70_000, 70_001, 400_000], np.int64)
+    h = ctypes.c_void_p()
+    return lib.gq_units_create(off.ctypes.data, 4, ctypes.byref(h)), h
+
+
+def _pipe(lib):
+    off = np.array([0, 5, 70_000, 70_001, 400_000], np.int64)
+    buckets = np.array([0, 2, 4], np.int64)
+    h = ctypes.c_void_p()
+    return lib.gq_pipe_create(off.ctypes.data, 4, buckets.ctypes.data, 2, 0, ctypes.byref(h)), h
+
+
+@pytest.mark.parametrize("make,destroy", [(_units, "gq_units_destroy"), (_pipe, "gq_pipe_destroy")])
+def test_failed_tables_leave_no_error(lib, make, destroy):
+    """The same of gq_units_create and gq_pipe_create."""
+    live, before = lib.host_live(), lib.host_calls()
+    st, h = make(lib)
+    n_calls = lib.host_calls() - before
+    assert st == GQ_OK and getattr(lib, destroy)(h) == GQ_OK
+    assert lib.host_live() == live and n_calls > 10
+    for k in range(1, n_calls + 1):
+        lib.host_fail_in(k)
+        st, h = make(lib)
+        assert st == GQ_ERR_HIP and not h.value, k
+        assert lib.host_live() == live, k
+        assert lib.hipPeekAtLastError() == 0, k
+    lib.host_fail_in(0)
