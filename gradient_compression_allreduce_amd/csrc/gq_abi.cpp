@@ -842,8 +842,10 @@ gq_status gq_pipe_create(const int64_t *h_off, int64_t n_units, const int64_t *b
         gq_units *t = nullptr;
         const gq_status st = gq_units_create(local.data(), ub - ua, &t);
         if (st != GQ_OK) {
+            const std::string why = g_last_error;   // (gq_pipe_destroy clears it)
             (void)gq_pipe_destroy(P);
-            return st;  // gq_units_create set the error text
+            g_last_error = why;
+            return st;
         }
         P->tab.push_back(t);
         P->base.push_back(base);

@@ -104,3 +104,16 @@ def test_failed_tables_leave_no_error(lib, make, destroy):
         assert lib.host_live() == live, k
         assert lib.hipPeekAtLastError() == 0, k
     lib.host_fail_in(0)
+
+
+def test_failed_pipe_keeps_its_error_text(lib):
+    """A bucket's table that cannot be made: gq_pipe_create tells why."""
+    before = lib.host_calls()
+    st, h = _pipe(lib)
+    n_calls = lib.host_calls() - before
+    assert st == GQ_OK and lib.gq_pipe_destroy(h) == GQ_OK
+    for k in range(1, n_calls + 1):
+        lib.host_fail_in(k)
+        st, h = _pipe(lib)
+        assert st == GQ_ERR_HIP and b"out of memory" in lib.gq_last_error(), (k, lib.gq_last_error())
+    lib.host_fail_in(0)
