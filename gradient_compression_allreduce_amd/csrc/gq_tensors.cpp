@@ -55,6 +55,15 @@ bool overlap(const std::vector<Span> &a, const std::vector<Span> &b) {
     return false;
 }
 
+// Whether `bytes` bytes from p on share memory with a tensor of a list.
+bool touches(const std::vector<Span> &spans, const void *p, int64_t bytes) {
+    const Span at = {reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes};
+    // the first tensor that ends behind p (they lie in order and apart)
+    const auto first = std::partition_point(spans.begin(), spans.end(),
+                                            [&](const Span &s) { return s.end <= at.begin; });
+    return first != spans.end() && first->begin < at.end;
+}
+
 gq_status tensors_create(const char *op, void *const *x, const int64_t *numel, const gq_dtype *dt,
                          int64_t count, gq_tensors **out) {
     std::vector<Span> spans;
@@ -184,6 +193,11 @@ gq_status gq_tensors_norm(gq_tensors *t, float in_mul, float *norm, float *norms
     GQ_ARG(arg_ptr(op, "norm", norm, 4));
     if (norms) GQ_ARG(arg_ptr(op, "norms", norms, 4));
     GQ_ARG(check_list(op, "the list", t));
+    const int64_t norms_bytes = norms ? 4 * t->count : 0;
+    if (touches(t->spans, norm, 4) || touches(t->spans, norms, norms_bytes))
+        return arg_fail(GQ_ERR_INVALID, op, "norm or norms lies in a tensor of the list");
+    if (norm >= norms && norm < norms + norms_bytes / 4)
+        return arg_fail(GQ_ERR_INVALID, op, "norm is one of norms");
     hipStream_t st = static_cast<hipStream_t>(stream);
     const TnNormArgs a = {t->d_tiles, t->n_tiles, t->d_parts, t->d_sums, t->d_ticket, norm, norms,
                           in_mul, t->data_bytes > TN_CACHED};
@@ -213,6 +227,9 @@ gq_status gq_tensors_clip(const gq_tensors *t, const float *norm, float max_norm
         if (overlap(t->spans, out->spans))
             return arg_fail(GQ_ERR_INVALID, op, "out shares memory with the list");
     }
+    // (one wave would write it while others read it)
+    if (touches((out ? out : t)->spans, norm, 4))
+        return arg_fail(GQ_ERR_INVALID, op, "norm lies in a tensor that the call writes");
     const int64_t bytes = t->data_bytes + (out ? out->data_bytes : 0);
     const TnClipArgs a = {t->d_tiles, out ? out->d_tiles : t->d_tiles, t->n_tiles, norm, max_norm,
                           eps, in_mul, bytes > TN_CACHED};

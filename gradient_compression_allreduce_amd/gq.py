@@ -1054,7 +1054,8 @@ def _list(name, t):
 
 def gq_tensors_norm(tensors, norm, norms=None, in_mul=1.0, stream=None):
     """norm (fp32, one element) = in_mul * the 2-norm of all tensors of the
-    list together; norms (fp32, one per tensor): also that of each."""
+    list together; norms (fp32, one per tensor): also that of each.  Neither
+    may lie in a tensor of the list, nor norm in norms."""
     _list("tensors", tensors)
     dev = _current_device()
     f32 = _dt()["f32"]
@@ -1069,7 +1070,8 @@ def gq_tensors_norm(tensors, norm, norms=None, in_mul=1.0, stream=None):
 def gq_tensors_clip(tensors, norm, max_norm, eps=1e-6, in_mul=1.0, out=None, stream=None):
     """Every tensor times in_mul * min(1, max_norm / (norm + eps)), norm being
     the fp32 norm of in_mul times the list: in place, or into the list out of
-    tensors of the same lengths and any types."""
+    tensors of the same lengths and any types.  norm may not lie in a tensor
+    that is written."""
     _list("tensors", tensors)
     _need("norm", norm, 1, _dt()["f32"], _current_device())
     op = _list("out", out).handle if out is not None else None

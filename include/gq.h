@@ -769,7 +769,8 @@ gq_status gq_tensors_info(const gq_tensors *t, int64_t *n, int64_t *count, int64
  * NaN; a list without elements, and a tensor without, gives 0.
  * in_mul  as for gq_quantize, e.g. 2^-16 for loss-scaled gradients.
  * norm    device pointer, 1 fp32.  norms: NULL, or a device array of count
- *         fp32.  Neither may lie in a tensor of the list.
+ *         fp32.  Neither may lie in a tensor of the list, nor norm in norms
+ *         (GQ_ERR_INVALID).
  * The list holds the call's scratch memory: norms of one list must be ordered,
  * captured ones included.  Equal calls give equal bits.
  * Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_DEVICE, GQ_ERR_HIP.
@@ -784,6 +785,7 @@ gq_status gq_tensors_norm(gq_tensors *t, float in_mul, float *norm, float *norms
  * and the product rounded to binary32, then to y's type.  A NaN norm gives NaN
  * everywhere; an infinite one 0, and NaN for elements that are infinite.
  * norm      device pointer, 1 fp32: of in_mul * x, as gq_tensors_norm writes it.
+ *           It may not lie in a tensor that the call writes (GQ_ERR_INVALID).
  * max_norm  >= 0 (inf: c is 1 unless the norm is NaN).  eps: finite, >= 0.
  * out       NULL: in place, and where f is 1 nothing is written.  Otherwise a
  *           list of tensors of the same lengths, of any types, that share no

@@ -303,3 +303,37 @@ def test_most_tensors(gq):
     torch.cuda.synchronize()
     assert _bits(x, _want(before, _factor(float(norm), 1.0, 0.0, 1.0), torch.float32))
     assert gq.lib.gq_tensors_destroy(h) == gq.GQ_OK
+
+
+def test_norm_inside_a_list(gq):
+    """A norm in a tensor that the call writes, or that its norm is taken of, is
+    refused before anything runs; one between the tensors, or in a list that
+    is only read, is not."""
+    flat = torch.arange(1, 20_001, dtype=torch.float32, device="cuda")
+    before = flat.clone()
+    t = gq.gq_tensors_create([flat[4:9000], flat[9004:19_000]])
+    two = torch.empty(2, device="cuda")
+    for p in (flat[4:5], flat[8999:9000], flat[9004:9005], flat[18_999:19_000]):
+        for call in (lambda: gq.gq_tensors_norm(t, p), lambda: gq.gq_tensors_clip(t, p, 1.0)):
+            with pytest.raises(gq.GQError, match="lies in a tensor"):
+                call()
+    for p in (flat[3:5], flat[9003:9005], flat[18_999:19_001]):
+        with pytest.raises(gq.GQError, match="lies in a tensor"):
+            gq.gq_tensors_norm(t, two, norms=p)
+    for p in (two[:1], two[1:]):
+        with pytest.raises(gq.GQError, match="one of norms"):
+            gq.gq_tensors_norm(t, p, norms=two)
+    torch.cuda.synchronize()
+    assert torch.equal(flat, before)
+    # between and behind the tensors
+    gq.gq_tensors_norm(t, flat[9002:9003], norms=flat[19_000:19_002])
+    want = [_norm64([before[4:9000]]), _norm64([before[9004:19_000]])]
+    for got, w, n in ((flat[9002], np.hypot(*want), 18_992), (flat[19_000], want[0], 8996),
+                      (flat[19_001], want[1], 9996)):
+        _near(got, w, n, "beside the tensors")
+    # in a tensor that is only read
+    y = torch.empty(18_992, device="cuda")
+    gq.gq_tensors_clip(t, flat[4:5], 2.0, eps=0.0,
+                       out=gq.gq_tensors_create([y[:8996], y[8996:]]))
+    f = _factor(5.0, 2.0, 0.0, 1.0)
+    assert _bits(y, _want(torch.cat([before[4:9000], before[9004:19_000]]), f, torch.float32))

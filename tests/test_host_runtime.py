@@ -117,3 +117,59 @@ def test_failed_pipe_keeps_its_error_text(lib):
         st, h = _pipe(lib)
         assert st == GQ_ERR_HIP and b"out of memory" in lib.gq_last_error(), (k, lib.gq_last_error())
     lib.host_fail_in(0)
+
+
+MiB = 1 << 20
+
+
+def test_norm_inside_a_list(lib):
+    """A norm or norms that lie in a tensor of the list would be read and
+    written, or written twice, by the call: refused, at every place of the tensors and with
+    the smallest overlap; the places between and beside them are accepted."""
+    # fp32 at 1 MiB, bf16 at 2 MiB (odd length), an empty one, fp32 at 3 MiB
+    at, numel, dt = [3 * MiB, MiB, 0, 2 * MiB], [5000, 100, 0, 9], [0, 0, 1, 2]
+    st, t = _list(lib, at, numel, dt)
+    assert st == GQ_OK
+    spans = [(MiB, MiB + 400), (2 * MiB, 2 * MiB + 18), (3 * MiB, 3 * MiB + 20_000)]
+    far = 64 * MiB
+    inside, outside = [], []
+    for b, e in spans:
+        inside += [b, b + 4, (e - 1) & ~3]
+        outside += [b - 4, (e + 3) & ~3]
+    for p in inside:
+        before = lib.host_launches()
+        for call in (lambda: lib.gq_tensors_norm(t, 1.0, p, None, None),
+                     lambda: lib.gq_tensors_norm(t, 1.0, far, p, None),
+                     lambda: lib.gq_tensors_norm(t, 1.0, far, p - 12, None),
+                     lambda: lib.gq_tensors_clip(t, p, 1.0, 0.0, 1.0, None, None),
+                     lambda: lib.gq_tensors_clip(t, p, 1.0, 0.0, 1.0, t, None)):
+            assert call() == GQ_ERR_INVALID, hex(p)
+            assert b"lies in a tensor" in lib.gq_last_error(), lib.gq_last_error()
+        assert lib.host_launches() == before
+    # norms around the whole of a tensor
+    assert lib.gq_tensors_norm(t, 1.0, far, 2 * MiB - 4, None) == GQ_ERR_INVALID
+    for p in outside:
+        assert lib.gq_tensors_norm(t, 1.0, p, None, None) == GQ_OK, hex(p)
+        assert lib.gq_tensors_clip(t, p, 1.0, 0.0, 1.0, None, None) == GQ_OK, hex(p)
+    for b, e in spans:
+        assert lib.gq_tensors_norm(t, 1.0, far, b - 16, None) == GQ_OK
+        assert lib.gq_tensors_norm(t, 1.0, far, (e + 3) & ~3, None) == GQ_OK
+    # one of the norms as the norm
+    for k in range(4):
+        assert lib.gq_tensors_norm(t, 1.0, far + 4 * k, far, None) == GQ_ERR_INVALID, k
+        assert b"norms" in lib.gq_last_error()
+    for p in (far - 4, far + 16):
+        assert lib.gq_tensors_norm(t, 1.0, p, far, None) == GQ_OK
+    # into another list: that one's tensors are written, the list's own are only read
+    st, out = _list(lib, [a and a + 8 * MiB for a in at], numel, dt)
+    assert st == GQ_OK
+    for p in inside:
+        assert lib.gq_tensors_clip(t, p, 1.0, 0.0, 1.0, out, None) == GQ_OK, hex(p)
+        assert lib.gq_tensors_clip(t, p + 8 * MiB, 1.0, 0.0, 1.0, out, None) == GQ_ERR_INVALID
+        assert b"lies in a tensor" in lib.gq_last_error()
+    # a list without elements has no place that could be taken
+    st, none = _list(lib, [0, 0], [0, 0])
+    assert st == GQ_OK and lib.gq_tensors_norm(none, 1.0, far, far + 4, None) == GQ_OK
+    assert lib.gq_tensors_clip(none, far, 1.0, 0.0, 1.0, None, None) == GQ_OK
+    for h in (t, out, none):
+        assert lib.gq_tensors_destroy(h) == GQ_OK
