@@ -414,3 +414,40 @@ def test_most_tokens(gq):
     i = torch.where((idx >= 0) & (idx != 5), idx, torch.full_like(idx, V)).long()
     want = torch.zeros(V + 1, dtype=torch.float64, device="cuda").index_add_(0, i, dy[:, 0].double())
     assert bool((grad[:, 0].double() == want[:V]).all())
+
+
+# gradients whose rows without a token are cleared by work groups of their own, among
+# those of the sums: four rows or more a token, of 1 KiB or more
+MANY_ROWS = [(2049, 8196, 256), (2100, 8403, 257), (2100, 8403, 513), (2500, 10_007, 1030),
+             (300, 8192, 14_003), (16_500, 66_007, 512)]
+
+
+@pytest.mark.parametrize("dt,out", [("f32", "f32"), ("bf16", "f32"), ("f16", "f16"),
+                                    ("bf16", "bf16")])
+def test_rows_cleared_beside_the_sums(gq, dt, out):
+    """Sums of small whole numbers, exact in any order, in a gradient of which
+    every element has to be written, and nothing else."""
+    rng = np.random.default_rng(9)
+    for k, (T, V, D) in enumerate(MANY_ROWS):
+        for j, kind in enumerate(("even", "skewed", "one", "outside", "first", "last")):
+            it = (torch.int32, torch.int64)[(k + j) % 2]
+            gap, shift, skip = (0, 1, 3)[(k + j) % 3], (k + j) % 4, (None, 0, V // 2)[j % 3]
+            say("cleared beside the sums", dt, out, T, V, D, kind, "skip", skip, "gap", gap)
+            if kind == "first":
+                idx = torch.arange(T, dtype=it, device="cuda")
+            elif kind == "last":
+                idx = torch.arange(V - T, V, dtype=it, device="cuda").flip(0)
+            else:
+                idx = _idx(rng, T, V, kind, it)
+            dy, _ = _wide(T, D, gap, dt, shift)
+            dy.copy_(torch.from_numpy(rng.integers(-4, 5, (T, D)).astype(np.float32)))
+            grad, flat = _wide(V, D, gap, out, shift)
+            _grad(gq, idx, dy, grad, skip=skip)
+            i = idx.long()
+            ok = (i >= 0) & (i < V) & (i != (-1 if skip is None else skip))
+            want = torch.zeros(V, D, dtype=torch.float64, device="cuda")
+            want.index_add_(0, i[ok], dy.double()[ok])
+            # (one rounding of a whole number below 2^24; zeros are +0)
+            assert _bits(grad, (want + 0.0).to(TORCH[out])), (T, V, D, kind)
+            _untouched(grad, flat)
+            del dy, grad, flat, want
