@@ -407,7 +407,6 @@ struct EgShape {
     static constexpr int SUB = 64 / LPR;                // rows of a wave at once
     static constexpr int GROUP = LPR == 64 ? 4 : 1;      // rows of LPR lanes, one after another
     static constexpr int FLY = 16;                      // tokens in flight
-    static constexpr int HOLD = LPR < 16 ? 16 / LPR : 1;  // tokens of the order a lane holds
     static __host__ __device__ int64_t slabs(int64_t cols) {
         return (cols + LPR * V - 1) / (LPR * V);
     }
@@ -425,7 +424,7 @@ __device__ __forceinline__ int32_t take(int32_t v, int from) {
 template <typename T, typename U, int V, int LPR>
 __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     using S = EgShape<V, LPR>;
-    constexpr int FLY = S::FLY, SUB = S::SUB, HOLD = S::HOLD, WINDOW = LPR * HOLD;
+    constexpr int FLY = S::FLY, SUB = S::SUB;
     const int lane = threadIdx.x & 63, l = lane % LPR, sub = lane / LPR;
     const int64_t slabs = S::slabs(a.cols);
     int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
@@ -455,27 +454,19 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed_sum(const EgSumArgs a) {
     const Cols c = cols_of<V>((slab * LPR + l) * V, a.cols);
     const T *dy = static_cast<const T *>(a.dy);
 
-    // the tokens of the order from `held` on, WINDOW or up to held_end, some a lane
-    int32_t held = 0, held_end = 0, have[HOLD] = {};
+    // the tokens of the order from `held` to held_end, LPR or fewer, one a lane
+    int32_t held = 0, held_end = 0, have = 0;
     auto hold = [&](int32_t at, int32_t end) __attribute__((always_inline)) {
         held = at;
-        held_end = end - at < WINDOW ? end : at + WINDOW;
-#pragma unroll
-        for (int h = 0; h < HOLD; ++h) {
-            have[h] = 0;
-            if (at + h * LPR + l < end) have[h] = a.order[at + h * LPR + l];
-        }
+        held_end = end - at < LPR ? end : at + LPR;
+        have = 0;
+        if (at + l < end) have = a.order[at + l];
     };
-    auto token = [&](int at) __attribute__((always_inline)) {
-        int32_t v = have[0];
-#pragma unroll
-        for (int h = 1; h < HOLD; ++h) v = at / LPR == h ? have[h] : v;
-        return take<LPR>(v, at % LPR);
-    };
+    auto token = [&](int at) __attribute__((always_inline)) { return take<LPR>(have, at % LPR); };
     // s += the tokens first .. end - 1 of the order
     auto sum = [&](int32_t first, int32_t end, float (&s)[V]) __attribute__((always_inline)) {
-        for (int32_t at = first; at < end; at += WINDOW) {
-            const int n = end - at < WINDOW ? end - at : WINDOW;
+        for (int32_t at = first; at < end; at += LPR) {
+            const int n = end - at < LPR ? end - at : LPR;
             if (at < held || at + n > held_end) hold(at, end);
             const int skip = at - held;
             for (int j = 0; j < n; j += FLY) {
