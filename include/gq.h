@@ -748,8 +748,10 @@ typedef struct gq_tensors gq_tensors;
  * The list keeps the addresses: the memory has to stay where it is, with any
  * contents, for as long as the list is used, as gradients in flat buffers do.
  * Tensors that have moved need a new list.
- * Allocates device memory (24 bytes per 4096 elements and 40 per tensor, and
- * 4 KiB) and synchronizes.  Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_HIP.
+ * Allocates device memory (24 bytes for each started 4096 elements of a tensor,
+ * 24 for each tensor that is empty or longer than 4096, and 4104 more), copies
+ * to it and synchronizes the device: made once, not in every step.
+ * Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_HIP.
  */
 gq_status gq_tensors_create(void *const *x, const int64_t *numel, const gq_dtype *dt,
                             int64_t count, gq_tensors **out);

@@ -173,3 +173,22 @@ def test_norm_inside_a_list(lib):
     assert lib.gq_tensors_clip(none, far, 1.0, 0.0, 1.0, None, None) == GQ_OK
     for h in (t, out, none):
         assert lib.gq_tensors_destroy(h) == GQ_OK
+
+
+def test_memory_of_a_list(lib):
+    """What a list allocates is what the header says."""
+    with open(os.path.join(ROOT, "include", "gq.h")) as f:
+        text = " ".join(f.read().replace("*", " ").split())
+    assert ("24 bytes for each started 4096 elements of a tensor, 24 for each tensor that is "
+            "empty or longer than 4096, and 4104 more") in text
+    for numel in ([1], [0], [4096], [4097], [8193], [0, 0, 5], [4097] * 300, [1, 70_000, 0, 4096]):
+        at = [MiB * (k + 1) for k in range(len(numel))]
+        st, h = _list(lib, at, numel)
+        n, count, size = (ctypes.c_int64() for _ in range(3))
+        assert st == GQ_OK
+        assert lib.gq_tensors_info(h, *(ctypes.byref(v) for v in (n, count, size))) == GQ_OK
+        tiles = sum(-(-m // 4096) for m in numel)
+        more = sum(m == 0 or m > 4096 for m in numel)
+        assert (n.value, count.value) == (sum(numel), len(numel))
+        assert size.value == 24 * tiles + 24 * more + 4104, numel
+        assert lib.gq_tensors_destroy(h) == GQ_OK
