@@ -1,5 +1,5 @@
 // gq_args.h -- argument checks of the C-ABI files (gq_mx4.cpp,
-// gq_ortho.cpp): each returns GQ_OK or sets the calling thread's error text.
+// gq_ortho.cpp, gq_tensors.cpp, gq_embed.cpp): each returns GQ_OK or sets the calling thread's error text.
 // Not part of the ABI.
 #pragma once
 

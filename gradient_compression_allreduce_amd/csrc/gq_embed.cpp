@@ -51,10 +51,19 @@ int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 
 // Whether one launch takes the gradient, in which the work group that has the most
 // frequent token's row sums that row alone: up to EG_SMALL tokens, and 2^21 elements of dy,
-// or 2^22 where the table is long and the tokens more evenly spread.  One launch / three,
-// bf16 added to fp32: 512 tokens of 8192 into 30522 rows 25 / 51 us, 2000 of 2048
-// 25 / 28, 1000 of 2048 into 200 20 / 23, 256 of 8192 into 100 24 / 19, 1697 of 2993 into
-// 173 58 / 27.
+// or 2^22 where the table is long and tokens are likely to be spread over more rows.  One
+// launch costs by the most frequent token's elements, which the host does not know, and
+// three by rows x columns of the table, so a bound on dy's elements is right for
+// neither; it bounds what one launch can lose.  One launch / three, bf16 into fp32, the
+// r-th most frequent token 1/r as often as the first:
+//   added, 30522 rows: 2048 tokens of 2048 25 / 28 us, of 2049 32 / 33, 1024 of 4096
+//   25 / 35, of 4100 38 / 38, 512 of 8192 25 / 51, and above the limit 512 of 8200 35 / 54,
+//   512 of 12288 44 / 71, 64 of 66000 51 / 304;
+//   the whole gradient: 512 of 8200 into 30522 228 / 214, 512 of 9000 into 16384 160 / 138,
+//   1024 of 2048 into 200 17 / 22, 256 of 8192 into 100 22 / 19, of 8200 27 / 19,
+//   2000 of 1100 into 173 29 / 23;
+//   added, 2000 of 2048 into 30522 with 25, 50 and 100% of one token: 67 / 27, 126 / 27 and
+//   244 / 23, 512 of 12288 124 / 71, 248 / 70 and 481 / 66.
 bool is_small(int64_t tokens, int64_t rows, int64_t cols) {
     return tokens <= EG_SMALL && tokens * cols <= (rows >= 8192 ? 1 << 22 : 1 << 21);
 }
@@ -151,7 +160,8 @@ gq_status gq_embed_grad(const void *idx, int32_t idx_bytes, int64_t tokens, cons
     // long, beside the sums, by more waves (with as many reads as writes the two together
     // are slower).  fp32, by the sort / beside the sums: 4000 tokens into 262144
     // rows of 900 columns 257 / 202 us, 30000 of 300 123 / 112, 16384 into 30522 of
-    // 1024 53 / 54, 131072 into 100003 of 2048 299 / 327.
+    // 1024 53 / 54, 131072 into 100003 of 2048 299 / 327.  (Eight rows are one wave's: of
+    // few and very long rows the waves are few, and 3 tokens of 2^20 into 100 take 1230 us.)
     const bool apart = !add && rows / 4 >= tokens &&
                        cols * static_cast<int64_t>(elem_bytes(out_dt)) >= 1024;
     sa.grad = add || apart ? nullptr : static_cast<char *>(grad);

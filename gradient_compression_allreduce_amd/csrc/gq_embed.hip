@@ -117,10 +117,14 @@ __global__ __launch_bounds__(EM_BLOCK) void k_embed(const EmArgs a) {
 // as where one token makes up much of a batch, looks through its tokens again
 // instead.)  More than 16384 tokens are first turned into row numbers of 32 bits
 // (k_embed_keys), which take the fewest instructions to look through.
-// Bound by instructions: T tokens are looked at by 256 work groups, 30 us for
-// 131072 (with the tokens' places found in a second look 49), 10 for 16384; 7 to 15%
-// of a gradient of 1024 columns.  Clearing the rows without a token comes on
-// top at 5.5 to 6 TB/s.
+// Bound by instructions: up to 262144 rows T tokens are looked at by 256 work groups at
+// most, 30 us for 131072 (with the tokens' places found in a second look 49), 10 for 16384;
+// 7 to 15% of a gradient of 1024 columns.  Beyond, every 1024 rows are one more work group
+// (of 132 KiB LDS, so a compute unit holds one) that looks at all of them, about
+// 4 x 10^12 looks a second: a gradient of 8 columns, added, of 131072 tokens into 2^18, 2^20
+// and 2^22 rows takes 50, 127 and 365 us, of 2^20 tokens 127, 370 and 1300; of one column,
+// 2^22 tokens into 2^22 rows 4.2 ms.  Clearing the rows without a token comes on top at
+// 5.5 to 6 TB/s.
 
 // The row of token i, or ~0 where it counts for none.
 __device__ __forceinline__ uint32_t row_of(const void *idx, bool wide, int64_t rows, int64_t skip,
@@ -396,7 +400,7 @@ __device__ __forceinline__ void finish(const Args &a, int64_t row, const Cols &c
                                        const Raw<U, V> &old) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        // (0 is added so that no sum of nothing becomes -0)
+        // (0 is added so that a sum of zeros times a negative mul is 0 and not -0)
         s[k] = s[k] * a.mul + (a.add ? elem<U, V>(old, k) : 0.0f);
     }
     store_cols<U, V>(static_cast<U *>(a.grad) + row * a.ldg, c, s);

@@ -811,7 +811,8 @@ gq_status gq_tensors_clip(const gq_tensors *t, const float *norm, float max_norm
 
 /*
  * gq_embed -- out[t] = mul * table[idx[t]]: one product rounded to binary32,
- * then to out's type (mul = 1 and one type: the row as it is).
+ * then to out's type (mul = 1 and one type: the row as it is, but for signalling
+ * NaNs, which become quiet).
  * table: rows x cols of dt, row stride ld; out: tokens x cols of out_dt, ldo.
  * mul: finite.  Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_HIP.
  */
@@ -838,7 +839,13 @@ gq_status gq_embed_grad_workspace(int64_t tokens, int64_t rows, int64_t cols, in
  *             gives, 16-byte aligned, contents of no matter; calls that share
  *             it must be ordered, captured ones included.
  * The order of each sum depends on idx and the sizes alone: equal calls give
- * equal bits.  Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_CAPACITY, GQ_ERR_HIP.
+ * equal bits.
+ * Time beyond what is read and written: from 2^18 rows on the tokens are looked
+ * at once for every 1024 rows, which takes about tokens * rows / 4e15 seconds on an
+ * MI355X (0.3 ms for 2^20 tokens into 2^20 rows, 4 ms for 2^22 into 2^22, minutes for
+ * 2^30 into 2^30).  Of up to 2048 tokens, those of one row are summed by one work
+ * group: 0.24 ms where 2000 tokens of 2048 columns all have the same index.
+ * Errors: GQ_ERR_INVALID, GQ_ERR_ALIGN, GQ_ERR_CAPACITY, GQ_ERR_HIP.
  */
 gq_status gq_embed_grad(const void *idx, int32_t idx_bytes, int64_t tokens, const void *dy,
                         gq_dtype dt, int64_t ldy, float mul, int64_t skip, int64_t rows,
